@@ -364,6 +364,157 @@ mpm_status mpm_moe_combine(const void* y_perm_dev, const int32_t* inv_perm_dev,
                            cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Residual RMSNorm                                                         */
+/* ------------------------------------------------------------------------ */
+
+#define MPM_DTYPE_BF16 0
+#define MPM_DTYPE_F32 1
+
+/*
+ * Residual addition and root-mean-square norm of the rows of x_dev (bf16
+ * [M, K], leading dimension ldx elements):
+ *   h = x + residual                     (fp32; residual_dev nullable: h = x)
+ *   rstd = 1 / sqrt(mean_K(h^2) + eps)   (fp32, of the unrounded h)
+ *   y = h * rstd * weight
+ * Outputs, each nullable: h_dev and y_dev bf16 [M, K], rounded once; rstd_dev
+ * fp32 [M]; row_q_dev / row_s_dev the row-wise MXFP8 copy of the bf16 y, the
+ * bytes mpm_mxfp8_quantize gives (codes [M, K], scales [M, K/32] in 128x4
+ * tiles with zeroed padding), whether or not y_dev is asked for.
+ * weight_dev: [K], MPM_DTYPE_BF16 or MPM_DTYPE_F32.  This norm is what the
+ * expert layer's input comes from; the pages take it as given, so it is an
+ * interface of this library.
+ * An output may be one of the inputs in place (same pointer and leading
+ * dimension); outputs must not overlap otherwise.  A row whose square sum
+ * exceeds fp32's range gets rstd 0; NaN and infinities spread over their own
+ * row only.
+ * Requirements: M >= 1, 1 <= K <= 16384, every leading dimension >= K, eps
+ * finite and > 0, at least one of y_dev and row_q_dev, row_q_dev and row_s_dev
+ * both or neither; bf16 pointers 2-byte and fp32 pointers 4-byte aligned (any
+ * K and pitch; 16-byte aligned rows of a multiple of 8 elements are fastest).
+ * With row_q_dev: K % 32 == 0, row_q_dev 16-byte aligned.
+ */
+mpm_status mpm_add_rmsnorm(const void* x_dev, int64_t M, int64_t K, int64_t ldx,
+                           const void* residual_dev, int64_t ldr,
+                           const void* weight_dev, int weight_dtype, float eps,
+                           void* h_dev, int64_t ldh, void* y_dev, int64_t ldy,
+                           float* rstd_dev, uint8_t* row_q_dev, uint8_t* row_s_dev,
+                           cudaStream_t stream);
+
+/*
+ * Gradient of mpm_add_rmsnorm.  With dy = dy + dy2, xh = h * rstd, g = dy * weight:
+ *   dx = rstd * (g - xh * mean_K(g * xh)) + dh      (bf16, rounded once)
+ *   dw = sum over rows of dy * xh                   (fp32)
+ * dx is the gradient of h, so of x and of the residual alike.  dy_dev and the
+ * nullable dy2_dev (a second reader of y: its gradients need no sum of their
+ * own) are bf16 [M, K]; h_dev bf16 [M, K] and rstd_dev fp32 [M] as the forward
+ * wrote them (h_dev = x without a residual); dh_dev (nullable) bf16 [M, K] is
+ * the gradient that reaches h along the residual stream.  dw_dev (nullable)
+ * fp32 [K] is overwritten; its sum runs in a fixed order through ws_dev, at
+ * least mpm_add_rmsnorm_backward_workspace_bytes(M, K) bytes, 4-byte aligned,
+ * uninitialised (NULL without dw_dev).
+ * Requirements as for mpm_add_rmsnorm; dx_dev may be dy_dev, dy2_dev, dh_dev
+ * or h_dev in place.
+ */
+size_t mpm_add_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K);
+mpm_status mpm_add_rmsnorm_backward(const void* dy_dev, int64_t lddy,
+                                    const void* dy2_dev, int64_t lddy2,
+                                    const void* h_dev, int64_t ldh, const float* rstd_dev,
+                                    const void* weight_dev, int weight_dtype,
+                                    const void* dh_dev, int64_t lddh, int64_t M, int64_t K,
+                                    void* dx_dev, int64_t lddx, float* dw_dev,
+                                    void* ws_dev, size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Router                                                                   */
+/* ------------------------------------------------------------------------ */
+
+#define MPM_SCORE_SOFTMAX 0
+#define MPM_SCORE_SIGMOID 1
+
+/*
+ * Top-k choice, routing weights, expert counts and balance loss of logits_dev
+ * ([T, E], MPM_DTYPE_BF16 or MPM_DTYPE_F32, leading dimension ld elements).
+ * Scores (fp32): softmax over the E experts, or sigmoid.  The k experts of a
+ * token are those with the largest logit (softmax) or score + bias (sigmoid;
+ * bias_dev, nullable, fp32 [E], sways the choice only), in descending order,
+ * ties to the lower expert.  prob = the chosen scores, divided by their sum if
+ * `normalize` (a sum of 0 gives 0), times `scale`.
+ * An expert is out of reach of a token where its logit or bias is NaN or at
+ * most bf16's lowest finite value (so -inf and either type's lowest value):
+ * its score is 0 and it is chosen, lowest expert first and with weight 0, only
+ * where fewer than k are left.  +inf reads as the largest finite value.
+ * token_mask_dev (nullable): u8 [T]; a token with 0 is routed like any other,
+ * but its weights are 0 and it is not counted.  Over the n unmasked tokens:
+ *   counts[e] = times e was chosen within reach       (int32 [E])
+ *   load[e]   = mean of the token's scores as shares of one (fp32 [E]; sigmoid
+ *               scores are divided by their sum over the experts)
+ *   loss      = E / (k n) * sum_e counts[e] * load[e] (fp32 [1]; 1 at perfect
+ *               balance; 0 when n = 0);  n_tokens = n  (int32 [1])
+ * ids_dev int32 [T, k] and prob_dev fp32 [T, k] are the inputs of
+ * mpm_moe_build_segments.  The workload routings of the pages are softmax,
+ * top-k with ties to the lower expert and renormalised weights.
+ * ws_dev: at least mpm_moe_route_workspace_bytes(T, E) bytes, 4-byte aligned,
+ * uninitialised.  Requirements: T >= 1, 1 <= E <= 1024, 1 <= k <= min(E, 64),
+ * T * k <= 2^30, ld >= E, scale finite, bias_dev only with sigmoid scores;
+ * pointers aligned to their element.
+ */
+size_t mpm_moe_route_workspace_bytes(int64_t T, int64_t E);
+mpm_status mpm_moe_route(const void* logits_dev, int logits_dtype, int64_t T, int64_t E, int64_t ld,
+                         int k, int score, int normalize, float scale, const float* bias_dev,
+                         const uint8_t* token_mask_dev, int32_t* ids_dev, float* prob_dev,
+                         int32_t* counts_dev, float* load_dev, int32_t* n_tokens_dev,
+                         float* loss_dev, void* ws_dev, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Gradient of mpm_moe_route with respect to the logits (same arguments), from
+ * dprob_dev (nullable, fp32 [T, k]: the gradient of prob) and dloss_dev
+ * (nullable, fp32 [1]: the gradient of loss), given the forward's ids, counts
+ * and n_tokens.  The choice and the counts are constants; the loss passes its
+ * gradient through load.  dlogits_dev has the logits' type, leading dimension
+ * ldd; it is 0 for experts out of reach and masked tokens.  The ids of a token
+ * are distinct; an id outside [0, E) sets MPM_ERR_DEVICE_BOUNDS and is skipped.
+ * dlogits_dev may be logits_dev in place.  Requirements as for mpm_moe_route,
+ * ldd >= E; counts_dev and n_tokens_dev may be NULL without dloss_dev, ids_dev
+ * without dprob_dev.
+ */
+mpm_status mpm_moe_route_backward(const void* logits_dev, int logits_dtype, int64_t T, int64_t E,
+                                  int64_t ld, int k, int score, int normalize, float scale,
+                                  const float* bias_dev, const uint8_t* token_mask_dev,
+                                  const int32_t* ids_dev, const int32_t* counts_dev,
+                                  const int32_t* n_tokens_dev, const float* dprob_dev,
+                                  const float* dloss_dev, void* dlogits_dev, int64_t ldd,
+                                  cudaStream_t stream);
+
+/*
+ * Gradient of the routing weights: dprob[t, j] = <dout[t], y_perm[inv_perm[t*k+j]]>
+ * / prob[t, j] (fp32 sums), the weight being applied in the FC1 epilogue so
+ * that y_perm is linear in it.  0 where inv_perm is negative or prob is 0; a
+ * row index >= capacity sets MPM_ERR_DEVICE_BOUNDS and gives 0.  dout bf16
+ * [T, H] and y_perm bf16 [capacity, H] dense, prob and dprob fp32 [T, k].
+ * Requirements: T, k, capacity >= 1, T * k <= 2^30, H >= 8, H % 8 == 0,
+ * dout_dev and y_perm_dev 16-byte aligned.
+ */
+mpm_status mpm_moe_combine_dprob(const void* dout_dev, const void* y_perm_dev,
+                                 const int32_t* inv_perm_dev, const float* prob_dev, int64_t T,
+                                 int k, int64_t H, int64_t capacity, float* dprob_dev,
+                                 cudaStream_t stream);
+
+/*
+ * Row-wise MXFP8 rows of T tokens (codes u8 [T, K], scales [T, K/32] in 128x4
+ * tiles: what mpm_add_rmsnorm and mpm_mxfp8_quantize write) into the permuted
+ * layout: the row-wise bytes mpm_mxfp8_quantize_gather gives for the bf16 rows
+ * they were quantised from.  Row r < seg_offsets[E] is token perm[r] / k, zero
+ * codes and scales where perm[r] < 0; rows at or beyond it are not written.  A
+ * token >= T sets MPM_ERR_DEVICE_BOUNDS and that row is zero.
+ * Requirements: T, E, capacity >= 1, 1 <= k <= 64, K >= 32, K % 32 == 0, T and
+ * capacity < 2^31 - 256; code pointers 16-byte, scale pointers 4-byte aligned.
+ */
+mpm_status mpm_moe_gather_mxfp8(const uint8_t* src_q_dev, const uint8_t* src_s_dev, int64_t T,
+                                int64_t K, int k, const int32_t* perm_dev,
+                                const int32_t* seg_offsets_dev, int64_t E, int64_t capacity,
+                                uint8_t* dst_q_dev, uint8_t* dst_s_dev, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Dequantisation and transpose: operands of the BF16 backward              */
 /* ------------------------------------------------------------------------ */
 

@@ -23,8 +23,11 @@ GROUP_M, GROUP_K = 0, 1
 TILE_SMALL_M = 1
 EPI_F32, EPI_BF16, EPI_SWIGLU, EPI_SWIGLU_SAVE, EPI_DSWIGLU, EPI_BF16_ONLINE = 0, 1, 2, 3, 4, 5
 GATHER_BF16, GATHER_NVFP4 = 0, 1
+DTYPE_BF16, DTYPE_F32 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 _vp, _i64, _u32, _int, _sz = C.c_void_p, C.c_int64, C.c_uint, C.c_int, C.c_size_t
+_f32 = C.c_float
 
 
 class GroupedGemmDesc(C.Structure):
@@ -72,6 +75,18 @@ _SIGS = {
     "mpm_nvfp4_quantize_scatter_workspace_bytes": (C.c_size_t, [_i64, _i64]),
     "mpm_nvfp4_quantize_scatter": (_int, [_vp, _i64, _i64, _i64, _vp, _int, _vp, _vp, _i64,
                                           _i64, _vp, _vp, _vp, _vp, _vp, C.c_size_t, _vp]),
+    "mpm_add_rmsnorm": (_int, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _int, _f32, _vp, _i64, _vp,
+                               _i64, _vp, _vp, _vp, _vp]),
+    "mpm_add_rmsnorm_backward_workspace_bytes": (_sz, [_i64, _i64]),
+    "mpm_add_rmsnorm_backward": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _int, _vp, _i64,
+                                        _i64, _i64, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "mpm_moe_route_workspace_bytes": (_sz, [_i64, _i64]),
+    "mpm_moe_route": (_int, [_vp, _int, _i64, _i64, _i64, _int, _int, _int, _f32, _vp, _vp, _vp, _vp,
+                             _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "mpm_moe_route_backward": (_int, [_vp, _int, _i64, _i64, _i64, _int, _int, _int, _f32, _vp, _vp,
+                                      _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "mpm_moe_combine_dprob": (_int, [_vp, _vp, _vp, _vp, _i64, _int, _i64, _i64, _vp, _vp]),
+    "mpm_moe_gather_mxfp8": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _vp, _i64, _i64, _vp, _vp, _vp]),
     "mpm_nvfp4_dequantize": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp]),
     "mpm_mxfp8_dequantize": (_int, [_vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp]),
     "mpm_transpose_bf16": (_int, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp]),

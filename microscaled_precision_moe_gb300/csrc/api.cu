@@ -2,6 +2,7 @@
 // Nothing here allocates device memory; every entry point validates its
 // arguments before launching anything and returns an mpm_status.
 #include <cuda.h>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -10,6 +11,8 @@
 #include "moe.cuh"
 #include "gemm.cuh"
 #include "dequant.cuh"
+#include "norm.cuh"
+#include "router.cuh"
 
 namespace {
 
@@ -357,6 +360,156 @@ mpm_status mpm_moe_combine(const void* y, const int32_t* inv, int64_t T, int k, 
   if (T < 1 || k < 1 || H < 8 || H % 8 != 0) return MPM_ERR_SHAPE;
   if (!aligned(y, 16) || !aligned(out, 16)) return MPM_ERR_ALIGN;
   return cuda_status(mpm::launch_combine(y, inv, T, k, H, out, stream));
+}
+
+mpm_status mpm_add_rmsnorm(const void* x, int64_t M, int64_t K, int64_t ldx, const void* residual,
+                           int64_t ldr, const void* weight, int weight_dtype, float eps, void* h,
+                           int64_t ldh, void* y, int64_t ldy, float* rstd, uint8_t* row_q,
+                           uint8_t* row_s, cudaStream_t stream) {
+  if (!x || !weight || (!y && !row_q) || (!row_q != !row_s)) return MPM_ERR_NULL;
+  if (weight_dtype != MPM_DTYPE_BF16 && weight_dtype != MPM_DTYPE_F32) return MPM_ERR_UNSUPPORTED;
+  if (M < 1 || M > (1ll << 31) - 256 || K < 1 || K > 16384) return MPM_ERR_SHAPE;
+  if (ldx < K || (residual && ldr < K) || (h && ldh < K) || (y && ldy < K)) return MPM_ERR_SHAPE;
+  if (row_q && K % 32 != 0) return MPM_ERR_SHAPE;
+  if (!std::isfinite(eps) || !(eps > 0.0f)) return MPM_ERR_SHAPE;
+  if (!aligned(x, 2) || !aligned(residual, 2) || !aligned(h, 2) || !aligned(y, 2) ||
+      !aligned(weight, weight_dtype == MPM_DTYPE_F32 ? 4 : 2) || !aligned(rstd, 4) ||
+      !aligned(row_q, 16))
+    return MPM_ERR_ALIGN;
+  mpm::NormFwd p{};
+  p.x = static_cast<const uint16_t*>(x); p.ldx = ldx;
+  p.r = static_cast<const uint16_t*>(residual); p.ldr = ldr;
+  p.w = weight; p.w_f32 = weight_dtype == MPM_DTYPE_F32;
+  p.eps = eps;
+  p.h = static_cast<uint16_t*>(h); p.ldh = ldh;
+  p.y = static_cast<uint16_t*>(y); p.ldy = ldy;
+  p.rstd = rstd; p.q = row_q; p.s = row_s; p.s_cols_pad = pad_to(K / 32, 4);
+  p.M = M; p.K = (int)K;
+  return cuda_status(mpm::launch_add_rmsnorm(p, stream));
+}
+
+size_t mpm_add_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K) {
+  if (M < 1 || K < 1 || K > 16384) return 0;
+  return (size_t)mpm::rmsnorm_backward_parts(M, (int)K) * (size_t)K * sizeof(float);
+}
+
+mpm_status mpm_add_rmsnorm_backward(const void* dy, int64_t lddy, const void* dy2, int64_t lddy2,
+                                    const void* h, int64_t ldh, const float* rstd,
+                                    const void* weight, int weight_dtype, const void* dh,
+                                    int64_t lddh, int64_t M, int64_t K, void* dx, int64_t lddx,
+                                    float* dw, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!dy || !h || !rstd || !weight || !dx || (dw && !ws)) return MPM_ERR_NULL;
+  if (weight_dtype != MPM_DTYPE_BF16 && weight_dtype != MPM_DTYPE_F32) return MPM_ERR_UNSUPPORTED;
+  if (M < 1 || M > (1ll << 31) - 256 || K < 1 || K > 16384) return MPM_ERR_SHAPE;
+  if (lddy < K || (dy2 && lddy2 < K) || ldh < K || (dh && lddh < K) || lddx < K) return MPM_ERR_SHAPE;
+  if (dw && ws_bytes < mpm_add_rmsnorm_backward_workspace_bytes(M, K)) return MPM_ERR_SHAPE;
+  if (!aligned(dy, 2) || !aligned(dy2, 2) || !aligned(h, 2) || !aligned(dh, 2) || !aligned(dx, 2) ||
+      !aligned(weight, weight_dtype == MPM_DTYPE_F32 ? 4 : 2) || !aligned(rstd, 4) ||
+      !aligned(dw, 4) || !aligned(ws, 4))
+    return MPM_ERR_ALIGN;
+  mpm::NormBwd p{};
+  p.dy = static_cast<const uint16_t*>(dy); p.lddy = lddy;
+  p.dy2 = static_cast<const uint16_t*>(dy2); p.lddy2 = lddy2;
+  p.h = static_cast<const uint16_t*>(h); p.ldh = ldh;
+  p.w = weight; p.w_f32 = weight_dtype == MPM_DTYPE_F32;
+  p.rstd = rstd;
+  p.dh = static_cast<const uint16_t*>(dh); p.lddh = lddh;
+  p.dx = static_cast<uint16_t*>(dx); p.lddx = lddx;
+  p.dw = dw; p.part = static_cast<float*>(ws);
+  p.M = M; p.K = (int)K;
+  return cuda_status(mpm::launch_add_rmsnorm_backward(p, stream));
+}
+
+size_t mpm_moe_route_workspace_bytes(int64_t T, int64_t E) {
+  if (T < 1 || E < 1 || E > 1024) return 0;
+  return mpm::route_ws_bytes(T, (int)E);
+}
+
+}  // extern "C"
+
+// the checks mpm_moe_route and its backward share, and their common arguments
+static mpm_status route_args(mpm::RouteArgs& a, const void* logits, int dtype, int64_t T, int64_t E,
+                             int64_t ld, int k, int score, int normalize, float scale,
+                             const float* bias, const uint8_t* mask) {
+  if (!logits) return MPM_ERR_NULL;
+  if (dtype != MPM_DTYPE_BF16 && dtype != MPM_DTYPE_F32) return MPM_ERR_UNSUPPORTED;
+  if (score != MPM_SCORE_SOFTMAX && score != MPM_SCORE_SIGMOID) return MPM_ERR_UNSUPPORTED;
+  if (bias && score != MPM_SCORE_SIGMOID) return MPM_ERR_UNSUPPORTED;
+  if (T < 1 || E < 1 || E > 1024 || k < 1 || k > 64 || k > E || ld < E) return MPM_ERR_SHAPE;
+  if (T > (1ll << 30) / k || !std::isfinite(scale)) return MPM_ERR_SHAPE;
+  if (!aligned(logits, dtype == MPM_DTYPE_F32 ? 4 : 2) || !aligned(bias, 4)) return MPM_ERR_ALIGN;
+  a.logits = logits; a.bf16 = dtype == MPM_DTYPE_BF16;
+  a.T = T; a.E = (int)E; a.ld = ld; a.k = k;
+  a.sigmoid = score == MPM_SCORE_SIGMOID; a.normalize = normalize ? 1 : 0; a.scale = scale;
+  a.bias = bias; a.mask = mask;
+  a.status = status_ptr();
+  return MPM_OK;
+}
+
+extern "C" {
+
+mpm_status mpm_moe_route(const void* logits, int logits_dtype, int64_t T, int64_t E, int64_t ld,
+                         int k, int score, int normalize, float scale, const float* bias,
+                         const uint8_t* mask, int32_t* ids, float* prob, int32_t* counts,
+                         float* load, int32_t* n_tokens, float* loss, void* ws, size_t ws_bytes,
+                         cudaStream_t stream) {
+  if (!ids || !prob || !counts || !load || !n_tokens || !loss || !ws) return MPM_ERR_NULL;
+  mpm::RouteArgs a{};
+  const mpm_status st = route_args(a, logits, logits_dtype, T, E, ld, k, score, normalize, scale,
+                                   bias, mask);
+  if (st != MPM_OK) return st;
+  if (ws_bytes < mpm::route_ws_bytes(T, (int)E)) return MPM_ERR_SHAPE;
+  if (!aligned(ids, 4) || !aligned(prob, 4) || !aligned(counts, 4) || !aligned(load, 4) ||
+      !aligned(n_tokens, 4) || !aligned(loss, 4) || !aligned(ws, 4))
+    return MPM_ERR_ALIGN;
+  a.ids = ids; a.prob = prob; a.counts = counts; a.load = load; a.n_tokens = n_tokens; a.loss = loss;
+  return cuda_status(mpm::launch_route(a, ws, stream));
+}
+
+mpm_status mpm_moe_route_backward(const void* logits, int logits_dtype, int64_t T, int64_t E,
+                                  int64_t ld, int k, int score, int normalize, float scale,
+                                  const float* bias, const uint8_t* mask, const int32_t* ids,
+                                  const int32_t* counts, const int32_t* n_tokens,
+                                  const float* dprob, const float* dloss, void* dlogits,
+                                  int64_t ldd, cudaStream_t stream) {
+  if (!dlogits || (dprob && !ids) || (dloss && (!counts || !n_tokens))) return MPM_ERR_NULL;
+  mpm::RouteArgs a{};
+  const mpm_status st = route_args(a, logits, logits_dtype, T, E, ld, k, score, normalize, scale,
+                                   bias, mask);
+  if (st != MPM_OK) return st;
+  if (ldd < E) return MPM_ERR_SHAPE;
+  if (!aligned(dlogits, logits_dtype == MPM_DTYPE_F32 ? 4 : 2) || !aligned(ids, 4) ||
+      !aligned(counts, 4) || !aligned(n_tokens, 4) || !aligned(dprob, 4) || !aligned(dloss, 4))
+    return MPM_ERR_ALIGN;
+  a.in_ids = ids; a.in_counts = counts; a.in_n = n_tokens;
+  a.dprob = dprob; a.dloss = dloss;
+  a.dlogits = dlogits; a.ldd = ldd;
+  return cuda_status(mpm::launch_route_backward(a, stream));
+}
+
+mpm_status mpm_moe_combine_dprob(const void* dout, const void* y, const int32_t* inv,
+                                 const float* prob, int64_t T, int k, int64_t H, int64_t cap,
+                                 float* dprob, cudaStream_t stream) {
+  if (!dout || !y || !inv || !prob || !dprob) return MPM_ERR_NULL;
+  if (T < 1 || k < 1 || T > (1ll << 30) / k || H < 8 || H % 8 != 0 || cap < 1) return MPM_ERR_SHAPE;
+  if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(inv, 4) || !aligned(prob, 4) ||
+      !aligned(dprob, 4))
+    return MPM_ERR_ALIGN;
+  return cuda_status(mpm::launch_combine_dprob(dout, y, inv, prob, T, k, H, cap, dprob, status_ptr(),
+                                               stream));
+}
+
+mpm_status mpm_moe_gather_mxfp8(const uint8_t* q, const uint8_t* s, int64_t T, int64_t K, int k,
+                                const int32_t* perm, const int32_t* seg, int64_t E, int64_t cap,
+                                uint8_t* dst_q, uint8_t* dst_s, cudaStream_t stream) {
+  if (!q || !s || !perm || !seg || !dst_q || !dst_s) return MPM_ERR_NULL;
+  if (T < 1 || K < 32 || K % 32 != 0 || k < 1 || k > 64 || E < 1 || cap < 1) return MPM_ERR_SHAPE;
+  if (T > (1ll << 31) - 256 || cap > (1ll << 31) - 256 || K > (1ll << 31) - 256) return MPM_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(dst_q, 16) || !aligned(s, 4) || !aligned(dst_s, 4) ||
+      !aligned(perm, 4) || !aligned(seg, 4))
+    return MPM_ERR_ALIGN;
+  return cuda_status(mpm::launch_gather_mxfp8(q, s, T, K, k, perm, seg + E, cap, dst_q, dst_s,
+                                              status_ptr(), stream));
 }
 
 mpm_status mpm_nvfp4_dequantize(const uint8_t* q, const uint8_t* s, const float* outer,

@@ -389,6 +389,54 @@ __global__ void __launch_bounds__(256) gather_nvfp4_kernel(const uint4* __restri
   }
 }
 
+// MXFP8 rows: codes (K bytes) and 128x4-tiled E8M0 scales (K/32 columns) move
+// together.  One CTA per 128 destination rows (one row of scale tiles), as
+// gather_nvfp4_kernel.
+__global__ void __launch_bounds__(256) gather_mxfp8_kernel(const uint4* __restrict__ src_q,
+                                                          const uint8_t* __restrict__ src_s,
+                                                          long long T, long long K, int k,
+                                                          const int* __restrict__ perm,
+                                                          const int* __restrict__ seg_end,
+                                                          long long cap, uint4* __restrict__ dst_q,
+                                                          uint8_t* __restrict__ dst_s, int* st) {
+  __shared__ long long tok[128];                  // source token of each row, -1 for padding
+  const long long rbase = (long long)blockIdx.x * 128;
+  long long rend = *seg_end;
+  if (rend > cap) rend = cap;
+  if (rbase >= rend) return;
+  const int nrows = (int)min(128LL, rend - rbase);
+  if (threadIdx.x < 128) {
+    long long t = -1;
+    if ((int)threadIdx.x < nrows) {
+      const int f = perm[rbase + threadIdx.x];
+      if (f >= 0) t = f / k;
+      if (t >= T) { set_status(st, MPM_ERR_DEVICE_BOUNDS); t = -1; }
+    }
+    tok[threadIdx.x] = t;
+  }
+  __syncthreads();
+  const long long q16 = K / 16;                  // uint4 chunks of codes per row
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = warp; i < nrows; i += 8) {
+    uint4* d = dst_q + (rbase + i) * q16;
+    const long long t = tok[i];
+    for (long long c = lane; c < q16; c += 32)
+      d[c] = t < 0 ? make_uint4(0, 0, 0, 0) : __ldg(src_q + t * q16 + c);
+  }
+  // scale tiles: word w of a tile holds row (w % 4) * 32 + w / 4
+  const long long cpad = (K / 32 + 3) / 4 * 4, ntiles = cpad / 4;
+  const long long rt = rbase >> 7;
+  const int w = threadIdx.x & 127;
+  const int r = (w & 3) * 32 + (w >> 2);
+  if (r >= nrows) return;
+  const long long t = tok[r];
+  for (long long g = threadIdx.x >> 7; g < ntiles; g += 2) {
+    uint32_t v = 0;
+    if (t >= 0) v = *reinterpret_cast<const uint32_t*>(src_s + sf_offset(t, g * 4, cpad));
+    reinterpret_cast<uint32_t*>(dst_s + (rt * ntiles + g) * 512)[w] = v;
+  }
+}
+
 // ---------------------------------------------------------------- combine
 // out[t] = sum_j y[inv[t*k + j]] in fp32, slot order, one rounding to bf16
 __global__ void __launch_bounds__(128) combine_kernel(const uint4* y, const int* inv, long long T,
@@ -417,6 +465,43 @@ __global__ void __launch_bounds__(128) combine_kernel(const uint4* y, const int*
     o[i] = *reinterpret_cast<uint32_t*>(&b);
   }
   out[t * H8 + c] = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// ---------------------------------------------------------------- gradient of the routing weights
+// out[t] = sum_j y[inv[t k + j]] and y of a slot is linear in its weight p (the
+// FC1 epilogue multiplies D by p), so d out[t] / d p_j = y / p_j and
+//   dprob[t, j] = <dout[t], y[inv[t k + j]]> / p_j.
+// A slot without a row (inv < 0) and a weight of 0 get 0: a weight of 0 comes
+// from a score of 0 (or a masked token), whose own gradient is 0.
+__global__ void __launch_bounds__(256) combine_dprob_kernel(const uint4* dout, const uint4* y,
+                                                           const int* inv, const float* prob,
+                                                           long long slots, int k, long long H8,
+                                                           long long cap, float* dprob, int* st) {
+  const long long f = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (f >= slots) return;
+  const int r = inv[f];
+  const float p = prob[f];
+  float acc = 0.0f;
+  if (r >= cap) {
+    if (lane == 0) set_status(st, MPM_ERR_DEVICE_BOUNDS);
+  } else if (r >= 0 && p != 0.0f) {
+    const uint4* a = dout + f / k * H8;
+    const uint4* b = y + (long long)r * H8;
+    for (long long c = lane; c < H8; c += 32) {
+      const uint4 u = __ldg(a + c), v = __ldg(b + c);
+      const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc = __fmaf_rn(bf16lo(uw[i]), bf16lo(vw[i]), acc);
+        acc = __fmaf_rn(bf16hi(uw[i]), bf16hi(vw[i]), acc);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc = __fadd_rn(acc, __shfl_xor_sync(0xffffffffu, acc, o));
+    acc = __fdiv_rn(acc, p);
+  }
+  if (lane == 0) dprob[f] = acc;
 }
 
 // ---------------------------------------------------------------- launchers
@@ -516,6 +601,25 @@ cudaError_t launch_combine(const void* y, const int* inv, long long T, int k, lo
   const dim3 grid((unsigned)T, (unsigned)((H8 + 127) / 128));
   combine_kernel<<<grid, 128, 0, s>>>(static_cast<const uint4*>(y), inv, T, k, H8,
                                       static_cast<uint4*>(out));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gather_mxfp8(const uint8_t* q, const uint8_t* sc, long long T, long long K, int k,
+                                const int* perm, const int* seg_end, long long cap, uint8_t* dst_q,
+                                uint8_t* dst_s, int* status, cudaStream_t s) {
+  gather_mxfp8_kernel<<<(unsigned)((cap + 127) / 128), 256, 0, s>>>(
+      reinterpret_cast<const uint4*>(q), sc, T, K, k, perm, seg_end, cap,
+      reinterpret_cast<uint4*>(dst_q), dst_s, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_combine_dprob(const void* dout, const void* y, const int* inv, const float* prob,
+                                 long long T, int k, long long H, long long cap, float* dprob,
+                                 int* status, cudaStream_t s) {
+  const long long slots = T * k;
+  combine_dprob_kernel<<<(unsigned)((slots + 7) / 8), 256, 0, s>>>(
+      static_cast<const uint4*>(dout), static_cast<const uint4*>(y), inv, prob, slots, k, H / 8, cap,
+      dprob, status);
   return cudaGetLastError();
 }
 

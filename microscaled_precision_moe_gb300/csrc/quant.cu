@@ -14,6 +14,7 @@
 // column-wise 32x1 copy, transposed, from a shared-memory copy of the tile.
 #include <cstring>
 #include "quant.cuh"
+#include "mxfp8.cuh"
 
 namespace mpm {
 
@@ -55,27 +56,6 @@ MPM_DEV const __nv_bfloat16* nvfp4_row_ptr(const Nvfp4Rows& p, long long row) {
   for (int i = 0; i < 3; ++i)
     if (k < p.nparts - 1 && lr >= p.part_rows[k]) { lr -= p.part_rows[k]; ++k; }
   return p.part[k] + (g * p.part_rows[k] + lr) * (long long)p.K;
-}
-
-// {s, s} as the operand of a packed f32x2 multiply
-MPM_DEV uint64_t f32x2_splat(float s) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(v) : "f"(s));
-  return v;
-}
-// the bf16 pair in w (low half first) times a power of two, then packed to
-// E4M3 (RN, satfinite, low byte first).  Both lanes go through one packed
-// f32x2 multiply: per lane the same IEEE product as a scalar multiply (exact
-// here), so the codes are those of the scalar path.
-MPM_DEV uint32_t e4m3x2_scaled(uint32_t w, uint64_t sc2) {
-  uint64_t v, r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(bf16lo(w)), "f"(bf16hi(w)));
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(v), "l"(sc2));
-  float lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(r));
-  uint16_t out;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(out) : "f"(lo), "f"(hi));
-  return out;
 }
 
 // the bf16 pair in w times r (one packed f32x2 multiply, per lane the IEEE
@@ -532,16 +512,6 @@ __global__ void __launch_bounds__(256) group_amax_kernel(const GroupAmax p, int 
 // MXFP8
 // ============================================================================
 
-// Scale exponent e of a block whose |max| has the fp32 bit pattern `bits`:
-// the smallest e with a <= 448 * 2^e, clamped to [-127, 127].  For
-// a = 1.f * 2^p:  e = p - 8 + [1.f > 1.75].  Zero and subnormal a clamp to -127.
-MPM_DEV int mx_exponent(uint32_t bits) {
-  const int E = (int)(bits >> 23) & 0xFF;
-  if (E == 0) return -127;
-  const int e = (E - 127) - 8 + (((bits & 0x7FFFFFu) > 0x600000u) ? 1 : 0);
-  return e < -127 ? -127 : (e > 127 ? 127 : e);
-}
-
 // 32 bf16 values (16 words) -> 32 E4M3 codes (8 words) scaled by 2^-e
 MPM_DEV void mx_encode32(const uint32_t (&w)[16], float scale, uint32_t (&o)[8]) {
   const uint64_t sc2 = f32x2_splat(scale);
@@ -549,8 +519,6 @@ MPM_DEV void mx_encode32(const uint32_t (&w)[16], float scale, uint32_t (&o)[8])
   for (int j = 0; j < 8; ++j)
     o[j] = e4m3x2_scaled(w[2 * j], sc2) | (e4m3x2_scaled(w[2 * j + 1], sc2) << 16);
 }
-
-MPM_DEV float pow2_neg(int e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
 
 struct Mxfp8Args {
   const __nv_bfloat16* x;

@@ -17,6 +17,16 @@ def _ptr(t):
     return None if t is None else C.c_void_p(t.data_ptr())
 
 
+def _dp(t):
+    """A nullable tensor's address."""
+    return None if t is None else t.data_ptr()
+
+
+def _ld(t):
+    """Row pitch in elements (torch leaves the stride of a one-row matrix open)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
 def _stream(dev=None):
     return C.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
@@ -336,6 +346,31 @@ def moe_gather_nvfp4(q, s, ts, K: int, perm, seg, E: int, k: int, cap: int, out=
     return dq, ds, dts
 
 
+def moe_gather_mxfp8(q, s, perm, seg, E: int, k: int, cap: int, out=None):
+    """Row-wise MXFP8 rows (codes [T, K], tiled scales) -> the same two in the
+    permuted layout of cap rows: the row-wise bytes mxfp8_quantize_gather gives
+    for the bf16 rows they came from."""
+    lib = L.load()
+    _check(q, "q", torch.uint8, dim=2, contiguous=True)
+    T, K = q.shape
+    if K % 32 != 0:
+        raise ValueError(f"q: K = {K} is not a multiple of the 32-value MXFP8 block")
+    _check(s, "s", torch.uint8, contiguous=True, min_numel=scale_bytes(T, K // 32))
+    _check_route(perm, seg, E, cap)
+    dev = q.device
+    if out is None:
+        out = (torch.empty(cap, K, dtype=torch.uint8, device=dev),
+               torch.empty(scale_bytes(cap, K // 32), dtype=torch.uint8, device=dev))
+    dq, ds = out
+    _check(dq, "out codes", torch.uint8, contiguous=True, min_numel=cap * K)
+    _check(ds, "out scales", torch.uint8, contiguous=True, min_numel=scale_bytes(cap, K // 32))
+    _need_cuda(q, s, perm, seg, dq, ds)
+    st = lib.mpm_moe_gather_mxfp8(q.data_ptr(), s.data_ptr(), T, K, k, perm.data_ptr(),
+                                  seg.data_ptr(), E, cap, dq.data_ptr(), ds.data_ptr(), _stream(dev))
+    L.check(st, "mpm_moe_gather_mxfp8")
+    return dq, ds
+
+
 def moe_combine(y_perm, inv_perm, T: int, k: int, out=None):
     """out [T, H] bf16: each token's k rows of y_perm summed in slot order."""
     lib = L.load()
@@ -349,6 +384,250 @@ def moe_combine(y_perm, inv_perm, T: int, k: int, out=None):
     st = lib.mpm_moe_combine(_ptr(y_perm), _ptr(inv_perm), T, k, H, _ptr(out),
                              _stream(y_perm.device))
     L.check(st, "mpm_moe_combine")
+    return out
+
+
+def moe_combine_dprob(dout, y_perm, inv_perm, prob, out=None):
+    """dprob fp32 [T, k]: the gradient of the routing weights prob [T, k] from
+    dout bf16 [T, H] and the expert outputs y_perm bf16 [capacity, H] that the
+    forward combined (0 where the weight is 0 or the slot has no row)."""
+    lib = L.load()
+    _check(dout, "dout", torch.bfloat16, dim=2, contiguous=True)
+    _check(y_perm, "y_perm", torch.bfloat16, dim=2, contiguous=True)
+    _check(prob, "prob", torch.float32, dim=2, contiguous=True)
+    T, k = prob.shape
+    H = dout.shape[1]
+    if dout.shape[0] != T or y_perm.shape[1] != H:
+        raise ValueError(f"dout {tuple(dout.shape)} and y_perm {tuple(y_perm.shape)} do not match "
+                         f"prob {tuple(prob.shape)}")
+    _check(inv_perm, "inv_perm", torch.int32, contiguous=True, min_numel=T * k)
+    if out is None:
+        out = torch.empty(T, k, dtype=torch.float32, device=dout.device)
+    _check(out, "out", torch.float32, contiguous=True, min_numel=T * k)
+    _need_cuda(dout, y_perm, inv_perm, prob, out)
+    st = lib.mpm_moe_combine_dprob(dout.data_ptr(), y_perm.data_ptr(), inv_perm.data_ptr(),
+                                   prob.data_ptr(), T, k, H, y_perm.shape[0], out.data_ptr(),
+                                   _stream(dout.device))
+    L.check(st, "mpm_moe_combine_dprob")
+    return out
+
+
+# ------------------------------------------------------------------ residual RMSNorm
+
+def _weight_dtype(weight, K):
+    if weight.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"weight: expected bf16 or fp32, got {weight.dtype}")
+    if weight.dim() != 1 or weight.shape[0] != K or not weight.is_contiguous():
+        raise ValueError(f"weight: expected a contiguous [{K}], got shape {tuple(weight.shape)}")
+    return L.DTYPE_F32 if weight.dtype == torch.float32 else L.DTYPE_BF16
+
+
+def _check_like(t, name, M, K):
+    """A bf16 [M, K] with dense rows."""
+    _check_rows(t, name)
+    if t.shape != (M, K):
+        raise ValueError(f"{name}: expected shape {(M, K)}, got {tuple(t.shape)}")
+
+
+def add_rmsnorm(x, weight, residual=None, eps=1e-6, want_y=True, quantize=False, out=None):
+    """h = x + residual and y = h / rms(h) * weight of bf16 [M, K] rows.
+
+    Returns a dict (``out`` when given, its buffers reused): y bf16 [M, K]
+    (unless want_y is False), h bf16 [M, K] (with a residual), rstd fp32 [M],
+    and with ``quantize`` row_q u8 [M, K], row_s (tiled [M, K/32]): the bytes
+    mxfp8_quantize(y, colwise=False) gives.  weight: bf16 or fp32 [K]."""
+    lib = L.load()
+    _check_rows(x, "x")
+    M, K = x.shape
+    wdt = _weight_dtype(weight, K)
+    if residual is not None:
+        _check_like(residual, "residual", M, K)
+    dev = x.device
+    o = {} if out is None else out
+    if want_y and "y" not in o:
+        o["y"] = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
+    if residual is not None and "h" not in o:
+        o["h"] = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
+    if "rstd" not in o:
+        o["rstd"] = torch.empty(M, dtype=torch.float32, device=dev)
+    if quantize:
+        if K % 32 != 0:
+            raise ValueError(f"x: K = {K} is not a multiple of the 32-value MXFP8 block")
+        if "row_q" not in o:
+            o["row_q"] = torch.empty(M, K, dtype=torch.uint8, device=dev)
+        if "row_s" not in o:
+            o["row_s"] = torch.empty(scale_bytes(M, K // 32), dtype=torch.uint8, device=dev)
+    y = o["y"] if want_y else None
+    h = o["h"] if residual is not None else None
+    q, s = (o["row_q"], o["row_s"]) if quantize else (None, None)
+    rstd = o["rstd"]
+    if out is not None:
+        for t, name in ((y, "y"), (h, "h")):
+            if t is not None:
+                _check_like(t, name, M, K)
+        _check(rstd, "rstd", torch.float32, contiguous=True, min_numel=M)
+        if quantize:
+            _check(q, "row_q", torch.uint8, contiguous=True, min_numel=M * K)
+            _check(s, "row_s", torch.uint8, contiguous=True, min_numel=scale_bytes(M, K // 32))
+    _need_cuda(x, weight, residual, y, h, rstd, q, s)
+    st = lib.mpm_add_rmsnorm(
+        x.data_ptr(), M, K, _ld(x), _dp(residual), 0 if residual is None else _ld(residual),
+        weight.data_ptr(), wdt, eps, _dp(h), 0 if h is None else _ld(h),
+        _dp(y), 0 if y is None else _ld(y), rstd.data_ptr(), _dp(q), _dp(s), _stream(dev))
+    L.check(st, "mpm_add_rmsnorm")
+    return o
+
+
+def add_rmsnorm_backward_workspace_bytes(M: int, K: int) -> int:
+    return int(L.load().mpm_add_rmsnorm_backward_workspace_bytes(M, K))
+
+
+def add_rmsnorm_backward(dy, h, rstd, weight, dy2=None, dh=None, want_dw=True, out=None, ws=None):
+    """Gradient of add_rmsnorm: (dx bf16 [M, K], dw fp32 [K] or None).  dx is
+    the gradient of h, so of x and the residual alike.  dy (+ dy2): gradient
+    of y from its one or two readers; dh: gradient that reaches h along the
+    residual stream; h, rstd: the forward's (h = x without a residual).
+    ``out``: (dx, dw) buffers; ws: uint8 workspace of
+    add_rmsnorm_backward_workspace_bytes(M, K)."""
+    lib = L.load()
+    _check_rows(dy, "dy")
+    M, K = dy.shape
+    _check_like(h, "h", M, K)
+    wdt = _weight_dtype(weight, K)
+    _check(rstd, "rstd", torch.float32, contiguous=True, min_numel=M)
+    for t, name in ((dy2, "dy2"), (dh, "dh")):
+        if t is not None:
+            _check_like(t, name, M, K)
+    dev = dy.device
+    if out is None:
+        out = (torch.empty(M, K, dtype=torch.bfloat16, device=dev),
+               torch.empty(K, dtype=torch.float32, device=dev) if want_dw else None)
+    dx, dw = out
+    if not want_dw:
+        dw = None
+    _check_like(dx, "dx", M, K)
+    if want_dw:
+        _check(dw, "dw", torch.float32, contiguous=True, min_numel=K)
+        need = lib.mpm_add_rmsnorm_backward_workspace_bytes(M, K)
+        if ws is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check(ws, "ws", torch.uint8, contiguous=True, min_numel=need)
+    else:
+        ws = None
+    _need_cuda(dy, h, rstd, weight, dy2, dh, dx, dw, ws)
+    st = lib.mpm_add_rmsnorm_backward(
+        dy.data_ptr(), _ld(dy), _dp(dy2), 0 if dy2 is None else _ld(dy2), h.data_ptr(), _ld(h),
+        rstd.data_ptr(), weight.data_ptr(), wdt, _dp(dh), 0 if dh is None else _ld(dh), M, K,
+        dx.data_ptr(), _ld(dx), _dp(dw), _dp(ws), 0 if ws is None else ws.numel(), _stream(dev))
+    L.check(st, "mpm_add_rmsnorm_backward")
+    return dx, dw
+
+
+# ------------------------------------------------------------------ router
+
+_SCORES = {"softmax": L.SCORE_SOFTMAX, "sigmoid": L.SCORE_SIGMOID}
+
+
+def _route_args(logits, score, bias, token_mask):
+    """(score code, logits dtype code) of a router call, its inputs checked."""
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"logits: expected bf16 or fp32, got {logits.dtype}")
+    if logits.dim() != 2 or logits.stride(1) != 1:
+        raise ValueError(f"logits: expected [T, E] with dense rows, got shape {tuple(logits.shape)}")
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {tuple(_SCORES)}, got {score!r}")
+    T, E = logits.shape
+    if bias is not None:
+        _check(bias, "bias", torch.float32, dim=1, contiguous=True)
+        if bias.shape[0] != E:
+            raise ValueError(f"bias: expected [{E}], got shape {tuple(bias.shape)}")
+        if score != "sigmoid":
+            raise ValueError("bias: the choice bias belongs to sigmoid scores")
+    if token_mask is not None:
+        if token_mask.dtype not in (torch.bool, torch.uint8):
+            raise TypeError(f"token_mask: expected bool or uint8, got {token_mask.dtype}")
+        if token_mask.shape != (T,) or not token_mask.is_contiguous():
+            raise ValueError(f"token_mask: expected a contiguous [{T}], got {tuple(token_mask.shape)}")
+    return _SCORES[score], L.DTYPE_F32 if logits.dtype == torch.float32 else L.DTYPE_BF16
+
+
+def moe_route_workspace_bytes(T: int, E: int) -> int:
+    return int(L.load().mpm_moe_route_workspace_bytes(T, E))
+
+
+def moe_route(logits, k: int, score="softmax", normalize=True, scale=1.0, bias=None,
+              token_mask=None, out=None, ws=None):
+    """Top-k routing of logits [T, E] (bf16 or fp32).
+
+    Returns a dict (``out`` when given): ids int32 [T, k], prob fp32 [T, k]
+    (the inputs of moe_build_segments), counts int32 [E], load fp32 [E] (mean
+    score shares), n_tokens int32 [1] and loss fp32 [1], the balance loss
+    E / (k n) sum_e counts_e load_e.  score: "softmax", or "sigmoid" with an
+    optional choice ``bias`` fp32 [E].  token_mask: bool [T], False for tokens
+    that get weight 0 and are not counted.  Experts masked with -inf or the
+    type's lowest value are out of reach."""
+    lib = L.load()
+    sc, ldt = _route_args(logits, score, bias, token_mask)
+    T, E = logits.shape
+    dev = logits.device
+    need = lib.mpm_moe_route_workspace_bytes(T, E)
+    i32, f32 = torch.int32, torch.float32
+    if out is None:
+        out = {"ids": torch.empty(T, k, dtype=i32, device=dev),
+               "prob": torch.empty(T, k, dtype=f32, device=dev),
+               "counts": torch.empty(E, dtype=i32, device=dev),
+               "load": torch.empty(E, dtype=f32, device=dev),
+               "n_tokens": torch.empty(1, dtype=i32, device=dev),
+               "loss": torch.empty(1, dtype=f32, device=dev)}
+    else:
+        for name, dt, n in (("ids", i32, T * k), ("prob", f32, T * k), ("counts", i32, E),
+                            ("load", f32, E), ("n_tokens", i32, 1), ("loss", f32, 1)):
+            _check(out[name], name, dt, contiguous=True, min_numel=n)
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(ws, "ws", torch.uint8, contiguous=True, min_numel=need)
+    _need_cuda(logits, bias, token_mask, ws, *out.values())
+    st = lib.mpm_moe_route(
+        logits.data_ptr(), ldt, T, E, _ld(logits), k, sc, 1 if normalize else 0, scale, _dp(bias),
+        _dp(token_mask), out["ids"].data_ptr(), out["prob"].data_ptr(), out["counts"].data_ptr(),
+        out["load"].data_ptr(), out["n_tokens"].data_ptr(), out["loss"].data_ptr(), ws.data_ptr(),
+        ws.numel(), _stream(dev))
+    L.check(st, "mpm_moe_route")
+    return out
+
+
+def moe_route_backward(logits, ids, counts, n_tokens, dprob=None, dloss=None, score="softmax",
+                       normalize=True, scale=1.0, bias=None, token_mask=None, out=None):
+    """dlogits [T, E] (the logits' type) of moe_route with the same arguments,
+    from dprob fp32 [T, k] and / or dloss fp32 [1]; ids, counts and n_tokens
+    are the forward's.  The choice and the counts are constants."""
+    lib = L.load()
+    sc, ldt = _route_args(logits, score, bias, token_mask)
+    T, E = logits.shape
+    dev = logits.device
+    _check(ids, "ids", torch.int32, dim=2, contiguous=True)
+    k = ids.shape[1]
+    if ids.shape[0] != T:
+        raise ValueError(f"ids: expected [{T}, k], got shape {tuple(ids.shape)}")
+    _check(counts, "counts", torch.int32, contiguous=True, min_numel=E)
+    _check(n_tokens, "n_tokens", torch.int32, min_numel=1)
+    if dprob is not None:
+        _check(dprob, "dprob", torch.float32, contiguous=True)
+        if dprob.shape != ids.shape:
+            raise ValueError(f"dprob: expected {tuple(ids.shape)}, got shape {tuple(dprob.shape)}")
+    if dloss is not None:
+        _check(dloss, "dloss", torch.float32, min_numel=1)
+    if out is None:
+        out = torch.empty(T, E, dtype=logits.dtype, device=dev)
+    _check(out, "out", logits.dtype, dim=2)
+    if out.shape != logits.shape or out.stride(1) != 1:
+        raise ValueError(f"out: expected {tuple(logits.shape)} with dense rows")
+    _need_cuda(logits, ids, counts, n_tokens, dprob, dloss, bias, token_mask, out)
+    st = lib.mpm_moe_route_backward(
+        logits.data_ptr(), ldt, T, E, _ld(logits), k, sc, 1 if normalize else 0, scale, _dp(bias),
+        _dp(token_mask), ids.data_ptr(), counts.data_ptr(), n_tokens.data_ptr(), _dp(dprob),
+        _dp(dloss), out.data_ptr(), _ld(out), _stream(dev))
+    L.check(st, "mpm_moe_route_backward")
     return out
 
 

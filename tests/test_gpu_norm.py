@@ -1,0 +1,239 @@
+"""The residual RMSNorm on the GPU against its fp64 definition, and its MXFP8
+output byte for byte against the quantiser.
+
+Bounds, derived from the arithmetic: a value rounded once to bf16 is off by at
+most 2^-8 of itself; rstd is an fp32 function of an fp32 sum of K positive
+squares whose longest chain of additions is below 80 (5e-6); sums with
+cancellation are off by their chain length times 2^-24 of the sum of their
+magnitudes.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import norm as N
+from oracle import quant as Q
+from tests.gpu_util import need_gpu, np_bf16, u8, assert_bytes_equal
+
+pytestmark = pytest.mark.gpu
+
+BF16, RSTD, DX, DW = 2.0 ** -8, 5e-6, 1e-5, 2e-5
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def _ops():
+    from microscaled_precision_moe_gb300 import ops
+    return ops
+
+
+def _rows(seed, M, K, pad=0, std=1.0, off=0):
+    """bf16 [M, K] inside rows of K + pad elements, starting `off` elements
+    into the buffer; every eighth row 100 times as large."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    v = torch.randn(M * (K + pad) + off, device="cuda", generator=g) * std
+    v = v.to(torch.bfloat16)[off:].view(M, K + pad)[:, :K]
+    v[::8] *= 100
+    return v
+
+
+def _weight(seed, K, f32):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    w = 1.0 + 0.2 * torch.randn(K, device="cuda", generator=g)
+    return w if f32 else w.to(torch.bfloat16)
+
+
+def _within(got, want, tol, what):
+    bad = np.abs(np.asarray(got, np.float64) - want) > tol
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} out of bounds, first {np.argwhere(bad)[0]}"
+
+
+def _check_forward(o, x, w, r, eps, quantize):
+    ops = _ops()
+    xr = np_bf16(x), None if r is None else np_bf16(r)
+    h, y, rstd = N.add_rmsnorm(xr[0], w.float().cpu().numpy(), xr[1], eps)
+    _within(o["rstd"].cpu().numpy(), rstd, RSTD * rstd, "rstd")
+    _within(np_bf16(o["y"]), y, (BF16 + 2 * RSTD) * np.abs(y) + 1e-38, "y")
+    if r is not None:
+        _within(np_bf16(o["h"]), h, (BF16 + 1e-6) * np.abs(h) + 1e-38, "h")
+    if quantize:
+        ref = ops.mxfp8_quantize(o["y"], colwise=False)
+        assert_bytes_equal(u8(o["row_q"]), u8(ref["row_q"]), "codes")
+        assert_bytes_equal(u8(o["row_s"]), u8(ref["row_s"]), "tiled scales")
+
+
+# widths on both sides of every vector, block and thread-count boundary
+@pytest.mark.parametrize("M,K", [(1, 32), (3, 64), (129, 96), (5, 2048), (64, 7168), (2, 4096), (2, 4128),
+                                 (7, 8192), (2, 16384)])
+@pytest.mark.parametrize("pad", [0, 8, 5])
+def test_forward_with_quantised_output(M, K, pad):
+    x, r = _rows(1, M, K, pad), _rows(2, M, K, pad, 3.0)
+    w = _weight(3, K, K % 64 == 0)
+    o = _ops().add_rmsnorm(x, w, residual=r, eps=1e-5, quantize=True)
+    _check_forward(o, x, w, r, 1e-5, True)
+
+
+@pytest.mark.parametrize("M,K,pad,off", [(1, 1, 0, 0), (4, 7, 0, 0), (33, 100, 0, 0), (9, 1003, 2, 1),
+                                         (3, 2056, 0, 0), (2, 4097, 0, 0), (2, 16383, 0, 0), (5, 1544, 24, 0),
+                                         (5, 512, 0, 3), (6, 520, 4, 4), (6, 1030, 0, 2)])
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("res", [True, False])
+def test_forward_any_width_pitch_and_alignment(M, K, pad, off, f32, res):
+    x, r = _rows(4, M, K, pad, off=off), _rows(5, M, K, pad) if res else None
+    w = _weight(6, K, f32)
+    o = _ops().add_rmsnorm(x, w, residual=r)
+    assert ("h" in o) == res
+    _check_forward(o, x, w, r, 1e-6, False)
+
+
+def test_codes_match_the_oracle_quantiser():
+    x, w = _rows(7, 40, 256), _weight(8, 256, True)
+    o = _ops().add_rmsnorm(x, w, quantize=True)
+    codes, scales = Q.mxfp8_quantize_rowwise(np_bf16(o["y"]))[:2]
+    assert_bytes_equal(u8(o["row_q"]), codes, "codes")
+    assert_bytes_equal(Q.unswizzle_scales(u8(o["row_s"]), 40, 8), scales, "scales")
+
+
+def test_only_the_outputs_asked_for_and_8_bits_alone():
+    ops = _ops()
+    x, w = _rows(9, 6, 128), _weight(10, 128, False)
+    full = ops.add_rmsnorm(x, w, quantize=True)
+    o = ops.add_rmsnorm(x, w, want_y=False, quantize=True)
+    assert set(o) == {"rstd", "row_q", "row_s"}
+    assert torch.equal(o["row_q"], full["row_q"]) and torch.equal(o["row_s"], full["row_s"])
+    assert set(ops.add_rmsnorm(x, w)) == {"y", "rstd"}
+
+
+@pytest.mark.parametrize("K,pad", [(96, 32), (100, 28)])
+def test_nothing_outside_the_outputs_is_written(K, pad):
+    M = 5
+    buf = {n: torch.full((M + 2, K + pad), 7.0, dtype=torch.bfloat16, device="cuda") for n in ("y", "h", "dx")}
+    view = {n: b[1:M + 1, :K] for n, b in buf.items()}
+    x, r, w = _rows(11, M, K), _rows(12, M, K), _weight(13, K, True)
+    o = _ops().add_rmsnorm(x, w, residual=r, out={"y": view["y"], "h": view["h"]})
+    _ops().add_rmsnorm_backward(x, o["h"], o["rstd"], w, out=(view["dx"], torch.empty(K, device="cuda")))
+    torch.cuda.synchronize()
+    for b in buf.values():
+        assert (b[0] == 7).all() and (b[-1] == 7).all() and (b[:, K:] == 7).all()
+
+
+@pytest.mark.parametrize("K", [2048, 7168, 1001])
+def test_in_place_residual(K):
+    ops = _ops()
+    x, r, w = _rows(14, 70, K), _rows(15, 70, K), _weight(16, K, False)
+    ref = ops.add_rmsnorm(x, w, residual=r)
+    x2, r2 = x.clone(), r.clone()
+    o = ops.add_rmsnorm(x2, w, residual=r2, out={"h": r2, "y": x2})
+    assert torch.equal(o["h"], ref["h"]) and torch.equal(o["y"], ref["y"]) and o["h"] is r2
+    dx, dw = ops.add_rmsnorm_backward(x, ref["h"], ref["rstd"], w, dh=r)
+    r3 = r.clone()
+    dx2, dw2 = ops.add_rmsnorm_backward(x, ref["h"], ref["rstd"], w, dh=r3, out=(r3, torch.empty_like(dw)))
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+def test_rows_of_zeros_infinities_and_nan():
+    """A zero row gives zeros; NaN and infinities stay in their rows."""
+    K = 256
+    x, w = _rows(17, 8, K), _weight(18, K, True)
+    x[2] = 0
+    x[3, 5] = float("inf")
+    x[4, 6] = float("nan")
+    x[5] = 1e30                                       # the square sum leaves fp32's range
+    o = _ops().add_rmsnorm(x, w, quantize=True)
+    y, rstd = np_bf16(o["y"]), o["rstd"].cpu().numpy()
+    assert not y[2].any() and abs(rstd[2] - 1e3) < 1e-2
+    assert not u8(o["row_q"])[2].any()
+    assert rstd[3] == 0 and np.isnan(y[3, 5]) and np.isnan(y[4]).all()
+    assert rstd[5] == 0 and not y[5].any()
+    keep = [0, 1, 6, 7]
+    ref = _ops().add_rmsnorm(x[keep].contiguous(), w)
+    assert torch.equal(o["y"][keep], ref["y"]) and torch.equal(o["rstd"][keep], ref["rstd"])
+
+
+@pytest.mark.parametrize("M,K,pad,off", [(1, 32, 0, 0), (2, 1, 0, 0), (17, 100, 0, 0), (129, 2048, 0, 0),
+                                         (40, 7168, 8, 0), (700, 64, 0, 0), (1500, 1544, 24, 0), (9, 1003, 2, 1),
+                                         (3, 4104, 0, 0), (3, 16384, 0, 0), (2, 16383, 0, 0), (30, 1030, 0, 2)])
+@pytest.mark.parametrize("two,res,f32", [(True, True, True), (False, True, False), (False, False, True)])
+def test_backward(M, K, pad, off, two, res, f32):
+    ops = _ops()
+    h, w = _rows(20, M, K, pad, 2.0, off), _weight(21, K, f32)
+    dy, dy2 = _rows(22, M, K, pad, 1e-2), _rows(23, M, K, pad, 1e-2) if two else None
+    dh = _rows(24, M, K, pad, 1e-2) if res else None
+    rstd = ops.add_rmsnorm(h, w)["rstd"]
+    dx, dw = ops.add_rmsnorm_backward(dy, h, rstd, w, dy2=dy2, dh=dh)
+    total = np_bf16(dy).astype(np.float64) + (np_bf16(dy2) if two else 0.0)
+    rx, rw, mx, mw = N.add_rmsnorm_backward(total, np_bf16(h), rstd.cpu().numpy(), w.float().cpu().numpy(),
+                                            np_bf16(dh) if res else None)
+    _within(np_bf16(dx), rx, BF16 * np.abs(rx) + DX * mx + 1e-38, "dx")
+    _within(dw.cpu().numpy(), rw, DW * mw + 1e-38, "dw")
+    again = ops.add_rmsnorm_backward(dy, h, rstd, w, dy2=dy2, dh=dh)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+    alone, none = ops.add_rmsnorm_backward(dy, h, rstd, w, dy2=dy2, dh=dh, want_dw=False)
+    assert none is None and torch.equal(alone, dx)
+
+
+def test_backward_against_differences_of_the_forward():
+    """<dy, y> moves by <dx, v> along v: the kernels' own forward and backward,
+    fp32 rows made of bf16 values, a step large enough for bf16's rounding."""
+    ops = _ops()
+    M, K, eps = 64, 512, 1e-2
+    x, w = _rows(25, M, K), _weight(26, K, True)
+    x[::8] /= 100
+    v = torch.randn(M, K, device="cuda", generator=torch.Generator(device="cuda").manual_seed(27)).to(torch.bfloat16)
+    dy = _rows(28, M, K)
+    lo, hi = (x.float() - 0.05 * v.float()).to(torch.bfloat16), (x.float() + 0.05 * v.float()).to(torch.bfloat16)
+    f = [(ops.add_rmsnorm(t, w, eps=eps)["y"].double() * dy.double()).sum(1) for t in (lo, hi)]
+    o = ops.add_rmsnorm(x, w, eps=eps)
+    dx, _ = ops.add_rmsnorm_backward(dy, x, o["rstd"], w)
+    want = (dx.double() * (hi.double() - lo.double())).sum(1)
+    # y's rounding: K independent errors of at most 2^-9 |y dy| each, twice; the
+    # step's third-order term is below 1 % of the change; six standard deviations
+    noise = 6 * (2 * (2.0 ** -9 * o["y"].double() * dy.double()).square().sum(1)).sqrt()
+    size = (dx.double() * (hi.double() - lo.double())).square().sum(1).sqrt() * 6
+    assert ((f[1] - f[0] - want).abs() <= noise + 0.02 * size).all()
+
+
+def test_other_stream_and_graph_capture():
+    ops = _ops()
+    x, r, w = _rows(30, 33, 1024), _rows(31, 33, 1024), _weight(32, 1024, False)
+    ref = ops.add_rmsnorm(x, w, residual=r, quantize=True)
+    dref = ops.add_rmsnorm_backward(x, ref["h"], ref["rstd"], w, dh=r)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        o = ops.add_rmsnorm(x, w, residual=r, quantize=True)
+        d = ops.add_rmsnorm_backward(x, o["h"], o["rstd"], w, dh=r)
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o2 = ops.add_rmsnorm(x, w, residual=r, quantize=True)
+        d2 = ops.add_rmsnorm_backward(x, o2["h"], o2["rstd"], w, dh=r)
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    for a in (o, o2):
+        assert all(torch.equal(a[n], ref[n]) for n in ref)
+    for a in (d, d2):
+        assert all(torch.equal(s, t) for s, t in zip(a, dref))
+
+
+def test_offsets_past_32_bits():
+    """The last rows of a matrix of more than 2^31 elements."""
+    ops = _ops()
+    M, K = 270000, 8192
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    x[:] = _rows(33, 1, K)
+    tail = _rows(34, 130, K)
+    x[-130:] = tail
+    w = _weight(35, K, True)
+    o = ops.add_rmsnorm(x, w, quantize=True)
+    ref = ops.add_rmsnorm(tail.contiguous(), w)
+    assert torch.equal(o["y"][-130:], ref["y"])
+    q = ops.mxfp8_quantize(ref["y"], colwise=False)["row_q"]
+    assert torch.equal(o["row_q"][-130:], q)
+    dx, _ = ops.add_rmsnorm_backward(x, x, o["rstd"], w)
+    dref, _ = ops.add_rmsnorm_backward(tail, tail, ref["rstd"], w)
+    assert torch.equal(dx[-130:], dref)
