@@ -12,6 +12,8 @@ import torch
 
 from . import _lib as L
 
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
 
 def _ptr(t):
     return None if t is None else C.c_void_p(t.data_ptr())
@@ -22,13 +24,25 @@ def _dp(t):
     return None if t is None else t.data_ptr()
 
 
-def _ld(t):
-    """Row pitch in elements (torch leaves the stride of a one-row matrix open)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _mat(t, name, M, K):
+    """Row pitch in elements of a bf16 [M, K] with dense rows (torch leaves the
+    stride of a one-row matrix open)."""
+    if t.dtype is not _BF16 or t.shape != (M, K) or t.stride(1) != 1:
+        _check_rows(t, name)
+        if t.shape != (M, K):
+            raise ValueError(f"{name}: expected shape {(M, K)}, got {tuple(t.shape)}")
+    ld = t.stride(0)
+    return ld if ld >= K or M > 1 else K
 
 
 def _stream(dev=None):
     return C.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _raw_stream(dev):
+    """The device's current stream as an integer: the address _stream gives,
+    without building a Stream object (0.1 against 2.1 us a call on the host)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _need_cuda(*ts):
@@ -366,7 +380,8 @@ def moe_gather_mxfp8(q, s, perm, seg, E: int, k: int, cap: int, out=None):
     _check(ds, "out scales", torch.uint8, contiguous=True, min_numel=scale_bytes(cap, K // 32))
     _need_cuda(q, s, perm, seg, dq, ds)
     st = lib.mpm_moe_gather_mxfp8(q.data_ptr(), s.data_ptr(), T, K, k, perm.data_ptr(),
-                                  seg.data_ptr(), E, cap, dq.data_ptr(), ds.data_ptr(), _stream(dev))
+                                  seg.data_ptr(), E, cap, dq.data_ptr(), ds.data_ptr(),
+                                  _raw_stream(dev))
     L.check(st, "mpm_moe_gather_mxfp8")
     return dq, ds
 
@@ -407,7 +422,7 @@ def moe_combine_dprob(dout, y_perm, inv_perm, prob, out=None):
     _need_cuda(dout, y_perm, inv_perm, prob, out)
     st = lib.mpm_moe_combine_dprob(dout.data_ptr(), y_perm.data_ptr(), inv_perm.data_ptr(),
                                    prob.data_ptr(), T, k, H, y_perm.shape[0], out.data_ptr(),
-                                   _stream(dout.device))
+                                   _raw_stream(dout.device))
     L.check(st, "mpm_moe_combine_dprob")
     return out
 
@@ -415,18 +430,11 @@ def moe_combine_dprob(dout, y_perm, inv_perm, prob, out=None):
 # ------------------------------------------------------------------ residual RMSNorm
 
 def _weight_dtype(weight, K):
-    if weight.dtype not in (torch.bfloat16, torch.float32):
+    if weight.dtype is not _F32 and weight.dtype is not _BF16:
         raise TypeError(f"weight: expected bf16 or fp32, got {weight.dtype}")
-    if weight.dim() != 1 or weight.shape[0] != K or not weight.is_contiguous():
+    if weight.shape != (K,) or not weight.is_contiguous():
         raise ValueError(f"weight: expected a contiguous [{K}], got shape {tuple(weight.shape)}")
-    return L.DTYPE_F32 if weight.dtype == torch.float32 else L.DTYPE_BF16
-
-
-def _check_like(t, name, M, K):
-    """A bf16 [M, K] with dense rows."""
-    _check_rows(t, name)
-    if t.shape != (M, K):
-        raise ValueError(f"{name}: expected shape {(M, K)}, got {tuple(t.shape)}")
+    return L.DTYPE_F32 if weight.dtype is _F32 else L.DTYPE_BF16
 
 
 def add_rmsnorm(x, weight, residual=None, eps=1e-6, want_y=True, quantize=False, out=None):
@@ -437,44 +445,54 @@ def add_rmsnorm(x, weight, residual=None, eps=1e-6, want_y=True, quantize=False,
     and with ``quantize`` row_q u8 [M, K], row_s (tiled [M, K/32]): the bytes
     mxfp8_quantize(y, colwise=False) gives.  weight: bf16 or fp32 [K]."""
     lib = L.load()
-    _check_rows(x, "x")
+    if x.dim() != 2:
+        _check_rows(x, "x")
     M, K = x.shape
+    ldx = _mat(x, "x", M, K)
     wdt = _weight_dtype(weight, K)
-    if residual is not None:
-        _check_like(residual, "residual", M, K)
     dev = x.device
+    y = h = q = s = None
+    ldr = ldh = ldy = 0
     o = {} if out is None else out
-    if want_y and "y" not in o:
-        o["y"] = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
-    if residual is not None and "h" not in o:
-        o["h"] = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
-    if "rstd" not in o:
-        o["rstd"] = torch.empty(M, dtype=torch.float32, device=dev)
+    if residual is not None:
+        ldr = _mat(residual, "residual", M, K)
+        h = o.get("h")
+        if h is None:
+            h = o["h"] = torch.empty(M, K, dtype=_BF16, device=dev)
+            ldh = K
+        else:
+            ldh = _mat(h, "h", M, K)
+    if want_y:
+        y = o.get("y")
+        if y is None:
+            y = o["y"] = torch.empty(M, K, dtype=_BF16, device=dev)
+            ldy = K
+        else:
+            ldy = _mat(y, "y", M, K)
+    rstd = o.get("rstd")
+    if rstd is None:
+        rstd = o["rstd"] = torch.empty(M, dtype=_F32, device=dev)
+    else:
+        _check(rstd, "rstd", _F32, contiguous=True, min_numel=M)
     if quantize:
         if K % 32 != 0:
             raise ValueError(f"x: K = {K} is not a multiple of the 32-value MXFP8 block")
-        if "row_q" not in o:
-            o["row_q"] = torch.empty(M, K, dtype=torch.uint8, device=dev)
-        if "row_s" not in o:
-            o["row_s"] = torch.empty(scale_bytes(M, K // 32), dtype=torch.uint8, device=dev)
-    y = o["y"] if want_y else None
-    h = o["h"] if residual is not None else None
-    q, s = (o["row_q"], o["row_s"]) if quantize else (None, None)
-    rstd = o["rstd"]
-    if out is not None:
-        for t, name in ((y, "y"), (h, "h")):
-            if t is not None:
-                _check_like(t, name, M, K)
-        _check(rstd, "rstd", torch.float32, contiguous=True, min_numel=M)
-        if quantize:
-            _check(q, "row_q", torch.uint8, contiguous=True, min_numel=M * K)
-            _check(s, "row_s", torch.uint8, contiguous=True, min_numel=scale_bytes(M, K // 32))
+        sb = lib.mpm_scale_bytes(M, K // 32)
+        q, s = o.get("row_q"), o.get("row_s")
+        if q is None:
+            q = o["row_q"] = torch.empty(M, K, dtype=_U8, device=dev)
+        else:
+            _check(q, "row_q", _U8, contiguous=True, min_numel=M * K)
+        if s is None:
+            s = o["row_s"] = torch.empty(sb, dtype=_U8, device=dev)
+        else:
+            _check(s, "row_s", _U8, contiguous=True, min_numel=sb)
     _need_cuda(x, weight, residual, y, h, rstd, q, s)
-    st = lib.mpm_add_rmsnorm(
-        x.data_ptr(), M, K, _ld(x), _dp(residual), 0 if residual is None else _ld(residual),
-        weight.data_ptr(), wdt, eps, _dp(h), 0 if h is None else _ld(h),
-        _dp(y), 0 if y is None else _ld(y), rstd.data_ptr(), _dp(q), _dp(s), _stream(dev))
-    L.check(st, "mpm_add_rmsnorm")
+    st = lib.mpm_add_rmsnorm(x.data_ptr(), M, K, ldx, _dp(residual), ldr, weight.data_ptr(), wdt, eps,
+                             _dp(h), ldh, _dp(y), ldy, rstd.data_ptr(), _dp(q), _dp(s),
+                             _raw_stream(dev))
+    if st:
+        L.check(st, "mpm_add_rmsnorm")
     return o
 
 
@@ -490,36 +508,41 @@ def add_rmsnorm_backward(dy, h, rstd, weight, dy2=None, dh=None, want_dw=True, o
     ``out``: (dx, dw) buffers; ws: uint8 workspace of
     add_rmsnorm_backward_workspace_bytes(M, K)."""
     lib = L.load()
-    _check_rows(dy, "dy")
+    if dy.dim() != 2:
+        _check_rows(dy, "dy")
     M, K = dy.shape
-    _check_like(h, "h", M, K)
+    lddy = _mat(dy, "dy", M, K)
+    ldh = _mat(h, "h", M, K)
     wdt = _weight_dtype(weight, K)
-    _check(rstd, "rstd", torch.float32, contiguous=True, min_numel=M)
-    for t, name in ((dy2, "dy2"), (dh, "dh")):
-        if t is not None:
-            _check_like(t, name, M, K)
+    _check(rstd, "rstd", _F32, contiguous=True, min_numel=M)
+    lddy2 = 0 if dy2 is None else _mat(dy2, "dy2", M, K)
+    lddh = 0 if dh is None else _mat(dh, "dh", M, K)
     dev = dy.device
+    wsb = 0
     if out is None:
-        out = (torch.empty(M, K, dtype=torch.bfloat16, device=dev),
-               torch.empty(K, dtype=torch.float32, device=dev) if want_dw else None)
-    dx, dw = out
-    if not want_dw:
-        dw = None
-    _check_like(dx, "dx", M, K)
+        dx, lddx = torch.empty(M, K, dtype=_BF16, device=dev), K
+        dw = torch.empty(K, dtype=_F32, device=dev) if want_dw else None
+    else:
+        dx, dw = out
+        lddx = _mat(dx, "dx", M, K)
+        if want_dw:
+            _check(dw, "dw", _F32, contiguous=True, min_numel=K)
+        else:
+            dw = None
     if want_dw:
-        _check(dw, "dw", torch.float32, contiguous=True, min_numel=K)
-        need = lib.mpm_add_rmsnorm_backward_workspace_bytes(M, K)
+        wsb = lib.mpm_add_rmsnorm_backward_workspace_bytes(M, K)
         if ws is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        _check(ws, "ws", torch.uint8, contiguous=True, min_numel=need)
+            ws = torch.empty(wsb, dtype=_U8, device=dev)
+        else:
+            _check(ws, "ws", _U8, contiguous=True, min_numel=wsb)
     else:
         ws = None
     _need_cuda(dy, h, rstd, weight, dy2, dh, dx, dw, ws)
-    st = lib.mpm_add_rmsnorm_backward(
-        dy.data_ptr(), _ld(dy), _dp(dy2), 0 if dy2 is None else _ld(dy2), h.data_ptr(), _ld(h),
-        rstd.data_ptr(), weight.data_ptr(), wdt, _dp(dh), 0 if dh is None else _ld(dh), M, K,
-        dx.data_ptr(), _ld(dx), _dp(dw), _dp(ws), 0 if ws is None else ws.numel(), _stream(dev))
-    L.check(st, "mpm_add_rmsnorm_backward")
+    st = lib.mpm_add_rmsnorm_backward(dy.data_ptr(), lddy, _dp(dy2), lddy2, h.data_ptr(), ldh,
+                                      rstd.data_ptr(), weight.data_ptr(), wdt, _dp(dh), lddh, M, K,
+                                      dx.data_ptr(), lddx, _dp(dw), _dp(ws), wsb, _raw_stream(dev))
+    if st:
+        L.check(st, "mpm_add_rmsnorm_backward")
     return dx, dw
 
 
@@ -529,26 +552,30 @@ _SCORES = {"softmax": L.SCORE_SOFTMAX, "sigmoid": L.SCORE_SIGMOID}
 
 
 def _route_args(logits, score, bias, token_mask):
-    """(score code, logits dtype code) of a router call, its inputs checked."""
-    if logits.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"logits: expected bf16 or fp32, got {logits.dtype}")
-    if logits.dim() != 2 or logits.stride(1) != 1:
+    """(T, E, row pitch, score code, logits dtype code) of a router call, its
+    inputs checked."""
+    dt = logits.dtype
+    if dt is not _F32 and dt is not _BF16:
+        raise TypeError(f"logits: expected bf16 or fp32, got {dt}")
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] != 1):
         raise ValueError(f"logits: expected [T, E] with dense rows, got shape {tuple(logits.shape)}")
-    if score not in _SCORES:
+    sc = _SCORES.get(score)
+    if sc is None:
         raise ValueError(f"score must be one of {tuple(_SCORES)}, got {score!r}")
     T, E = logits.shape
     if bias is not None:
-        _check(bias, "bias", torch.float32, dim=1, contiguous=True)
-        if bias.shape[0] != E:
+        _check(bias, "bias", _F32, contiguous=True)
+        if bias.shape != (E,):
             raise ValueError(f"bias: expected [{E}], got shape {tuple(bias.shape)}")
         if score != "sigmoid":
             raise ValueError("bias: the choice bias belongs to sigmoid scores")
     if token_mask is not None:
-        if token_mask.dtype not in (torch.bool, torch.uint8):
+        if token_mask.dtype is not torch.bool and token_mask.dtype is not _U8:
             raise TypeError(f"token_mask: expected bool or uint8, got {token_mask.dtype}")
         if token_mask.shape != (T,) or not token_mask.is_contiguous():
             raise ValueError(f"token_mask: expected a contiguous [{T}], got {tuple(token_mask.shape)}")
-    return _SCORES[score], L.DTYPE_F32 if logits.dtype == torch.float32 else L.DTYPE_BF16
+    ld = logits.stride(0)
+    return T, E, ld if ld >= E or T > 1 else E, sc, L.DTYPE_F32 if dt is _F32 else L.DTYPE_BF16
 
 
 def moe_route_workspace_bytes(T: int, E: int) -> int:
@@ -565,34 +592,39 @@ def moe_route(logits, k: int, score="softmax", normalize=True, scale=1.0, bias=N
     E / (k n) sum_e counts_e load_e.  score: "softmax", or "sigmoid" with an
     optional choice ``bias`` fp32 [E].  token_mask: bool [T], False for tokens
     that get weight 0 and are not counted.  Experts masked with -inf or the
-    type's lowest value are out of reach."""
+    type's lowest value are out of reach.  ws: uint8 workspace of
+    moe_route_workspace_bytes(T, E)."""
     lib = L.load()
-    sc, ldt = _route_args(logits, score, bias, token_mask)
-    T, E = logits.shape
+    T, E, ld, sc, ldt = _route_args(logits, score, bias, token_mask)
     dev = logits.device
-    need = lib.mpm_moe_route_workspace_bytes(T, E)
-    i32, f32 = torch.int32, torch.float32
     if out is None:
-        out = {"ids": torch.empty(T, k, dtype=i32, device=dev),
-               "prob": torch.empty(T, k, dtype=f32, device=dev),
-               "counts": torch.empty(E, dtype=i32, device=dev),
-               "load": torch.empty(E, dtype=f32, device=dev),
-               "n_tokens": torch.empty(1, dtype=i32, device=dev),
-               "loss": torch.empty(1, dtype=f32, device=dev)}
+        ids = torch.empty(T, k, dtype=_I32, device=dev)
+        prob = torch.empty(T, k, dtype=_F32, device=dev)
+        counts = torch.empty(E, dtype=_I32, device=dev)
+        load = torch.empty(E, dtype=_F32, device=dev)
+        n_tokens = torch.empty(1, dtype=_I32, device=dev)
+        loss = torch.empty(1, dtype=_F32, device=dev)
+        out = {"ids": ids, "prob": prob, "counts": counts, "load": load, "n_tokens": n_tokens,
+               "loss": loss}
     else:
-        for name, dt, n in (("ids", i32, T * k), ("prob", f32, T * k), ("counts", i32, E),
-                            ("load", f32, E), ("n_tokens", i32, 1), ("loss", f32, 1)):
+        for name, dt, n in (("ids", _I32, T * k), ("prob", _F32, T * k), ("counts", _I32, E),
+                            ("load", _F32, E), ("n_tokens", _I32, 1), ("loss", _F32, 1)):
             _check(out[name], name, dt, contiguous=True, min_numel=n)
+        ids, prob, counts, load, n_tokens, loss = (out[n] for n in ("ids", "prob", "counts", "load",
+                                                                    "n_tokens", "loss"))
+    wsb = lib.mpm_moe_route_workspace_bytes(T, E)
     if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _check(ws, "ws", torch.uint8, contiguous=True, min_numel=need)
-    _need_cuda(logits, bias, token_mask, ws, *out.values())
-    st = lib.mpm_moe_route(
-        logits.data_ptr(), ldt, T, E, _ld(logits), k, sc, 1 if normalize else 0, scale, _dp(bias),
-        _dp(token_mask), out["ids"].data_ptr(), out["prob"].data_ptr(), out["counts"].data_ptr(),
-        out["load"].data_ptr(), out["n_tokens"].data_ptr(), out["loss"].data_ptr(), ws.data_ptr(),
-        ws.numel(), _stream(dev))
-    L.check(st, "mpm_moe_route")
+        if wsb:
+            ws = torch.empty(wsb, dtype=_U8, device=dev)
+    else:
+        _check(ws, "ws", _U8, contiguous=True, min_numel=wsb)
+    _need_cuda(logits, bias, token_mask, ws, ids, prob, counts, load, n_tokens, loss)
+    st = lib.mpm_moe_route(logits.data_ptr(), ldt, T, E, ld, k, sc, 1 if normalize else 0, scale,
+                           _dp(bias), _dp(token_mask), ids.data_ptr(), prob.data_ptr(),
+                           counts.data_ptr(), load.data_ptr(), n_tokens.data_ptr(), loss.data_ptr(),
+                           _dp(ws), wsb, _raw_stream(dev))
+    if st:
+        L.check(st, "mpm_moe_route")
     return out
 
 
@@ -602,32 +634,34 @@ def moe_route_backward(logits, ids, counts, n_tokens, dprob=None, dloss=None, sc
     from dprob fp32 [T, k] and / or dloss fp32 [1]; ids, counts and n_tokens
     are the forward's.  The choice and the counts are constants."""
     lib = L.load()
-    sc, ldt = _route_args(logits, score, bias, token_mask)
-    T, E = logits.shape
+    T, E, ld, sc, ldt = _route_args(logits, score, bias, token_mask)
     dev = logits.device
-    _check(ids, "ids", torch.int32, dim=2, contiguous=True)
+    _check(ids, "ids", _I32, dim=2, contiguous=True)
     k = ids.shape[1]
     if ids.shape[0] != T:
         raise ValueError(f"ids: expected [{T}, k], got shape {tuple(ids.shape)}")
-    _check(counts, "counts", torch.int32, contiguous=True, min_numel=E)
-    _check(n_tokens, "n_tokens", torch.int32, min_numel=1)
+    _check(counts, "counts", _I32, contiguous=True, min_numel=E)
+    _check(n_tokens, "n_tokens", _I32, min_numel=1)
     if dprob is not None:
-        _check(dprob, "dprob", torch.float32, contiguous=True)
+        _check(dprob, "dprob", _F32, contiguous=True)
         if dprob.shape != ids.shape:
             raise ValueError(f"dprob: expected {tuple(ids.shape)}, got shape {tuple(dprob.shape)}")
     if dloss is not None:
-        _check(dloss, "dloss", torch.float32, min_numel=1)
+        _check(dloss, "dloss", _F32, min_numel=1)
     if out is None:
-        out = torch.empty(T, E, dtype=logits.dtype, device=dev)
-    _check(out, "out", logits.dtype, dim=2)
-    if out.shape != logits.shape or out.stride(1) != 1:
-        raise ValueError(f"out: expected {tuple(logits.shape)} with dense rows")
+        out, ldd = torch.empty(T, E, dtype=logits.dtype, device=dev), E
+    else:
+        _check(out, "out", logits.dtype, dim=2)
+        if out.shape != logits.shape or (out.stride(1) != 1 and E != 1):
+            raise ValueError(f"out: expected {tuple(logits.shape)} with dense rows")
+        ldd = max(out.stride(0), E) if T == 1 else out.stride(0)
     _need_cuda(logits, ids, counts, n_tokens, dprob, dloss, bias, token_mask, out)
-    st = lib.mpm_moe_route_backward(
-        logits.data_ptr(), ldt, T, E, _ld(logits), k, sc, 1 if normalize else 0, scale, _dp(bias),
-        _dp(token_mask), ids.data_ptr(), counts.data_ptr(), n_tokens.data_ptr(), _dp(dprob),
-        _dp(dloss), out.data_ptr(), _ld(out), _stream(dev))
-    L.check(st, "mpm_moe_route_backward")
+    st = lib.mpm_moe_route_backward(logits.data_ptr(), ldt, T, E, ld, k, sc, 1 if normalize else 0,
+                                    scale, _dp(bias), _dp(token_mask), ids.data_ptr(),
+                                    counts.data_ptr(), n_tokens.data_ptr(), _dp(dprob), _dp(dloss),
+                                    out.data_ptr(), ldd, _raw_stream(dev))
+    if st:
+        L.check(st, "mpm_moe_route_backward")
     return out
 
 
