@@ -453,12 +453,14 @@ mpm_status mpm_moe_route(const void* logits, int logits_dtype, int64_t T, int64_
                          const uint8_t* mask, int32_t* ids, float* prob, int32_t* counts,
                          float* load, int32_t* n_tokens, float* loss, void* ws, size_t ws_bytes,
                          cudaStream_t stream) {
-  if (!ids || !prob || !counts || !load || !n_tokens || !loss || !ws) return MPM_ERR_NULL;
+  if (!ids || !prob || !counts || !load || !n_tokens || !loss) return MPM_ERR_NULL;
   mpm::RouteArgs a{};
   const mpm_status st = route_args(a, logits, logits_dtype, T, E, ld, k, score, normalize, scale,
                                    bias, mask);
   if (st != MPM_OK) return st;
-  if (ws_bytes < mpm::route_ws_bytes(T, (int)E)) return MPM_ERR_SHAPE;
+  const size_t need = mpm::route_ws_bytes(T, (int)E);
+  if (need && !ws) return MPM_ERR_NULL;
+  if (ws_bytes < need) return MPM_ERR_SHAPE;
   if (!aligned(ids, 4) || !aligned(prob, 4) || !aligned(counts, 4) || !aligned(load, 4) ||
       !aligned(n_tokens, 4) || !aligned(loss, 4) || !aligned(ws, 4))
     return MPM_ERR_ALIGN;

@@ -13,190 +13,479 @@
 // unmasked tokens, c_e the counts and P_e the mean over them of a token's
 // scores as shares of one, loss = E / (k n) sum_e c_e P_e: 1 at perfect balance.
 //
-// One warp per token, expert e in lane e % 32.  The choice compares the keys
-// themselves (order-preserving integers), k times the warp's maximum and the
-// lowest expert that holds it, so it is exact and ties go to the lower expert.
-// Scores use expf and IEEE division: with a bias the choice depends on their
-// last bit.  Sums over tokens go through per-block partials added in a fixed
-// order (no floating-point atomics).
+// One warp per token, expert e in lane e % 32 (bf16: experts 2 l and 2 l + 1 of
+// every 64 in lane l), so that runs of heavy experts spread over the lanes; the
+// next token's logits are in flight while this one is worked on.  The choice
+// compares the keys themselves, so it is exact, and ties go to the lower expert:
+//   1. tau: the k-th largest of the 32 lanes' own maxima (k warp maxima; equal
+//      lane maxima leave together, which can only lower tau).  At least k keys
+//      are >= tau, and few more: about 10 of 256 for k = 8.
+//   2. Those keys move to one lane each (ballots and shared memory), and each
+//      lane counts the keys above its own, its place among the choices; only
+//      where places collide are equal keys told apart by expert.
+// With k > 32, more than 32 such keys (masses of ties) or fewer than k lanes with
+// an expert in reach, the warp takes k maxima one after the other instead.
+// Softmax scores use the hardware exponential (a few ulp); sigmoid scores expf
+// and IEEE division, since with a bias the choice depends on their last bit.
+// Sums over tokens go through per-block partials added in a fixed order (no
+// floating-point atomics).
 #include "router.cuh"
 
 namespace mpm {
 
-constexpr int kRouteWarps = 8;
-constexpr int kRouteMaxParts = 608;
+constexpr int kRouteMaxParts = 152;                     // one block of up to 32 warps on each SM
+constexpr int kClusterCtas = 8;
+constexpr long long kClusterTokens = 512;               // one cluster routes up to this many tokens
 constexpr float kDeadLogit = -3.3895313892515355e38f;   // bf16's lowest finite value
 constexpr float kLargest = 3.4028234663852886e38f;
+constexpr float kLog2e = 1.44269504088896341f;
 
-// order-preserving map of a number (not NaN) to an integer above 0
+// warps of a block: as many as its registers allow
+constexpr int route_warps(int ne) { return ne <= 8 ? 32 : (ne <= 16 ? 16 : 8); }
+
+// order-preserving map of a number (not NaN) to an integer above 1, and back
 MPM_DEV uint32_t ordered_bits(float v) {
   const uint32_t u = __float_as_uint(__fadd_rn(v, 0.0f));      // -0 compares equal to +0
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
-
+MPM_DEV float ordered_value(uint32_t o) {
+  return __uint_as_float(o ^ ((uint32_t)((int)~o >> 31) | 0x80000000u));
+}
 MPM_DEV float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   return v;
 }
-MPM_DEV float warp_max(float v) {
+MPM_DEV float warp_max(float v) { return ordered_value(__reduce_max_sync(0xFFFFFFFFu, ordered_bits(v))); }
+
+// exp(v) for v <= 0, by the change of base 2^(v log2 e); -inf gives 0
+MPM_DEV float exp_neg(float v) { return exp2_ftz(__fmul_rn(v, kLog2e)); }
+
+// the lane's i-th expert
+template <bool BF16>
+MPM_DEV int expert_of(int i, int lane) {
+  return BF16 ? (i >> 1) * 64 + lane * 2 + (i & 1) : i * 32 + lane;
+}
+
+// A token's logits as loaded: a lane's NE values, bf16 pairs packed; -inf past E
+template <int NE, bool BF16>
+struct RawLogits {
+  static constexpr int W = BF16 ? NE / 2 : NE;
+  uint32_t w[W];
+  MPM_DEV void load(const RouteArgs& a, int t, int lane) {
+    if constexpr (BF16) {
+      const uint16_t* p = static_cast<const uint16_t*>(a.logits) + t * a.ld + lane * 2;
+      if (a.vec) {                       // even E, 4-byte aligned rows
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+        for (int i = 0; i < W; ++i)
+          w[i] = i * 64 + lane * 2 < a.E ? *reinterpret_cast<const uint32_t*>(p + i * 64) : 0xFF80FF80u;
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const int e = i * 64 + lane * 2;
+          const uint32_t lo = e < a.E ? p[i * 64] : 0xFF80u;
+          const uint32_t hi = e + 1 < a.E ? p[i * 64 + 1] : 0xFF80u;
+          w[i] = lo | (hi << 16);
+        }
+      }
+    } else {
+      const uint32_t* p = static_cast<const uint32_t*>(a.logits) + t * a.ld + lane;
+      if (a.vec) {                       // E = 32 NE
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = p[i * 32];
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = i * 32 + lane < a.E ? p[i * 32] : 0xFF800000u;
+      }
+    }
+  }
+  MPM_DEV float value(int i) const {
+    if constexpr (BF16) return (i & 1) ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
+    else return __uint_as_float(w[i]);
+  }
+};
+
+// Logits with -inf for what is out of reach; dead_bias: the lane's experts
+// whose bias puts them there
+template <int NE, bool BF16>
+MPM_DEV void route_logits(const RawLogits<NE, BF16>& raw, uint32_t dead_bias, float (&l)[NE]) {
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const float v = raw.value(i);
+    l[i] = (v > kDeadLogit && !(dead_bias >> i & 1u)) ? fminf(v, kLargest) : -INFINITY;
+  }
+}
+
+template <int NE, bool BF16>
+MPM_DEV uint32_t route_bias(const RouteArgs& a, int lane, float (&bias)[NE]) {
+  uint32_t dead = 0;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int e = expert_of<BF16>(i, lane);
+    bias[i] = (a.bias && e < a.E) ? a.bias[e] : 0.0f;
+    if (!(bias[i] > kDeadLogit)) dead |= 1u << i;
+  }
+  return dead;
+}
+
+// ---------------------------------------------------------------- forward
+// k maxima one after the other, lowest expert first among equals, those out of
+// reach last: ids, weights and counts of a token
+template <int NE, bool BF16>
+MPM_DEV void route_one_by_one(const RouteArgs& a, int t, int lane, const float (&key)[NE],
+                              const float (&s)[NE], float unit, bool on, int* sh_counts) {
+  uint32_t taken = 0;
+  float w0 = 0.0f, w1 = 0.0f, d = 0.0f;                 // lane j: weights of choices j and 32 + j
+  for (int j = 0; j < a.k; ++j) {
+    uint32_t best = 0;
+    int at = 0x7FFFFFFF, slot = 0;
+    float w = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const int e = expert_of<BF16>(i, lane);
+      uint32_t o = key[i] > -INFINITY ? ordered_bits(key[i]) : 1u;
+      if (e >= a.E || (taken >> i & 1u)) o = 0u;
+      if (o > best) { best = o; at = e; slot = i; w = s[i]; }
+    }
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
+    const int e = __reduce_min_sync(0xFFFFFFFFu, best == top ? at : 0x7FFFFFFF);
+    if (e == at) taken |= 1u << slot;
+    w = __shfl_sync(0xFFFFFFFFu, w, __ffs(__ballot_sync(0xFFFFFFFFu, e == at)) - 1);
+    d = __fadd_rn(d, w);
+    if ((j & 31) == lane) { if (j < 32) w0 = w; else w1 = w; }
+    if (lane == 0) {
+      a.ids[t * a.k + j] = e;
+      if (on && top > 1u) atomicAdd(&sh_counts[e], 1);
+    }
+  }
+  const float f = !a.normalize ? unit : (d > 0.0f ? __fdiv_rn(1.0f, d) : 0.0f);
+  const float sc = on ? __fmul_rn(f, a.scale) : 0.0f;
+  if (lane < a.k) a.prob[t * a.k + lane] = __fmul_rn(w0, sc);
+  if (lane + 32 < a.k) a.prob[t * a.k + 32 + lane] = __fmul_rn(w1, sc);
+}
+
+// a warp's shared memory in the token loop, NE * 32 + 64 words: its keys by
+// slot, the candidates' slots, the candidates' keys
+template <int NE>
+struct __align__(16) RouteWarp {
+  float key[NE * 32];
+  int slot[32];
+  float cand[32];
+};
+
+// One token: ids and weights to global memory, counts to sh_counts, shares
+// added to load.  raw: its logits; replaced by those of token `next`.
+template <int NE, bool SIG, bool BF16>
+MPM_DEV void route_token(const RouteArgs& a, int t, int next, int lane, RawLogits<NE, BF16>& raw,
+                         bool on, uint32_t dead_bias, const float (&bias)[NE], float (&load)[NE],
+                         int* sh_counts, RouteWarp<NE>& sh) {
+  float l[NE], s[NE], sig_key[SIG ? NE : 1];
+  float top = -INFINITY, sum = 0.0f;
+  if constexpr (SIG) {
+    route_logits<NE, BF16>(raw, dead_bias, l);
+  } else {
+    // NaN becomes -inf here; the other ways out of reach show in tau and the maximum
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      l[i] = fmaxf(raw.value(i), -INFINITY);
+      top = fmaxf(top, l[i]);
+    }
+  }
+  if (next < (int)a.T) raw.load(a, next, lane);
+  if constexpr (SIG) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      // l = -inf: expf gives inf and the score is 0
+      s[i] = __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l[i])));
+      sum = __fadd_rn(sum, s[i]);
+      sig_key[i] = l[i] > -INFINITY ? __fadd_rn(s[i], bias[i]) : -INFINITY;
+      top = fmaxf(top, sig_key[i]);
+    }
+  }
+  float (&key)[NE] = [&]() -> float (&)[NE] {
+    if constexpr (SIG) return sig_key; else return l;
+  }();
+  uint32_t o = ordered_bits(top);
+  uint32_t tau = __reduce_max_sync(0xFFFFFFFFu, o);
+  float m = ordered_value(tau);
+#pragma unroll 4
+  for (int j = 1; j < a.k; ++j) {
+    if (o == tau) o = 0;
+    tau = __reduce_max_sync(0xFFFFFFFFu, o);
+  }
+  const float least = ordered_value(tau);               // tau = 0 (lanes ran out): NaN
+  bool quick = least > kDeadLogit && a.k <= 32;
+  float m2 = 0.0f;
+  if constexpr (!SIG) {
+    if (quick && fabsf(m) < 32768.0f) {
+      // exp(l - m) as 2^(l log2 e - m log2 e), the product exact within the
+      // FMA: the rounding of m log2 e is one factor, below 1.003, of all s
+      m2 = __fmul_rn(m, kLog2e);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) s[i] = exp2_ftz(__fmaf_rn(l[i], kLog2e, -m2));
+    } else {
+      quick = false;
+      RawLogits<NE, BF16> again;
+      again.load(a, t, lane);
+      route_logits<NE, BF16>(again, 0u, l);
+      m = fminf(fmaxf(m, -kLargest), kLargest);         // none in reach: exp(-inf) = 0
+#pragma unroll
+      for (int i = 0; i < NE; ++i) s[i] = exp_neg(__fsub_rn(l[i], m));
+    }
+#pragma unroll
+    for (int i = 0; i < NE; ++i) sum = __fadd_rn(sum, s[i]);
+  }
+  sum = warp_sum(sum);
+  const float share = on && sum > 0.0f ? rcp_ftz(sum) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) load[i] = __fmaf_rn(s[i], share, load[i]);
+  // a weight before normalisation is s times this
+  const float unit = SIG ? 1.0f : share;
+  if (quick) {
+    __syncwarp();                        // the previous token's candidates have been read
+    const uint32_t below_lane = (1u << lane) - 1u;
+    uint32_t mine = 0;                   // the lane's candidates by slot
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      sh.key[i * 32 + lane] = key[i];
+      if (key[i] >= least) mine |= 1u << i;
+    }
+    int n = 0;
+    for (uint32_t b = __ballot_sync(0xFFFFFFFFu, mine != 0); b && n <= 32;
+         b = __ballot_sync(0xFFFFFFFFu, mine != 0)) {
+      const int at = n + __popc(b & below_lane);
+      if (mine && at < 32) sh.slot[at] = (__ffs(mine) - 1) * 32 + lane;
+      mine &= mine - 1;
+      n += __popc(b);
+    }
+    if (n <= 32) {
+      __syncwarp();
+      // lane c has candidate c, in no particular order
+      const int slot = lane < n ? sh.slot[lane] : 0;
+      const float c = lane < n ? sh.key[slot] : -INFINITY;
+      const int e = expert_of<BF16>(slot >> 5, slot & 31);
+      sh.cand[lane] = c;
+      __syncwarp();
+      int place = 0;
+      for (int j = 0; j < n; j += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(&sh.cand[j]);
+        place += (q.x > c ? 1 : 0) + (q.y > c ? 1 : 0) + (q.z > c ? 1 : 0) + (q.w > c ? 1 : 0);
+      }
+      bool chosen = lane < n && place < a.k;
+      // equal keys share a place: then k lanes do not hold the k places
+      const uint32_t held = __reduce_or_sync(0xFFFFFFFFu, chosen ? 1u << place : 0u);
+      if (__popc(held) != a.k || __popc(__ballot_sync(0xFFFFFFFFu, chosen)) != a.k) {
+        for (int j = 0; j < n; ++j) {
+          const int ej = __shfl_sync(0xFFFFFFFFu, e, j);
+          place += sh.cand[j] == c && ej < e ? 1 : 0;
+        }
+        chosen = lane < n && place < a.k;
+      }
+      float w = 0.0f;
+      if (chosen) {
+        if constexpr (SIG) {
+          float v;
+          if constexpr (BF16) v = bf16lo(static_cast<const uint16_t*>(a.logits)[t * a.ld + e]);
+          else v = static_cast<const float*>(a.logits)[t * a.ld + e];
+          w = __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-fminf(v, kLargest))));
+        } else {
+          w = exp2_ftz(__fmaf_rn(c, kLog2e, -m2));
+        }
+      }
+      float f = unit;
+      if (a.normalize) {
+        const float d = warp_sum(w);
+        f = d > 0.0f ? rcp_ftz(d) : 0.0f;
+      }
+      if (chosen) {
+        const int to = t * a.k + place;
+        a.ids[to] = e;
+        a.prob[to] = on ? __fmul_rn(__fmul_rn(w, f), a.scale) : 0.0f;
+        if (on) atomicAdd(&sh_counts[e], 1);
+      }
+      return;
+    }
+  }
+  if constexpr (!SIG) {
+    RawLogits<NE, BF16> again;
+    again.load(a, t, lane);
+    route_logits<NE, BF16>(again, 0u, l);
+  }
+  route_one_by_one<NE, BF16>(a, t, lane, key, s, unit, on, sh_counts);
+}
+
+// totals of expert e over all tokens -> counts and load; returns its part of the loss
+MPM_DEV float route_expert_totals(const RouteArgs& a, int e, float load, int c, float n) {
+  load = __fdiv_rn(load, n);
+  a.load[e] = load;
+  a.counts[e] = c;
+  return __fmul_rn((float)c, load);
+}
+MPM_DEV void route_totals(const RouteArgs& a, float loss, int n) {
+  const float nf = (float)(n > 0 ? n : 1);
+  *a.loss = __fdiv_rn(__fmul_rn(loss, (float)a.E), __fmul_rn((float)a.k, nf));
+  *a.n_tokens = n;
+}
+
+MPM_DEV uint32_t ld_cluster_u32(const void* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_to_rank(smem_u32(p), rank)) : "memory");
   return v;
 }
 
-// A token's logits: l[i] of expert 32 i + lane, -inf where it is out of reach
-// (past E, masked, or its bias masked); returns the lane's live bits
-template <int NE>
-MPM_DEV uint32_t route_load(const RouteArgs& a, long long t, int lane, float (&l)[NE]) {
-  uint32_t live = 0;
-#pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    const int e = i * 32 + lane;
-    float v = -INFINITY;
-    if (e < a.E) {
-      if (a.bf16) v = __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.logits)[t * a.ld + e] << 16);
-      else v = static_cast<const float*>(a.logits)[t * a.ld + e];
-      if (v > kDeadLogit && (!a.bias || a.bias[e] > kDeadLogit)) live |= 1u << i;
-      v = fminf(v, kLargest);
-    }
-    l[i] = (live >> i & 1u) ? v : -INFINITY;
-  }
-  return live;
-}
-
-// scores s[i] (0 where dead) of a token from its logits, and their sum
-template <int NE>
-MPM_DEV float route_scores(const RouteArgs& a, const float (&l)[NE], uint32_t live, float (&s)[NE]) {
-  float sum = 0.0f;
-  if (a.sigmoid) {
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      s[i] = (live >> i & 1u) ? __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l[i]))) : 0.0f;
-      sum = __fadd_rn(sum, s[i]);
-    }
-    return warp_sum(sum);
-  }
-  float m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < NE; ++i) m = fmaxf(m, l[i]);
-  m = warp_max(m);
-#pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    s[i] = (live >> i & 1u) ? expf(__fsub_rn(l[i], m)) : 0.0f;
-    sum = __fadd_rn(sum, s[i]);
-  }
-  sum = warp_sum(sum);
-  const float d = sum > 0.0f ? sum : 1.0f;
-#pragma unroll
-  for (int i = 0; i < NE; ++i) s[i] = __fdiv_rn(s[i], d);
-  return sum > 0.0f ? 1.0f : 0.0f;
-}
-
-template <int NE>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs a) {
-  extern __shared__ uint8_t route_smem[];
-  float* sh_load = reinterpret_cast<float*>(route_smem);             // [warps][E]
-  int* sh_counts = reinterpret_cast<int*>(sh_load + kRouteWarps * a.E);   // [E]
-  __shared__ int sh_n;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Shared memory: the block's loads [E] and counts [E], then a region that
+// holds the warps' keys and candidates during the token loop and their lanes' loads
+// [warps][E] after it
+template <int NE, bool SIG, bool BF16>
+__global__ void __launch_bounds__(32 * route_warps(NE)) route_kernel(const RouteArgs a) {
+  extern __shared__ __align__(16) uint8_t route_smem[];
+  float* sh_load = reinterpret_cast<float*>(route_smem);
+  int* sh_counts = reinterpret_cast<int*>(sh_load + a.E);
+  uint8_t* region = route_smem + (size_t)(2 * a.E + 3) / 4 * 16;
+  float* sh_part = reinterpret_cast<float*>(region);
+  __shared__ int sh_n[32];
+  __shared__ float sh_loss;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, W = blockDim.x >> 5;
+  RouteWarp<NE>& sh = reinterpret_cast<RouteWarp<NE>*>(region)[warp];
+  const int step = gridDim.x * W, T = (int)a.T;         // T k <= 2^30
+  int t = blockIdx.x * W + warp;
+  RawLogits<NE, BF16> raw;
+  if (t < T) raw.load(a, t, lane);
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) sh_counts[e] = 0;
-  if (threadIdx.x == 0) sh_n = 0;
-  __syncthreads();
-  float load[NE];
+  float load[NE], bias[NE];
 #pragma unroll
   for (int i = 0; i < NE; ++i) load[i] = 0.0f;
-  int n = 0;
-  for (long long t = (long long)blockIdx.x * kRouteWarps + warp; t < a.T;
-       t += (long long)gridDim.x * kRouteWarps) {
-    float l[NE], s[NE];
-    const uint32_t live = route_load<NE>(a, t, lane, l);
-    const float sum = route_scores<NE>(a, l, live, s);
-    const bool on = !a.mask || a.mask[t] != 0;
-    if (on) {
-      ++n;
-      const float d = sum > 0.0f ? sum : 1.0f;
-#pragma unroll
-      for (int i = 0; i < NE; ++i) load[i] = __fadd_rn(load[i], a.sigmoid ? __fdiv_rn(s[i], d) : s[i]);
-    }
-    uint32_t key[NE];                      // 0: past E or chosen; 1: dead
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int e = i * 32 + lane;
-      float v = l[i];
-      if (a.sigmoid) v = (e < a.E && a.bias) ? __fadd_rn(s[i], a.bias[e]) : s[i];
-      key[i] = e >= a.E ? 0u : ((live >> i & 1u) ? ordered_bits(v) : 1u);
-    }
-    float w0 = 0.0f, w1 = 0.0f, wsum = 0.0f;    // lane j: weights of choices j and 32 + j
-    for (int j = 0; j < a.k; ++j) {
-      uint32_t best = 0;
-#pragma unroll
-      for (int i = 0; i < NE; ++i) best = max(best, key[i]);
-      best = __reduce_max_sync(0xFFFFFFFFu, best);
-      int at = 0x7FFFFFFF;
-#pragma unroll
-      for (int i = NE - 1; i >= 0; --i)
-        if (key[i] == best) at = i * 32 + lane;
-      at = __reduce_min_sync(0xFFFFFFFFu, at);
-      float w = 0.0f;
-#pragma unroll
-      for (int i = 0; i < NE; ++i)
-        if (i * 32 + lane == at) { key[i] = 0u; w = s[i]; }
-      w = __shfl_sync(0xFFFFFFFFu, w, at & 31);
-      wsum = __fadd_rn(wsum, w);
-      if ((j & 31) == lane) { if (j < 32) w0 = w; else w1 = w; }
-      if (lane == 0) {
-        a.ids[t * a.k + j] = at;
-        if (on && best > 1u) atomicAdd(&sh_counts[at], 1);
-      }
-    }
-    const float d = a.normalize && wsum > 0.0f ? wsum : 1.0f;
-    if (lane < a.k) a.prob[t * a.k + lane] = on ? __fmul_rn(__fdiv_rn(w0, d), a.scale) : 0.0f;
-    if (lane + 32 < a.k) a.prob[t * a.k + 32 + lane] = on ? __fmul_rn(__fdiv_rn(w1, d), a.scale) : 0.0f;
-  }
-#pragma unroll
-  for (int i = 0; i < NE; ++i)
-    if (i * 32 + lane < a.E) sh_load[warp * a.E + i * 32 + lane] = load[i];
-  if (lane == 0 && n) atomicAdd(&sh_n, n);
+  const uint32_t dead_bias = SIG ? route_bias<NE, BF16>(a, lane, bias) : 0u;
   __syncthreads();
+  int n = 0;
+  while (t < T) {
+    const bool on = !a.mask || a.mask[t] != 0;
+    const int next = t + step;
+    route_token<NE, SIG, BF16>(a, t, next, lane, raw, on, dead_bias, bias, load, sh_counts, sh);
+    n += on ? 1 : 0;
+    t = next;
+  }
+  if (!a.cluster) pdl_launch_dependents();
+  if (lane == 0) sh_n[warp] = n;
+  __syncthreads();                       // the region is free
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int e = expert_of<BF16>(i, lane);
+    if (e < a.E) sh_part[warp * a.E + e] = load[i];
+  }
+  __syncthreads();
+  n = __reduce_add_sync(0xFFFFFFFFu, lane < W ? sh_n[lane] : 0);
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
     float v = 0.0f;
-    for (int w = 0; w < kRouteWarps; ++w) v = __fadd_rn(v, sh_load[w * a.E + e]);
-    a.ws_load[(long long)blockIdx.x * a.E + e] = v;
-    a.ws_counts[(long long)blockIdx.x * a.E + e] = sh_counts[e];
+#pragma unroll 8
+    for (int w = 0; w < W; ++w) v = __fadd_rn(v, sh_part[w * a.E + e]);
+    if (a.cluster) {
+      sh_load[e] = v;
+    } else {
+      a.ws_load[(long long)blockIdx.x * a.E + e] = v;
+      a.ws_counts[(long long)blockIdx.x * a.E + e] = sh_counts[e];
+    }
   }
-  if (threadIdx.x == 0) a.ws_n[blockIdx.x] = sh_n;
+  if (!a.cluster) {
+    if (threadIdx.x == 0) a.ws_n[blockIdx.x] = n;
+    return;
+  }
+  // one cluster of 8 blocks holds every token: block r adds up the experts e = r mod 8
+  __syncthreads();                       // sh_n read by every thread
+  if (threadIdx.x == 0) sh_n[0] = n;
+  const uint32_t rank = cluster_ctarank();
+  cluster_sync();
+  int nc[kClusterCtas];
+#pragma unroll
+  for (int c = 0; c < kClusterCtas; ++c) nc[c] = (int)ld_cluster_u32(&sh_n[0], c);
+  float loss = 0.0f;
+  for (int e = threadIdx.x * kClusterCtas + rank; e < a.E; e += blockDim.x * kClusterCtas) {
+    uint32_t lc[kClusterCtas], cc[kClusterCtas];
+#pragma unroll
+    for (int c = 0; c < kClusterCtas; ++c) {
+      lc[c] = ld_cluster_u32(&sh_load[e], c);
+      cc[c] = ld_cluster_u32(&sh_counts[e], c);
+    }
+    n = 0;
+    float v = 0.0f;
+    int k = 0;
+#pragma unroll
+    for (int c = 0; c < kClusterCtas; ++c) {
+      n += nc[c];
+      v = __fadd_rn(v, __uint_as_float(lc[c]));
+      k += (int)cc[c];
+    }
+    loss = __fadd_rn(loss, route_expert_totals(a, e, v, k, (float)(n > 0 ? n : 1)));
+  }
+  loss = warp_sum(loss);
+  if (lane == 0) sh_part[warp] = loss;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < W; ++w) loss = __fadd_rn(loss, sh_part[w]);
+    sh_loss = loss;
+  }
+  cluster_sync();
+  if (rank == 0 && warp == 0) {
+    n = 0;
+#pragma unroll
+    for (int c = 0; c < kClusterCtas; ++c) n += nc[c];
+    loss = warp_sum(lane < kClusterCtas ? __uint_as_float(ld_cluster_u32(&sh_loss, lane)) : 0.0f);
+    if (lane == 0) route_totals(a, loss, n);
+  }
+  cluster_sync();                        // no block leaves while its shared memory is read
 }
 
-// the partials summed in block order: counts, mean scores, tokens, loss
+// The blocks' partials summed: one cluster of 8 blocks, each taking every 8th
+// group of 32 experts, warp w the parts w, w + 32, ... of them
 __global__ void __launch_bounds__(1024) route_finish_kernel(const RouteArgs a, int parts) {
-  __shared__ float sh[32];
-  const int e = threadIdx.x;
+  __shared__ float sh_l[32][33];
+  __shared__ int sh_c[32][33];
+  __shared__ int sh_n[32];
+  __shared__ float sh_loss;
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
   int n = 0;
-  for (int i = 0; i < parts; ++i) n += a.ws_n[i];
-  const float nf = (float)(n > 0 ? n : 1);
-  float v = 0.0f;
-  if (e < a.E) {
-    float load = 0.0f;
+  for (int i = threadIdx.x; i < parts; i += blockDim.x) n += a.ws_n[i];
+  n = __reduce_add_sync(0xFFFFFFFFu, n);
+  if (lane == 0) sh_n[warp] = n;
+  float loss = 0.0f;
+  for (int e0 = (int)rank * 32; e0 < a.E; e0 += kClusterCtas * 32) {
+    const int e = e0 + lane;
+    float v = 0.0f;
     int c = 0;
-    for (int i = 0; i < parts; ++i) {
-      load = __fadd_rn(load, a.ws_load[(long long)i * a.E + e]);
-      c += a.ws_counts[(long long)i * a.E + e];
+    if (e < a.E) {
+#pragma unroll 5
+      for (int i = warp; i < parts; i += 32) {
+        v = __fadd_rn(v, a.ws_load[(long long)i * a.E + e]);
+        c += a.ws_counts[(long long)i * a.E + e];
+      }
     }
-    load = __fdiv_rn(load, nf);
-    a.load[e] = load;
-    a.counts[e] = c;
-    v = __fmul_rn((float)c, load);
+    sh_l[warp][lane] = v;
+    sh_c[warp][lane] = c;
+    __syncthreads();
+    // warp w: the 32 partial sums of expert e0 + w
+    v = warp_sum(sh_l[lane][warp]);
+    c = __reduce_add_sync(0xFFFFFFFFu, sh_c[lane][warp]);
+    n = __reduce_add_sync(0xFFFFFFFFu, sh_n[lane]);
+    if (lane == 0 && e0 + warp < a.E)
+      loss = __fadd_rn(loss, route_expert_totals(a, e0 + warp, v, c, (float)(n > 0 ? n : 1)));
+    __syncthreads();
   }
-  v = warp_sum(v);
-  if ((e & 31) == 0) sh[e >> 5] = v;
+  if (lane == 0) sh_l[0][warp] = loss;
   __syncthreads();
-  if (e == 0) {
-    float s = 0.0f;
-    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) s = __fadd_rn(s, sh[i]);
-    *a.loss = __fdiv_rn(__fmul_rn(s, (float)a.E), __fmul_rn((float)a.k, nf));
-    *a.n_tokens = n;
+  if (warp == 0) {
+    loss = warp_sum(sh_l[0][lane]);
+    n = __reduce_add_sync(0xFFFFFFFFu, sh_n[lane]);
+    if (lane == 0) sh_loss = loss;
   }
+  cluster_sync();
+  if (rank == 0 && threadIdx.x == 0) {
+    for (uint32_t c = 1; c < kClusterCtas; ++c)
+      loss = __fadd_rn(loss, __uint_as_float(ld_cluster_u32(&sh_loss, c)));
+    route_totals(a, loss, n);
+  }
+  cluster_sync();
 }
 
 // ---------------------------------------------------------------- backward
@@ -205,40 +494,47 @@ __global__ void __launch_bounds__(1024) route_finish_kernel(const RouteArgs a, i
 // Sigmoid: dl = s (1 - s) ds, where a share s / S passes (dP - sum share dP) / S
 // on to s.  A normalised weight q_j = s_j / W passes
 // (dprob_j - sum q dprob) scale / W on to s of choice j.
-template <int NE>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_bwd_kernel(const RouteArgs a) {
-  extern __shared__ uint8_t route_smem[];
+// Scores: softmax numerators over a common sum; sigmoid with z = exp(-|l|) as
+// 1 / (1 + z) or z / (1 + z), and s (1 - s) = z / (1 + z)^2, without
+// cancellation at either end.  The choices' scores are recomputed from their
+// logits (one lane each), and their ds join the others through shared memory.
+MPM_DEV float sigmoid_parts(float l, float& slope) {
+  const float z = exp_neg(-fabsf(l)), q = rcp_ftz(__fadd_rn(1.0f, z)), zq = __fmul_rn(z, q);
+  slope = __fmul_rn(zq, q);
+  return l >= 0.0f ? q : zq;
+}
+
+constexpr int kBwdWarps = 8;
+
+template <int NE, bool SIG, bool BF16>
+__global__ void __launch_bounds__(32 * kBwdWarps) route_bwd_kernel(const RouteArgs a) {
+  extern __shared__ __align__(16) uint8_t route_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* sh = reinterpret_cast<float*>(route_smem) + warp * 2 * a.E;   // the token's s, then ds
-  float* shd = sh + a.E;
-  float dp[NE];                                   // dP of the lane's experts
+  float* shd = reinterpret_cast<float*>(route_smem) + warp * (32 * NE);      // the token's ds
+  const int step = gridDim.x * kBwdWarps, T = (int)a.T;      // T k <= 2^30
+  int t = blockIdx.x * kBwdWarps + warp;
+  RawLogits<NE, BF16> raw;
+  if (t < T) raw.load(a, t, lane);
+  float dp[NE], bias[NE];                         // dP of the lane's experts
+  const uint32_t dead_bias = SIG ? route_bias<NE, BF16>(a, lane, bias) : 0u;
   {
     const int n = a.in_n ? *a.in_n : 0;
     const float nf = (float)(n > 0 ? n : 1);
-    const float c = (a.dloss && a.in_counts && n > 0)
+    const float c = (a.dloss && n > 0)
                         ? __fdiv_rn(__fmul_rn(*a.dloss, (float)a.E), __fmul_rn((float)a.k, __fmul_rn(nf, nf)))
                         : 0.0f;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      const int e = i * 32 + lane;
-      dp[i] = (e < a.E && a.in_counts) ? __fmul_rn(c, (float)a.in_counts[e]) : 0.0f;
+      const int e = expert_of<BF16>(i, lane);
+      dp[i] = (e < a.E && a.dloss) ? __fmul_rn(c, (float)a.in_counts[e]) : 0.0f;
     }
   }
-  for (long long t = (long long)blockIdx.x * kRouteWarps + warp; t < a.T;
-       t += (long long)gridDim.x * kRouteWarps) {
+  while (t < T) {
     const bool on = !a.mask || a.mask[t] != 0;
-    float l[NE], s[NE], dl[NE];
-    const uint32_t live = route_load<NE>(a, t, lane, l);
-    const float sum = route_scores<NE>(a, l, live, s);
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < NE; ++i)
-      if (i * 32 + lane < a.E) { sh[i * 32 + lane] = s[i]; shd[i * 32 + lane] = 0.0f; }
-    __syncwarp();
+    // the choices' logits and gradients: lane j has choices j and 32 + j
+    float cl[2] = {-INFINITY, -INFINITY}, d[2] = {0.0f, 0.0f};
+    int id[2] = {-1, -1};
     if (a.dprob) {
-      // lane j: choices j and 32 + j
-      float w[2] = {0.0f, 0.0f}, d[2] = {0.0f, 0.0f};
-      int id[2] = {-1, -1};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int j = c * 32 + lane;
@@ -246,108 +542,194 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_bwd_kernel(const Route
         const int e = a.in_ids[t * a.k + j];
         if (e < 0 || e >= a.E) { set_status(a.status, MPM_ERR_DEVICE_BOUNDS); continue; }
         id[c] = e;
-        w[c] = sh[e];
+        float v;
+        if constexpr (BF16) v = bf16lo(static_cast<const uint16_t*>(a.logits)[t * a.ld + e]);
+        else v = static_cast<const float*>(a.logits)[t * a.ld + e];
+        if (v > kDeadLogit && (!SIG || !a.bias || a.bias[e] > kDeadLogit)) cl[c] = fminf(v, kLargest);
         d[c] = __fmul_rn(a.dprob[t * a.k + j], a.scale);
       }
-      if (a.normalize) {
-        const float W = warp_sum(__fadd_rn(w[0], w[1]));
-        const float r = W > 0.0f ? __fdiv_rn(1.0f, W) : 1.0f;
-        const float dot = __fmul_rn(warp_sum(__fadd_rn(__fmul_rn(w[0], d[0]), __fmul_rn(w[1], d[1]))), r);
+    }
+    float l[NE], s[NE], dl[NE];
+    route_logits<NE, BF16>(raw, dead_bias, l);
+    const int next = t + step;
+    if (next < T) raw.load(a, next, lane);
+    float sum = 0.0f, m = l[0];
+    if constexpr (SIG) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) d[c] = __fmul_rn(__fsub_rn(d[c], dot), r);
+      for (int i = 0; i < NE; ++i) {
+        s[i] = sigmoid_parts(l[i], dl[i]);        // dl: the slope s (1 - s), for now
+        sum = __fadd_rn(sum, s[i]);
       }
+    } else {
+#pragma unroll
+      for (int i = 1; i < NE; ++i) m = fmaxf(m, l[i]);
+      m = fmaxf(warp_max(m), -kLargest);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        s[i] = exp_neg(__fsub_rn(l[i], m));
+        sum = __fadd_rn(sum, s[i]);
+      }
+    }
+    sum = warp_sum(sum);
+    const float r = sum > 0.0f ? rcp_ftz(sum) : 0.0f;                // shares: s r
+    float ds[NE];
+    if (a.dprob) {
+      if (a.normalize) {
+        float w[2], slope;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          w[c] = SIG ? sigmoid_parts(cl[c], slope) : __fmul_rn(exp_neg(__fsub_rn(cl[c], m)), r);
+        const float wsum = warp_sum(__fadd_rn(w[0], w[1]));
+        const float rw = wsum > 0.0f ? __fdiv_rn(1.0f, wsum) : 1.0f;
+        const float dot = __fmul_rn(warp_sum(__fmaf_rn(w[0], d[0], __fmul_rn(w[1], d[1]))), rw);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) d[c] = __fmul_rn(__fsub_rn(d[c], dot), rw);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < NE; ++i) shd[i * 32 + lane] = 0.0f;
+      __syncwarp();
 #pragma unroll
       for (int c = 0; c < 2; ++c)
         if (id[c] >= 0) shd[id[c]] = d[c];
       __syncwarp();
-    }
 #pragma unroll
-    for (int i = 0; i < NE; ++i) dl[i] = i * 32 + lane < a.E ? shd[i * 32 + lane] : 0.0f;
-    if (a.sigmoid) {
-      const float S = sum > 0.0f ? sum : 1.0f;
-      float dot = 0.0f;
+      for (int i = 0; i < NE; ++i) ds[i] = shd[expert_of<BF16>(i, lane)];
+    } else {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) ds[i] = 0.0f;
+    }
+    float dot = 0.0f;
+    if constexpr (SIG) {
 #pragma unroll
       for (int i = 0; i < NE; ++i) dot = __fmaf_rn(s[i], dp[i], dot);
-      dot = __fdiv_rn(warp_sum(dot), S);
+      dot = __fmul_rn(warp_sum(dot), r);
 #pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        const float ds = __fadd_rn(dl[i], __fdiv_rn(__fsub_rn(dp[i], dot), S));
-        // s (1 - s) = z / (1 + z)^2 with z = exp(-|l|): no cancellation at either end
-        const float z = expf(-fabsf(l[i]));
-        const float q = __fadd_rn(1.0f, z);
-        dl[i] = __fmul_rn(__fdiv_rn(z, __fmul_rn(q, q)), ds);
-      }
+      for (int i = 0; i < NE; ++i) dl[i] = __fmul_rn(dl[i], __fmaf_rn(__fsub_rn(dp[i], dot), r, ds[i]));
     } else {
-      float dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
-        dl[i] = __fadd_rn(dl[i], dp[i]);
-        dot = __fmaf_rn(s[i], dl[i], dot);
+        s[i] = __fmul_rn(s[i], r);
+        ds[i] = __fadd_rn(ds[i], dp[i]);
+        dot = __fmaf_rn(s[i], ds[i], dot);
       }
       dot = warp_sum(dot);
 #pragma unroll
-      for (int i = 0; i < NE; ++i) dl[i] = __fmul_rn(s[i], __fsub_rn(dl[i], dot));
+      for (int i = 0; i < NE; ++i) dl[i] = __fmul_rn(s[i], __fsub_rn(ds[i], dot));
     }
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int e = i * 32 + lane;
-      if (e >= a.E) continue;
-      const float v = (on && (live >> i & 1u)) ? dl[i] : 0.0f;
-      if (a.bf16) static_cast<__nv_bfloat16*>(a.dlogits)[t * a.ldd + e] = __float2bfloat16_rn(v);
-      else static_cast<float*>(a.dlogits)[t * a.ldd + e] = v;
+    for (int i = 0; i < NE; ++i) dl[i] = (on && l[i] > -INFINITY) ? dl[i] : 0.0f;
+    if constexpr (BF16) {
+      __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.dlogits) + t * a.ldd;
+#pragma unroll
+      for (int i = 0; i < NE; i += 2) {
+        const int e = expert_of<BF16>(i, lane);
+        if (a.vec) {
+          if (e < a.E) *reinterpret_cast<__nv_bfloat162*>(p + e) = __floats2bfloat162_rn(dl[i], dl[i + 1]);
+        } else {
+          if (e < a.E) p[e] = __float2bfloat16_rn(dl[i]);
+          if (e + 1 < a.E) p[e + 1] = __float2bfloat16_rn(dl[i + 1]);
+        }
+      }
+    } else {
+      float* p = static_cast<float*>(a.dlogits) + t * a.ldd + lane;
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+        if (i * 32 + lane < a.E) p[i * 32] = dl[i];
     }
+    t = next;
   }
 }
 
 // ---------------------------------------------------------------- launchers
-static int route_parts(long long T) {
-  const long long n = (T + kRouteWarps - 1) / kRouteWarps;
+static int route_ne(int E) {
+  int ne = 2;
+  while (ne * 32 < E) ne *= 2;
+  return ne;
+}
+static int route_parts(long long T, int E) {
+  const int w = route_warps(route_ne(E));
+  const long long n = (T + w - 1) / w;
   return (int)(n < kRouteMaxParts ? n : kRouteMaxParts);
 }
-size_t route_ws_bytes(long long T, int E) { return (size_t)route_parts(T) * (2 * (size_t)E + 1) * 4; }
+size_t route_ws_bytes(long long T, int E) {
+  return T <= kClusterTokens ? 0 : (size_t)route_parts(T, E) * (2 * (size_t)E + 1) * 4;
+}
+// bf16: whether rows can be read in pairs; fp32: whether every lane's slot is full
+static bool route_vec(const void* p, long long ld, int bf16, int E) {
+  if (!bf16) return E == 32 * route_ne(E);
+  return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld % 2 == 0 && E % 2 == 0;
+}
 
-#define MPM_ROUTE_DISPATCH(E, CALL)      \
-  do {                                   \
-    const int ne_ = ((E) + 31) / 32;     \
-    if (ne_ <= 1) { CALL(1); }           \
-    else if (ne_ <= 2) { CALL(2); }      \
-    else if (ne_ <= 4) { CALL(4); }      \
-    else if (ne_ <= 8) { CALL(8); }      \
-    else if (ne_ <= 16) { CALL(16); }    \
-    else { CALL(32); }                   \
-  } while (0)
+template <int NE, bool SIG, bool BF16>
+static cudaError_t route_forward(RouteArgs a, cudaStream_t st) {
+  const bool small = a.T <= kClusterTokens;
+  int W = route_warps(NE);
+  if (small && a.T < (long long)kClusterCtas * W) W = (int)((a.T + kClusterCtas - 1) / kClusterCtas);
+  const size_t smem = (size_t)(2 * a.E + 3) / 4 * 16 + W * sizeof(RouteWarp<NE>);   // holds [W][E] too
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.blockDim = dim3(32 * W);
+  cfg.dynamicSmemBytes = smem;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kClusterCtas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  if (small) {
+    cfg.gridDim = dim3(kClusterCtas);
+    cfg.numAttrs = 1;
+    a.cluster = 1;
+    return cudaLaunchKernelEx(&cfg, route_kernel<NE, SIG, BF16>, a);
+  }
+  const int parts = route_parts(a.T, a.E);
+  cfg.gridDim = dim3((unsigned)parts);
+  cfg.numAttrs = 0;
+  cudaError_t err = cudaLaunchKernelEx(&cfg, route_kernel<NE, SIG, BF16>, a);
+  if (err != cudaSuccess) return err;
+  cfg.gridDim = dim3(kClusterCtas);
+  cfg.blockDim = dim3(1024);
+  cfg.dynamicSmemBytes = 0;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, route_finish_kernel, a, parts);
+}
+
+template <int NE, bool SIG, bool BF16>
+static cudaError_t route_backward(RouteArgs a, cudaStream_t st) {
+  const long long n = (a.T + kBwdWarps - 1) / kBwdWarps, most = 152 * 6;
+  route_bwd_kernel<NE, SIG, BF16><<<(unsigned)(n < most ? n : most), 32 * kBwdWarps,
+                                    (size_t)kBwdWarps * 32 * NE * 4, st>>>(a);
+  return cudaGetLastError();
+}
+
+#define MPM_ROUTE_NE(CALL, NE)                                               \
+  return a.sigmoid ? (a.bf16 ? CALL<NE, true, true>(a, st) : CALL<NE, true, false>(a, st))     \
+                   : (a.bf16 ? CALL<NE, false, true>(a, st) : CALL<NE, false, false>(a, st))
+#define MPM_ROUTE_DISPATCH(CALL)        \
+  switch (route_ne(a.E)) {              \
+    case 2: MPM_ROUTE_NE(CALL, 2);      \
+    case 4: MPM_ROUTE_NE(CALL, 4);      \
+    case 8: MPM_ROUTE_NE(CALL, 8);      \
+    case 16: MPM_ROUTE_NE(CALL, 16);    \
+    default: MPM_ROUTE_NE(CALL, 32);    \
+  }
 
 cudaError_t launch_route(const RouteArgs& in, void* ws, cudaStream_t st) {
   RouteArgs a = in;
-  const int parts = route_parts(a.T);
+  const size_t parts = (size_t)route_parts(a.T, a.E);
   a.ws_load = static_cast<float*>(ws);
-  a.ws_counts = reinterpret_cast<int*>(a.ws_load + (size_t)parts * a.E);
-  a.ws_n = a.ws_counts + (size_t)parts * a.E;
-  const size_t smem = (size_t)(kRouteWarps + 1) * a.E * 4;
-#define MPM_CALL(NE) route_kernel<NE><<<parts, 32 * kRouteWarps, smem, st>>>(a)
-  MPM_ROUTE_DISPATCH(a.E, MPM_CALL);
-#undef MPM_CALL
-  cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
-  route_finish_kernel<<<1, (a.E + 31) / 32 * 32, 0, st>>>(a, parts);
-  return cudaGetLastError();
+  a.ws_counts = reinterpret_cast<int*>(a.ws_load + parts * a.E);
+  a.ws_n = a.ws_counts + parts * a.E;
+  a.vec = route_vec(a.logits, a.ld, a.bf16, a.E);
+  MPM_ROUTE_DISPATCH(route_forward)
 }
 
-cudaError_t launch_route_backward(const RouteArgs& a, cudaStream_t st) {
-  const int parts = route_parts(a.T);
-  const size_t smem = (size_t)kRouteWarps * 2 * a.E * 4;
-#define MPM_CALL(NE)                                                                              \
-  do {                                                                                            \
-    if (smem > 48 * 1024) {                                                                       \
-      cudaError_t e_ = cudaFuncSetAttribute(route_bwd_kernel<NE>,                                 \
-                                            cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); \
-      if (e_ != cudaSuccess) return e_;                                                           \
-    }                                                                                             \
-    route_bwd_kernel<NE><<<parts, 32 * kRouteWarps, smem, st>>>(a);                               \
-  } while (0)
-  MPM_ROUTE_DISPATCH(a.E, MPM_CALL);
-#undef MPM_CALL
-  return cudaGetLastError();
+cudaError_t launch_route_backward(const RouteArgs& in, cudaStream_t st) {
+  RouteArgs a = in;
+  a.vec = route_vec(a.logits, a.ld, a.bf16, a.E) && route_vec(a.dlogits, a.ldd, a.bf16, a.E);
+  MPM_ROUTE_DISPATCH(route_backward)
 }
 
 }  // namespace mpm

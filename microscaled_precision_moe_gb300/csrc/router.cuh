@@ -20,6 +20,7 @@ struct RouteArgs {
   const float* dprob; const float* dloss;  // [T, k], [1] (nullable)
   void* dlogits; long long ldd;
   int* status;
+  int vec, cluster;                        // set by the launchers: aligned rows; one cluster
 };
 size_t route_ws_bytes(long long T, int E);
 cudaError_t launch_route(const RouteArgs& a, void* ws, cudaStream_t st);

@@ -150,13 +150,13 @@ def test_router_refusals(lib):
         return lib.mpm_moe_route(l, dt, T, E, ld, k, sc, nm, scale, bias, None, ids, P, P, P, P, loss, ws,
                                  wsb, None)
 
-    assert f(l=None) == NULL and f(ids=None) == NULL and f(loss=None) == NULL and f(ws=None) == NULL
+    assert f(l=None) == NULL and f(ids=None) == NULL and f(loss=None) == NULL
     assert f(dt=2) == UNSUP and f(sc=2) == UNSUP and f(bias=P, sc=0) == UNSUP
     assert f(T=0) == SHAPE and f(E=0, ld=16) == SHAPE and f(E=1025, ld=1025) == SHAPE
     assert f(k=0) == SHAPE and f(k=17) == SHAPE and f(E=128, ld=128, k=65) == SHAPE
     assert f(ld=15) == SHAPE and f(T=(1 << 30)) == SHAPE and f(scale=float("nan")) == SHAPE
-    need = lib.mpm_moe_route_workspace_bytes(4, 16)
-    assert need > 0 and f(wsb=need - 1) == SHAPE
+    need = lib.mpm_moe_route_workspace_bytes(4096, 16)
+    assert need > 0 and f(T=4096, wsb=need - 1) == SHAPE and f(T=4096, ws=None) == NULL
     assert lib.mpm_moe_route_workspace_bytes(0, 16) == 0
     assert f(l=Q) == ALIGN and f(bias=Q, sc=1) == ALIGN and f(ws=Q) == ALIGN
 
