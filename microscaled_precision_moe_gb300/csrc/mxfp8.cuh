@@ -38,4 +38,15 @@ MPM_DEV int mx_exponent(uint32_t bits) {
 
 MPM_DEV float pow2_neg(int e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
 
+// max |x| over bf16 pairs with packed bf16 abs / max (finite inputs), as the
+// 16-bit pattern of the larger magnitude in the low half
+template <int N>
+MPM_DEV uint32_t absmax_bf16x2_packed(const uint32_t (&w)[N]) {
+  __nv_bfloat162 acc = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
+#pragma unroll
+  for (int j = 1; j < N; ++j) acc = __hmax2(acc, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[j])));
+  const uint32_t m = *reinterpret_cast<uint32_t*>(&acc);
+  return max(m & 0xFFFFu, m >> 16);
+}
+
 }  // namespace mpm

@@ -10,40 +10,52 @@
 // quantises the stored y then run on the same operands.
 //
 // A row is held in the registers of the threads of one block (VEC consecutive
-// elements per load, IT loads per thread), so every operand is read once.
+// elements per load, IT loads per thread and operand), R rows at a time with all
+// their loads in flight together, so every operand is read once.
 #include "norm.cuh"
+#include "launch.cuh"
 #include "mxfp8.cuh"
 
 namespace mpm {
 
 constexpr int kNormMaxThreads = 512;
+constexpr int kNormMaxWarps = kNormMaxThreads / 32;
+constexpr int kRowsAtATime = 4;          // rows of up to 8 values a thread
+constexpr int kBwdThreads = 512;         // of the backward on each SM
 
-MPM_DEV float bf16_f(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-MPM_DEV uint16_t f_bf16(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+MPM_DEV uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
 
+// VEC consecutive bf16 as loaded: pairs, or one in the low half
 template <int VEC>
-MPM_DEV void load_bf16(const uint16_t* p, float (&v)[VEC]) {
-  if constexpr (VEC == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) { v[2 * j] = bf16lo(w[j]); v[2 * j + 1] = bf16hi(w[j]); }
-  } else {
-    v[0] = bf16_f(*p);
+struct RawBf16 {
+  static constexpr int W = (VEC + 1) / 2;
+  uint32_t w[W];
+  MPM_DEV void load(const uint16_t* p) {
+    if constexpr (VEC == 8) {
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+    } else {
+      w[0] = *p;
+    }
   }
-}
-template <int VEC>
-MPM_DEV void store_bf16(uint16_t* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 8) {
-    uint32_t w[4];
+  MPM_DEV void zero() {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = (uint32_t)f_bf16(v[2 * j]) | ((uint32_t)f_bf16(v[2 * j + 1]) << 16);
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-    *p = f_bf16(v[0]);
+    for (int j = 0; j < W; ++j) w[j] = 0;
   }
-}
+  MPM_DEV float value(int j) const { return (j & 1) ? bf16hi(w[j / 2]) : bf16lo(w[j / 2]); }
+  MPM_DEV void set(const float (&v)[VEC]) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j] = pack_bf16(v[2 * j], 2 * j + 1 < VEC ? v[2 * j + 1] : 0.0f);
+  }
+  MPM_DEV void store(uint16_t* p) const {
+    if constexpr (VEC == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *p = (uint16_t)w[0];
+  }
+};
+
 template <int VEC>
 MPM_DEV void load_weight(const void* w, int f32, int k, float (&v)[VEC]) {
   if (f32) {
@@ -56,177 +68,250 @@ MPM_DEV void load_weight(const void* w, int f32, int k, float (&v)[VEC]) {
       v[0] = *p;
     }
   } else {
-    load_bf16<VEC>(static_cast<const uint16_t*>(w) + k, v);
+    RawBf16<VEC> r;
+    r.load(static_cast<const uint16_t*>(w) + k);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) v[j] = r.value(j);
   }
 }
 
-// sum over the block's threads, in a fixed order; every thread gets it
-MPM_DEV float block_sum(float v, float* sh) {
+// R sums over the block's threads, in a fixed order; every thread gets them.
+// sh: the caller alternates between two, so one barrier a call suffices.
+template <int R>
+MPM_DEV void block_sums(float (&v)[R], float (*sh)[kNormMaxWarps]) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  const int nw = blockDim.x >> 5;
-  __syncthreads();                       // sh free (an earlier call's reads are over)
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v[r] = __fadd_rn(v[r], __shfl_xor_sync(0xFFFFFFFFu, v[r], o));
+  const int nw = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (nw == 1) return;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (lane == 0) sh[r][warp] = v[r];
   __syncthreads();
-  float t = 0.0f;
-  for (int i = 0; i < nw; ++i) t = __fadd_rn(t, sh[i]);
-  return t;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    v[r] = 0.0f;
+    for (int i = 0; i < nw; ++i) v[r] = __fadd_rn(v[r], sh[r][i]);
+  }
 }
 
-template <int VEC, int IT>
+template <int VEC, int IT, int R>
 __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_kernel(const NormFwd p) {
-  __shared__ float sh[kNormMaxThreads / 32];
-  const long long row = blockIdx.x;
+  __shared__ float sh[R][kNormMaxWarps];
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long row0 = (long long)blockIdx.x * R;
   const int t = threadIdx.x, nt = blockDim.x;
-  const int nblk = p.K >> 5;
-  if (row >= p.M) {                      // padding rows of the last scale tile
-    for (int c = t; c < (int)p.s_cols_pad; c += nt) p.s[sf_offset(row, c, p.s_cols_pad)] = 0;
-    return;
-  }
-  float h[IT][VEC];
-  float ss = 0.0f;
+  RawBf16<VEC> x[R][IT], res[R][IT];
 #pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const int k = (i * nt + t) * VEC;
-    if (k < p.K) {
-      load_bf16<VEC>(p.x + row * p.ldx + k, h[i]);
-      if (p.r) {
-        float r[VEC];
-        load_bf16<VEC>(p.r + row * p.ldr + k, r);
+  for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) h[i][j] = __fadd_rn(h[i][j], r[j]);
+    for (int i = 0; i < IT; ++i) {
+      const int k = (i * nt + t) * VEC;
+      x[r][i].zero();
+      res[r][i].zero();
+      if (k < p.K && row0 + r < p.M) {
+        x[r][i].load(p.x + (row0 + r) * p.ldx + k);
+        if (p.r) res[r][i].load(p.r + (row0 + r) * p.ldr + k);
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) h[i][j] = 0.0f;
     }
+  float h[R][IT][VEC], ss[R];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) ss = __fmaf_rn(h[i][j], h[i][j], ss);
+  for (int r = 0; r < R; ++r) {
+    ss[r] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        // x + 0 is x: no branch on whether there is a residual
+        h[r][i][j] = __fadd_rn(x[r][i].value(j), res[r][i].value(j));
+        ss[r] = __fmaf_rn(h[r][i][j], h[r][i][j], ss[r]);
+      }
   }
-  ss = block_sum(ss, sh);
-  const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)p.K), p.eps));
-  if (t == 0 && p.rstd) p.rstd[row] = rstd;
+  block_sums<R>(ss, sh);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    ss[r] = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss[r], (float)p.K), p.eps));
+    if (t == 0 && p.rstd && row0 + r < p.M) p.rstd[row0 + r] = ss[r];
+  }
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     const int k = (i * nt + t) * VEC;
     const bool in = k < p.K;
-    float y[VEC];
-    if (in) {
-      if (p.h) store_bf16<VEC>(p.h + row * p.ldh + k, h[i]);
-      load_weight<VEC>(p.w, p.w_f32, k, y);
+    float w[VEC];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) y[j] = __fmul_rn(__fmul_rn(h[i][j], rstd), y[j]);
-      if (p.y) store_bf16<VEC>(p.y + row * p.ldy + k, y);
-    } else {
+    for (int j = 0; j < VEC; ++j) w[j] = 0.0f;
+    if (in) load_weight<VEC>(p.w, p.w_f32, k, w);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) y[j] = 0.0f;
-    }
-    if (p.q) {
-      // K % 32 == 0: a block of 32 lies in 32 / VEC neighbouring lanes
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) m = max(m, (uint32_t)f_bf16(y[j]) & 0x7FFFu);
-#pragma unroll
-      for (int o = 16 / VEC; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      const int e = mx_exponent(m << 16);
-      if (in) {
-        const uint64_t sc = f32x2_splat(pow2_neg(e));
-        uint8_t* dst = p.q + row * (long long)p.K + k;
-        if constexpr (VEC == 8) {
-          uint32_t c[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            c[j] = e4m3x2_scaled((uint32_t)f_bf16(y[2 * j]) | ((uint32_t)f_bf16(y[2 * j + 1]) << 16), sc);
-          *reinterpret_cast<uint2*>(dst) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-        } else {
-          *dst = (uint8_t)e4m3x2_scaled(f_bf16(y[0]), sc);
-        }
-        if (k % 32 == 0) p.s[sf_offset(row, k >> 5, p.s_cols_pad)] = (uint8_t)(e + 127);
+    for (int r = 0; r < R; ++r) {
+      const long long row = row0 + r;
+      const bool live = in && row < p.M;
+      RawBf16<VEC> o;
+      if (p.h && live) {
+        o.set(h[r][i]);
+        o.store(p.h + row * p.ldh + k);
       }
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) h[r][i][j] = __fmul_rn(__fmul_rn(h[r][i][j], ss[r]), w[j]);
+      o.set(h[r][i]);
+      if (p.y && live) o.store(p.y + row * p.ldy + k);
+      if (!p.q) continue;
+      // K % 32 == 0: a block of 32 lies in 32 / VEC neighbouring lanes
+      uint32_t m = VEC == 8 ? absmax_bf16x2_packed(o.w) : o.w[0] & 0x7FFFu;
+#pragma unroll
+      for (int d = 16 / VEC; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+      const int e = mx_exponent(m << 16);
+      if (!live) continue;
+      const uint64_t sc = f32x2_splat(pow2_neg(e));
+      uint8_t* dst = p.q + row * (long long)p.K + k;
+      if constexpr (VEC == 8) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(e4m3x2_scaled(o.w[0], sc) | (e4m3x2_scaled(o.w[1], sc) << 16),
+                                                    e4m3x2_scaled(o.w[2], sc) | (e4m3x2_scaled(o.w[3], sc) << 16));
+      } else {
+        *dst = (uint8_t)e4m3x2_scaled(o.w[0], sc);
+      }
+      if (k % 32 == 0) p.s[sf_offset(row, k >> 5, p.s_cols_pad)] = (uint8_t)(e + 127);
     }
   }
-  if (p.q && t < (int)p.s_cols_pad - nblk) p.s[sf_offset(row, nblk + t, p.s_cols_pad)] = 0;
+  if (!p.q) return;
+  // zero the padding of the scale tiles: past K, and rows past M
+  const int nblk = p.K >> 5;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    for (int c = (row0 + r < p.M ? nblk : 0) + t; c < (int)p.s_cols_pad; c += nt)
+      p.s[sf_offset(row0 + r, c, p.s_cols_pad)] = 0;
 }
 
 // ---------------------------------------------------------------- backward
 // With xh = h rstd and g = dy w:
 //   dx = rstd (g - xh mean_K(g xh)) + dh,   dw = sum over rows of dy xh.
-// Blocks walk the rows blockIdx.x, blockIdx.x + gridDim.x, ...; each keeps its
-// columns' share of dw in fp32 registers and writes it to its row of the
-// workspace, which a second kernel sums in row order (no atomics: the same
-// bytes every time).
-template <int VEC, int IT>
+// Blocks walk the groups of R rows blockIdx.x, blockIdx.x + gridDim.x, ...; each
+// keeps its columns' share of dw in fp32 registers and writes it to its row of
+// the workspace, which a second kernel sums in a fixed order (no atomics: the
+// same bytes every time).
+// WIDE rows (32 values a thread) would not fit in registers with all operands
+// and the weight: the gradients of y are added as they arrive, dh is loaded
+// after the reduction and the weight is read again for every row.
+template <int VEC, int IT, int R>
 __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_bwd_kernel(const NormBwd p) {
-  __shared__ float sh[kNormMaxThreads / 32];
+  constexpr bool WIDE = VEC * IT > 16 || IT > 4;
+  __shared__ float sh[2][R][kNormMaxWarps];
   const int t = threadIdx.x, nt = blockDim.x;
-  float dw[IT][VEC];
+  pdl_wait();
+  float dw[IT][VEC], w[WIDE ? 1 : IT][VEC];
 #pragma unroll
-  for (int i = 0; i < IT; ++i)
+  for (int i = 0; i < IT; ++i) {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) dw[i][j] = 0.0f;
-  for (long long row = blockIdx.x; row < p.M; row += gridDim.x) {
-    const float rstd = p.rstd[row];
-    float g[IT][VEC], xh[IT][VEC];
-    float c = 0.0f;
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
+    if constexpr (!WIDE) {
       const int k = (i * nt + t) * VEC;
-      if (k < p.K) {
-        load_bf16<VEC>(p.dy + row * p.lddy + k, g[i]);
-        if (p.dy2) {
-          float d[VEC];
-          load_bf16<VEC>(p.dy2 + row * p.lddy2 + k, d);
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) g[i][j] = __fadd_rn(g[i][j], d[j]);
-        }
-        load_bf16<VEC>(p.h + row * p.ldh + k, xh[i]);
-        float w[VEC];
-        load_weight<VEC>(p.w, p.w_f32, k, w);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          xh[i][j] = __fmul_rn(xh[i][j], rstd);
-          dw[i][j] = __fmaf_rn(g[i][j], xh[i][j], dw[i][j]);
-          g[i][j] = __fmul_rn(g[i][j], w[j]);
-          c = __fmaf_rn(g[i][j], xh[i][j], c);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) g[i][j] = xh[i][j] = 0.0f;
-      }
-    }
-    c = __fdiv_rn(block_sum(c, sh), (float)p.K);
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int k = (i * nt + t) * VEC;
-      if (k >= p.K) continue;
-      float d[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) d[j] = __fmul_rn(rstd, __fmaf_rn(-xh[i][j], c, g[i][j]));
-      if (p.dh) {
-        float v[VEC];
-        load_bf16<VEC>(p.dh + row * p.lddh + k, v);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) d[j] = __fadd_rn(d[j], v[j]);
-      }
-      store_bf16<VEC>(p.dx + row * p.lddx + k, d);
+      for (int j = 0; j < VEC; ++j) w[i][j] = 0.0f;
+      if (k < p.K) load_weight<VEC>(p.w, p.w_f32, k, w[i]);
     }
   }
+  int parity = 0;
+  for (long long row0 = (long long)blockIdx.x * R; row0 < p.M; row0 += (long long)gridDim.x * R, parity ^= 1) {
+    constexpr int ITR = WIDE ? 1 : IT;
+    RawBf16<VEC> dy[R][ITR], dy2[R][ITR], h[R][IT], dh[R][ITR];
+    float g[R][WIDE ? IT : 1][VEC];                 // WIDE: dy + dy2
+    float rstd[R], c[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long row = row0 + r;
+      rstd[r] = row < p.M ? p.rstd[row] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int k = (i * nt + t) * VEC, iw = WIDE ? 0 : i;
+        dy[r][iw].zero(); dy2[r][iw].zero(); h[r][i].zero(); dh[r][iw].zero();
+        if (k < p.K && row < p.M) {
+          dy[r][iw].load(p.dy + row * p.lddy + k);
+          h[r][i].load(p.h + row * p.ldh + k);
+          if (p.dy2) dy2[r][iw].load(p.dy2 + row * p.lddy2 + k);
+          if (!WIDE && p.dh) dh[r][iw].load(p.dh + row * p.lddh + k);
+        }
+        if constexpr (WIDE) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) g[r][i][j] = __fadd_rn(dy[r][0].value(j), dy2[r][0].value(j));
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      c[r] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int k = (i * nt + t) * VEC, iw = WIDE ? 0 : i;
+        if constexpr (WIDE) {
+          if (k < p.K) load_weight<VEC>(p.w, p.w_f32, k, w[0]);
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float y = WIDE ? g[r][WIDE ? i : 0][j] : __fadd_rn(dy[r][iw].value(j), dy2[r][iw].value(j));
+          const float gx = __fmul_rn(y, __fmul_rn(h[r][i].value(j), rstd[r]));
+          dw[i][j] = __fadd_rn(dw[i][j], gx);
+          if (!WIDE || k < p.K) c[r] = __fmaf_rn(gx, w[iw][j], c[r]);
+        }
+      }
+    }
+    block_sums<R>(c, sh[parity]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long row = row0 + r;
+      const float mean = __fdiv_rn(c[r], (float)p.K);
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int k = (i * nt + t) * VEC, iw = WIDE ? 0 : i;
+        if (k >= p.K || row >= p.M) continue;
+        if constexpr (WIDE) {
+          load_weight<VEC>(p.w, p.w_f32, k, w[0]);
+          dh[r][0].zero();
+          if (p.dh) dh[r][0].load(p.dh + row * p.lddh + k);
+        }
+        float d[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float y = WIDE ? g[r][WIDE ? i : 0][j] : __fadd_rn(dy[r][iw].value(j), dy2[r][iw].value(j));
+          const float xh = __fmul_rn(h[r][i].value(j), rstd[r]);
+          d[j] = __fmaf_rn(rstd[r], __fmaf_rn(-xh, mean, __fmul_rn(y, w[iw][j])), dh[r][iw].value(j));
+        }
+        RawBf16<VEC> o;
+        o.set(d);
+        o.store(p.dx + row * p.lddx + k);
+      }
+    }
+  }
+  pdl_launch_dependents();
   if (!p.dw) return;
+  float* out = gridDim.x == 1 ? p.dw : p.part + (long long)blockIdx.x * p.K;
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     const int k = (i * nt + t) * VEC;
     if (k >= p.K) continue;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) p.part[(long long)blockIdx.x * p.K + k + j] = dw[i][j];
+    for (int j = 0; j < VEC; ++j) out[k + j] = dw[i][j];
   }
 }
 
-__global__ void __launch_bounds__(256) rmsnorm_dw_kernel(const float* part, int parts, int K, float* dw) {
-  const int k = blockIdx.x * blockDim.x + threadIdx.x;
-  if (k >= K) return;
+// dw = the sum of the partials: 32 columns a block, warp w the parts w, w + 32, ...
+__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* part, int parts, int K, float* dw) {
+  __shared__ float sh[32][33];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int k = blockIdx.x * 32 + lane;
   float s = 0.0f;
-  for (int i = 0; i < parts; ++i) s = __fadd_rn(s, part[(long long)i * K + k]);
-  dw[k] = s;
+  if (k < K) {
+#pragma unroll 8
+    for (int i = warp; i < parts; i += 32) s = __fadd_rn(s, part[(long long)i * K + k]);
+  }
+  sh[warp][lane] = s;
+  __syncthreads();
+  s = sh[lane][warp];                    // warp w: the 32 partial sums of column w
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
+  if (lane == 0 && blockIdx.x * 32 + warp < K) dw[blockIdx.x * 32 + warp] = s;
 }
 
 // ---------------------------------------------------------------- launchers
@@ -238,39 +323,66 @@ static unsigned norm_threads(int K, int per_thread) {
   return (unsigned)((n + 31) / 32 * 32);
 }
 
-cudaError_t launch_add_rmsnorm(const NormFwd& p, cudaStream_t st) {
+template <int VEC, int IT, int R>
+static cudaError_t norm_fwd(const NormFwd& p, cudaStream_t st) {
   const long long rows = p.q ? (p.M + 127) / 128 * 128 : p.M;
-  const bool v = p.K % 8 == 0 && vec8(p.x, p.ldx) && vec8(p.r, p.ldr) && vec8(p.h, p.ldh) &&
-                 vec8(p.y, p.ldy) && vec8(p.w, 0);
-  const dim3 grid((unsigned)rows);
-  if (v) {
-    if (p.K <= 8 * kNormMaxThreads) add_rmsnorm_kernel<8, 1><<<grid, norm_threads(p.K, 8), 0, st>>>(p);
-    else add_rmsnorm_kernel<8, 4><<<grid, norm_threads(p.K, 32), 0, st>>>(p);
-  } else {
-    if (p.K <= 4 * kNormMaxThreads) add_rmsnorm_kernel<1, 4><<<grid, norm_threads(p.K, 4), 0, st>>>(p);
-    else add_rmsnorm_kernel<1, 32><<<grid, norm_threads(p.K, 32), 0, st>>>(p);
-  }
-  return cudaGetLastError();
+  return launch_serial(add_rmsnorm_kernel<VEC, IT, R>, dim3((unsigned)((rows + R - 1) / R)),
+                       dim3(norm_threads(p.K, VEC * IT)), 0, st, p);
 }
 
-// blocks of the backward: enough to fill 152 SMs, each with its own partial dw
-long long rmsnorm_backward_parts(long long M, int) { return M < 304 ? M : 304; }
+// Values a thread holds of a row of K (VEC * IT): few, so that many threads
+// share it, up to 512 of them
+static int norm_per_thread(int K, bool vec) {
+  if (vec) return K <= 8 * kNormMaxThreads ? 8 : (K <= 16 * kNormMaxThreads ? 16 : 32);
+  return K <= 4 * kNormMaxThreads ? 4 : (K <= 16 * kNormMaxThreads ? 16 : 32);
+}
+
+cudaError_t launch_add_rmsnorm(const NormFwd& p, cudaStream_t st) {
+  const bool v = p.K % 8 == 0 && vec8(p.x, p.ldx) && vec8(p.r, p.ldr) && vec8(p.h, p.ldh) &&
+                 vec8(p.y, p.ldy) && vec8(p.w, 0);
+  const int per = norm_per_thread(p.K, v);
+  if (v) {
+    if (per == 8) return p.M >= kRowsAtATime * 152 * 4 ? norm_fwd<8, 1, kRowsAtATime>(p, st) : norm_fwd<8, 1, 1>(p, st);
+    return per == 16 ? norm_fwd<8, 2, 1>(p, st) : norm_fwd<8, 4, 1>(p, st);
+  }
+  if (per == 4) return norm_fwd<1, 4, 1>(p, st);
+  return per == 16 ? norm_fwd<1, 16, 1>(p, st) : norm_fwd<1, 32, 1>(p, st);
+}
+
+// Blocks of the backward: kBwdThreads threads on each of 152 SMs
+static long long bwd_parts(long long M, int K, int per_thread) {
+  const int n = kBwdThreads / (int)norm_threads(K, per_thread);
+  const long long most = 152ll * (n < 1 ? 1 : n);
+  return M < most ? M : most;
+}
+long long rmsnorm_backward_parts(long long M, int K) {
+  const long long a = bwd_parts(M, K, norm_per_thread(K, true)), b = bwd_parts(M, K, norm_per_thread(K, false));
+  return a > b ? a : b;
+}
+
+template <int VEC, int IT, int R>
+static cudaError_t norm_bwd(const NormBwd& p, cudaStream_t st) {
+  long long parts = bwd_parts(p.M, p.K, VEC * IT);
+  if (parts > (p.M + R - 1) / R) parts = (p.M + R - 1) / R;
+  cudaError_t err = launch_serial(add_rmsnorm_bwd_kernel<VEC, IT, R>, dim3((unsigned)parts),
+                                  dim3(norm_threads(p.K, VEC * IT)), 0, st, p);
+  if (err != cudaSuccess || !p.dw || parts == 1) return err;
+  return launch_serial(rmsnorm_dw_kernel, dim3((unsigned)((p.K + 31) / 32)), dim3(1024), 0, st,
+                       (const float*)p.part, (int)parts, p.K, p.dw);
+}
 
 cudaError_t launch_add_rmsnorm_backward(const NormBwd& p, cudaStream_t st) {
   const bool v = p.K % 8 == 0 && vec8(p.dy, p.lddy) && vec8(p.dy2, p.lddy2) && vec8(p.h, p.ldh) &&
                  vec8(p.dh, p.lddh) && vec8(p.dx, p.lddx) && vec8(p.w, 0);
-  const int parts = (int)rmsnorm_backward_parts(p.M, p.K);
+  const int per = norm_per_thread(p.K, v);
   if (v) {
-    if (p.K <= 8 * kNormMaxThreads) add_rmsnorm_bwd_kernel<8, 1><<<parts, norm_threads(p.K, 8), 0, st>>>(p);
-    else add_rmsnorm_bwd_kernel<8, 4><<<parts, norm_threads(p.K, 32), 0, st>>>(p);
-  } else {
-    if (p.K <= 4 * kNormMaxThreads) add_rmsnorm_bwd_kernel<1, 4><<<parts, norm_threads(p.K, 4), 0, st>>>(p);
-    else add_rmsnorm_bwd_kernel<1, 32><<<parts, norm_threads(p.K, 32), 0, st>>>(p);
+    // kRowsAtATime rows at a time where every block gets some
+    if (per == 8)
+      return p.M >= kRowsAtATime * bwd_parts(p.M, p.K, 8) ? norm_bwd<8, 1, kRowsAtATime>(p, st) : norm_bwd<8, 1, 1>(p, st);
+    return per == 16 ? norm_bwd<8, 2, 1>(p, st) : norm_bwd<8, 4, 1>(p, st);
   }
-  cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess || !p.dw) return err;
-  rmsnorm_dw_kernel<<<(unsigned)((p.K + 255) / 256), 256, 0, st>>>(p.part, parts, p.K, p.dw);
-  return cudaGetLastError();
+  if (per == 4) return norm_bwd<1, 4, 1>(p, st);
+  return per == 16 ? norm_bwd<1, 16, 1>(p, st) : norm_bwd<1, 32, 1>(p, st);
 }
 
 }  // namespace mpm

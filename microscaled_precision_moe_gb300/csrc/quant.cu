@@ -558,17 +558,6 @@ MPM_DEV uint32_t div_by_magic(uint32_t n, uint32_t m, int s1, int s2) {
 MPM_DEV void zero_scale_padding(uint8_t* s, long long rows, long long cols, long long tid,
                                 long long nthreads);
 
-// max |x| over bf16 pairs with packed bf16 abs / max (finite inputs), as the
-// 16-bit pattern of the larger magnitude in the low half
-template <int N>
-MPM_DEV uint32_t absmax_bf16x2_packed(const uint32_t (&w)[N]) {
-  __nv_bfloat162 acc = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
-#pragma unroll
-  for (int j = 1; j < N; ++j) acc = __hmax2(acc, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[j])));
-  const uint32_t m = *reinterpret_cast<uint32_t*>(&acc);
-  return max(m & 0xFFFFu, m >> 16);
-}
-
 // ---------------------------------------------------------------- MXFP8, TMA-staged
 // Persistent CTAs walk 128 x 64 tiles of x; a 2-deep ring of TMA loads keeps
 // the next tiles in flight while a tile is encoded from shared memory (two
