@@ -416,6 +416,7 @@ mpm_status mpm_add_rmsnorm_backward(const void* dy, int64_t lddy, const void* dy
   p.dh = static_cast<const uint16_t*>(dh); p.lddh = lddh;
   p.dx = static_cast<uint16_t*>(dx); p.lddx = lddx;
   p.dw = dw; p.part = static_cast<float*>(ws);
+  p.status = status_ptr();
   p.M = M; p.K = (int)K;
   return cuda_status(mpm::launch_add_rmsnorm_backward(p, stream));
 }

@@ -21,7 +21,8 @@ namespace mpm {
 constexpr int kNormMaxThreads = 512;
 constexpr int kNormMaxWarps = kNormMaxThreads / 32;
 constexpr int kRowsAtATime = 4;          // rows of up to 8 values a thread
-constexpr int kBwdThreads = 512;         // of the backward on each SM
+constexpr int kBwdThreads = 512;         // of the backward on each SM (rows in registers)
+constexpr int kRingStages = 8;           // most stages of the backward's ring
 
 MPM_DEV uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -55,6 +56,20 @@ struct RawBf16 {
     else *p = (uint16_t)w[0];
   }
 };
+
+// two fp32 operations at once, each lane the IEEE result of the scalar one
+MPM_DEV uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+MPM_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// a pair of bf16 as two fp32
+MPM_DEV uint64_t widen2(uint32_t w) { return f32x2(bf16lo(w), bf16hi(w)); }
 
 template <int VEC>
 MPM_DEV void load_weight(const void* w, int f32, int k, float (&v)[VEC]) {
@@ -185,11 +200,139 @@ __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_kernel(const Norm
 
 // ---------------------------------------------------------------- backward
 // With xh = h rstd and g = dy w:
-//   dx = rstd (g - xh mean_K(g xh)) + dh,   dw = sum over rows of dy xh.
-// Blocks walk the groups of R rows blockIdx.x, blockIdx.x + gridDim.x, ...; each
-// keeps its columns' share of dw in fp32 registers and writes it to its row of
-// the workspace, which a second kernel sums in a fixed order (no atomics: the
-// same bytes every time).
+//   dx = rstd (g - xh mean_K(g xh)) + dh,   dw = sum over rows of dy xh,
+// computed from u = dy rstd as t = u w, c = sum_K t h,
+//   dx = t - h (rstd^2 c / K) + dh,         dw += u h.
+// Blocks walk rows blockIdx.x, blockIdx.x + gridDim.x, ... (or groups of R of
+// them); each keeps its columns' share of dw in fp32 registers and writes it to
+// its row of the workspace, which a second kernel sums in a fixed order (no
+// atomics: the same bytes every time).
+
+// Rows of 16-byte aligned operands stream through a ring of S stages in shared
+// memory, one row's operands each, by bulk copies that thread 0 issues: S - 1
+// rows are in flight whatever the threads are doing.  One thread per 8 columns.
+// A stage is refilled after the block barrier of the next row's reduction, by
+// when every thread is past its last read of it.
+template <bool TWO, bool RES>
+__global__ void __launch_bounds__(1024) add_rmsnorm_bwd_ring_kernel(const NormBwd p, int S) {
+  constexpr int NT = 2 + (TWO ? 1 : 0) + (RES ? 1 : 0);
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float sh[2][32];
+  __shared__ __align__(8) uint64_t bars[kRingStages];
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, nw = blockDim.x >> 5;
+  const uint32_t row_bytes = (uint32_t)p.K * 2, stage_bytes = NT * row_bytes;
+  const uint32_t base = smem_u32(ring), bar0 = smem_u32(bars);
+  const int k = t * 8;
+  const bool in = k < p.K;
+  if (t == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(bar0 + 8 * s, 1);
+    fence_mbar_init();
+    fence_proxy_async();
+  }
+  pdl_wait();
+  auto issue = [&](long long row, int s) {
+    const uint32_t dst = base + s * stage_bytes, bar = bar0 + 8 * s;
+    mbar_arrive_expect_tx(bar, stage_bytes);
+    bulk_load(dst, p.dy + row * p.lddy, row_bytes, bar);
+    bulk_load(dst + row_bytes, p.h + row * p.ldh, row_bytes, bar);
+    if (TWO) bulk_load(dst + 2 * row_bytes, p.dy2 + row * p.lddy2, row_bytes, bar);
+    if (RES) bulk_load(dst + (NT - 1) * row_bytes, p.dh + row * p.lddh, row_bytes, bar);
+  };
+  const long long step = gridDim.x;
+  if (t == 0) {
+    long long row = blockIdx.x;
+    for (int s = 0; s < S && row < p.M; ++s, row += step) issue(row, s);
+  }
+  uint64_t w[4], dw[4];
+  {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    if (in) load_weight<8>(p.w, p.w_f32, k, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) { w[j] = f32x2(v[2 * j], v[2 * j + 1]); dw[j] = 0; }
+  }
+  __syncthreads();
+  const float rk = __fdiv_rn(1.0f, (float)p.K);
+  int s = 0, it = 0;
+  uint32_t phase = 0;
+  long long row = blockIdx.x;
+  float rstd = row < p.M ? p.rstd[row] : 0.0f;
+  for (; row < p.M; row += step, ++it) {
+    const float next_rstd = row + step < p.M ? p.rstd[row + step] : 0.0f;
+    const bool ok = mbar_wait(bar0 + 8 * s, phase, p.status);
+    const uint8_t* st = ring + s * stage_bytes + t * 16;
+    RawBf16<8> a, b, h;
+    a.zero(); b.zero(); h.zero();
+    if (in) {
+      a.load(reinterpret_cast<const uint16_t*>(st));
+      h.load(reinterpret_cast<const uint16_t*>(st + row_bytes));
+      if (TWO) b.load(reinterpret_cast<const uint16_t*>(st + 2 * row_bytes));
+    }
+    uint64_t u[4], c2 = 0;
+    const uint64_t rstd2 = f32x2(rstd, rstd);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t y = TWO ? add2(widen2(a.w[j]), widen2(b.w[j])) : widen2(a.w[j]);
+      const uint64_t hh = widen2(h.w[j]), v = mul_f32x2(y, rstd2);
+      dw[j] = fma2(v, hh, dw[j]);
+      u[j] = mul_f32x2(v, w[j]);
+      c2 = fma2(u[j], hh, c2);
+    }
+    float c, chi;
+    f32x2_split(c2, c, chi);
+    c = __fadd_rn(c, chi);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) c = __fadd_rn(c, __shfl_xor_sync(0xFFFFFFFFu, c, o));
+    if (lane == 0) sh[it & 1][warp] = c;
+    if (__syncthreads_or(!ok)) {
+      // a copy did not arrive in time (reported): let the others land (bounded), no result
+      if (t == 0)
+        for (int j = it > 0 ? 1 : 0, i = s; j < S && row < p.M; ++j, row += step) {
+          mbar_wait(bar0 + 8 * i, phase, nullptr);
+          if (++i == S) { i = 0; phase ^= 1; }
+        }
+      return;
+    }
+    // the previous row's stage has been read by every thread
+    if (t == 0 && it > 0) {
+      const long long ahead = row + (long long)(S - 1) * step;
+      if (ahead < p.M) issue(ahead, s == 0 ? S - 1 : s - 1);
+    }
+    c = lane < nw ? sh[it & 1][lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) c = __fadd_rn(c, __shfl_xor_sync(0xFFFFFFFFu, c, o));
+    const float f = -__fmul_rn(__fmul_rn(rstd, rstd), __fmul_rn(c, rk));
+    if (in) {
+      RawBf16<8> r, o;
+      if (RES) r.load(reinterpret_cast<const uint16_t*>(st + (NT - 1) * row_bytes));
+      const uint64_t f2 = f32x2(f, f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint64_t d = fma2(widen2(h.w[j]), f2, u[j]);
+        if (RES) d = add2(d, widen2(r.w[j]));
+        float lo, hi;
+        f32x2_split(d, lo, hi);
+        o.w[j] = pack_bf16(lo, hi);
+      }
+      o.store(p.dx + row * p.lddx + k);
+    }
+    rstd = next_rstd;
+    if (++s == S) { s = 0; phase ^= 1; }
+  }
+  pdl_launch_dependents();
+  if (!p.dw || !in) return;
+  float* out = (gridDim.x == 1 ? p.dw : p.part + (long long)blockIdx.x * p.K) + k;
+  if (reinterpret_cast<uintptr_t>(out) % 16 == 0) {
+    reinterpret_cast<ulonglong2*>(out)[0] = make_ulonglong2(dw[0], dw[1]);
+    reinterpret_cast<ulonglong2*>(out)[1] = make_ulonglong2(dw[2], dw[3]);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f32x2_split(dw[j], out[2 * j], out[2 * j + 1]);
+}
+
+// The other forms hold R rows in registers, all their loads in flight together.
 // WIDE rows (32 values a thread) would not fit in registers with all operands
 // and the weight: the gradients of y are added as they arrive, dh is loaded
 // after the reduction and the weight is read again for every row.
@@ -249,9 +392,9 @@ __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_bwd_kernel(const 
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
           const float y = WIDE ? g[r][WIDE ? i : 0][j] : __fadd_rn(dy[r][iw].value(j), dy2[r][iw].value(j));
-          const float gx = __fmul_rn(y, __fmul_rn(h[r][i].value(j), rstd[r]));
-          dw[i][j] = __fadd_rn(dw[i][j], gx);
-          if (!WIDE || k < p.K) c[r] = __fmaf_rn(gx, w[iw][j], c[r]);
+          const float u = __fmul_rn(y, rstd[r]);
+          dw[i][j] = __fmaf_rn(u, h[r][i].value(j), dw[i][j]);
+          if (!WIDE || k < p.K) c[r] = __fmaf_rn(__fmul_rn(u, w[iw][j]), h[r][i].value(j), c[r]);
         }
       }
     }
@@ -259,7 +402,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_bwd_kernel(const 
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const long long row = row0 + r;
-      const float mean = __fdiv_rn(c[r], (float)p.K);
+      const float f = -__fmul_rn(__fmul_rn(rstd[r], rstd[r]), __fdiv_rn(c[r], (float)p.K));
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
         const int k = (i * nt + t) * VEC, iw = WIDE ? 0 : i;
@@ -273,8 +416,8 @@ __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_bwd_kernel(const 
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
           const float y = WIDE ? g[r][WIDE ? i : 0][j] : __fadd_rn(dy[r][iw].value(j), dy2[r][iw].value(j));
-          const float xh = __fmul_rn(h[r][i].value(j), rstd[r]);
-          d[j] = __fmaf_rn(rstd[r], __fmaf_rn(-xh, mean, __fmul_rn(y, w[iw][j])), dh[r][iw].value(j));
+          const float u = __fmul_rn(__fmul_rn(y, rstd[r]), w[iw][j]);
+          d[j] = __fadd_rn(__fmaf_rn(h[r][i].value(j), f, u), dh[r][iw].value(j));
         }
         RawBf16<VEC> o;
         o.set(d);
@@ -289,8 +432,15 @@ __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_bwd_kernel(const 
   for (int i = 0; i < IT; ++i) {
     const int k = (i * nt + t) * VEC;
     if (k >= p.K) continue;
+    if (VEC == 8 && reinterpret_cast<uintptr_t>(out) % 16 == 0) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) out[k + j] = dw[i][j];
+      for (int j = 0; j < VEC; j += 4)
+        *reinterpret_cast<float4*>(out + k + j) =
+            make_float4(dw[i][j], dw[i][(j + 1) % VEC], dw[i][(j + 2) % VEC], dw[i][(j + 3) % VEC]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) out[k + j] = dw[i][j];
+    }
   }
 }
 
@@ -349,15 +499,48 @@ cudaError_t launch_add_rmsnorm(const NormFwd& p, cudaStream_t st) {
   return per == 16 ? norm_fwd<1, 16, 1>(p, st) : norm_fwd<1, 32, 1>(p, st);
 }
 
-// Blocks of the backward: kBwdThreads threads on each of 152 SMs
+// The ring form: 16-byte aligned rows of 512 to 8192 elements, as many blocks an
+// SM as 1024 threads make, and the stages that fit beside one another.
+struct NormRing { int blocks, stages, smem; };
+static NormRing bwd_ring(int K, int operands) {
+  NormRing r{0, 0, 0};
+  if (K % 8 != 0 || K < 512 || K > 8192) return r;
+  r.blocks = 1024 / (int)norm_threads(K, 8);
+  const int row = 2 * K * operands;
+  r.stages = (222 * 1024 / r.blocks - 1024) / row;
+  if (r.stages > kRingStages) r.stages = kRingStages;
+  r.smem = r.stages * row;
+  return r;
+}
+
+// Blocks of the backward, each with its own partial dw
 static long long bwd_parts(long long M, int K, int per_thread) {
   const int n = kBwdThreads / (int)norm_threads(K, per_thread);
   const long long most = 152ll * (n < 1 ? 1 : n);
   return M < most ? M : most;
 }
 long long rmsnorm_backward_parts(long long M, int K) {
-  const long long a = bwd_parts(M, K, norm_per_thread(K, true)), b = bwd_parts(M, K, norm_per_thread(K, false));
-  return a > b ? a : b;
+  long long n = bwd_parts(M, K, norm_per_thread(K, true));
+  const long long b = bwd_parts(M, K, norm_per_thread(K, false)), c = 152ll * bwd_ring(K, 4).blocks;
+  if (b > n) n = b;
+  if (c > n) n = c;
+  return n < M ? n : M;
+}
+
+static cudaError_t norm_dw(const NormBwd& p, long long parts, cudaStream_t st) {
+  if (!p.dw || parts == 1) return cudaSuccess;
+  return launch_serial(rmsnorm_dw_kernel, dim3((unsigned)((p.K + 31) / 32)), dim3(1024), 0, st,
+                       (const float*)p.part, (int)parts, p.K, p.dw);
+}
+
+template <bool TWO, bool RES>
+static cudaError_t norm_bwd_ring(const NormBwd& p, const NormRing& r, cudaStream_t st) {
+  const auto kernel = add_rmsnorm_bwd_ring_kernel<TWO, RES>;
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, r.smem);
+  if (err != cudaSuccess) return err;
+  const long long parts = p.M < 152ll * r.blocks ? p.M : 152ll * r.blocks;
+  err = launch_serial(kernel, dim3((unsigned)parts), dim3(norm_threads(p.K, 8)), (size_t)r.smem, st, p, r.stages);
+  return err != cudaSuccess ? err : norm_dw(p, parts, st);
 }
 
 template <int VEC, int IT, int R>
@@ -366,9 +549,7 @@ static cudaError_t norm_bwd(const NormBwd& p, cudaStream_t st) {
   if (parts > (p.M + R - 1) / R) parts = (p.M + R - 1) / R;
   cudaError_t err = launch_serial(add_rmsnorm_bwd_kernel<VEC, IT, R>, dim3((unsigned)parts),
                                   dim3(norm_threads(p.K, VEC * IT)), 0, st, p);
-  if (err != cudaSuccess || !p.dw || parts == 1) return err;
-  return launch_serial(rmsnorm_dw_kernel, dim3((unsigned)((p.K + 31) / 32)), dim3(1024), 0, st,
-                       (const float*)p.part, (int)parts, p.K, p.dw);
+  return err != cudaSuccess ? err : norm_dw(p, parts, st);
 }
 
 cudaError_t launch_add_rmsnorm_backward(const NormBwd& p, cudaStream_t st) {
@@ -376,6 +557,11 @@ cudaError_t launch_add_rmsnorm_backward(const NormBwd& p, cudaStream_t st) {
                  vec8(p.dh, p.lddh) && vec8(p.dx, p.lddx) && vec8(p.w, 0);
   const int per = norm_per_thread(p.K, v);
   if (v) {
+    const NormRing r = bwd_ring(p.K, 2 + (p.dy2 != nullptr) + (p.dh != nullptr));
+    if (r.stages >= 3) {
+      if (p.dy2) return p.dh ? norm_bwd_ring<true, true>(p, r, st) : norm_bwd_ring<true, false>(p, r, st);
+      return p.dh ? norm_bwd_ring<false, true>(p, r, st) : norm_bwd_ring<false, false>(p, r, st);
+    }
     // kRowsAtATime rows at a time where every block gets some
     if (per == 8)
       return p.M >= kRowsAtATime * bwd_parts(p.M, p.K, 8) ? norm_bwd<8, 1, kRowsAtATime>(p, st) : norm_bwd<8, 1, 1>(p, st);

@@ -27,6 +27,7 @@ struct NormBwd {
   uint16_t* dx; long long lddx;
   float* dw;                               // fp32 [K] (nullable)
   float* part;                             // workspace [parts, K]
+  int* status;
   long long M; int K;
 };
 long long rmsnorm_backward_parts(long long M, int K);
