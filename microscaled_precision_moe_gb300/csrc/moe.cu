@@ -11,6 +11,7 @@
 // index t*k + j.  Every step is integer work, so results are bit-identical
 // run to run.
 #include "moe.cuh"
+#include "launch.cuh"
 
 namespace mpm {
 
@@ -389,51 +390,80 @@ __global__ void __launch_bounds__(256) gather_nvfp4_kernel(const uint4* __restri
   }
 }
 
-// MXFP8 rows: codes (K bytes) and 128x4-tiled E8M0 scales (K/32 columns) move
-// together.  One CTA per 128 destination rows (one row of scale tiles), as
-// gather_nvfp4_kernel.
+// MXFP8 rows: codes (K bytes) and 128x4-tiled E8M0 scales (K/32 columns).  Two
+// kinds of blocks, since a row's codes are one run and its scales one word in
+// each of K/128 tiles that it shares with 127 rows: the first code_blocks copy
+// 2 KB of the codes of 16 rows each (two rows a warp, all eight 16-byte loads of
+// a lane in flight together); the others write whole runs of up to 8 scale tiles
+// of 128 rows, one word (a row's four scales of a tile) per thread and tile.
+constexpr int kGatherRows = 16, kGatherTiles = 8, kGatherChunk = 128;   // 16-byte words
+
 __global__ void __launch_bounds__(256) gather_mxfp8_kernel(const uint4* __restrict__ src_q,
                                                           const uint8_t* __restrict__ src_s,
-                                                          long long T, long long K, int k,
+                                                          int T, long long K, int k,
                                                           const int* __restrict__ perm,
                                                           const int* __restrict__ seg_end,
-                                                          long long cap, uint4* __restrict__ dst_q,
+                                                          long long cap, long long code_blocks,
+                                                          uint4* __restrict__ dst_q,
                                                           uint8_t* __restrict__ dst_s, int* st) {
-  __shared__ long long tok[128];                  // source token of each row, -1 for padding
-  const long long rbase = (long long)blockIdx.x * 128;
-  long long rend = *seg_end;
-  if (rend > cap) rend = cap;
-  if (rbase >= rend) return;
-  const int nrows = (int)min(128LL, rend - rbase);
-  if (threadIdx.x < 128) {
-    long long t = -1;
-    if ((int)threadIdx.x < nrows) {
-      const int f = perm[rbase + threadIdx.x];
-      if (f >= 0) t = f / k;
-      if (t >= T) { set_status(st, MPM_ERR_DEVICE_BOUNDS); t = -1; }
-    }
-    tok[threadIdx.x] = t;
-  }
-  __syncthreads();
-  const long long q16 = K / 16;                  // uint4 chunks of codes per row
+  pdl_wait();
+  pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = warp; i < nrows; i += 8) {
-    uint4* d = dst_q + (rbase + i) * q16;
-    const long long t = tok[i];
-    for (long long c = lane; c < q16; c += 32)
-      d[c] = t < 0 ? make_uint4(0, 0, 0, 0) : __ldg(src_q + t * q16 + c);
+  if (blockIdx.x < code_blocks) {
+    const int q16 = (int)(K / 16);               // 16-byte words of codes per row
+    const unsigned row_blocks = (unsigned)((cap + kGatherRows - 1) / kGatherRows);
+    const unsigned chunk = blockIdx.x / row_blocks;
+    const long long r0 = (long long)(blockIdx.x - chunk * row_blocks) * kGatherRows + warp * 2;
+    const int c0 = (int)chunk * kGatherChunk + lane;
+    int f[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) f[i] = r0 + i < cap ? perm[r0 + i] : -1;
+    const long long rend = min((long long)*seg_end, cap);
+    uint4 v[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      int t = f[i] >= 0 ? f[i] / k : -1;
+      if (t >= T) {
+        if (lane == 0 && r0 + i < rend) set_status(st, MPM_ERR_DEVICE_BOUNDS);
+        t = -1;
+      }
+      const uint4* s = src_q + (long long)max(t, 0) * q16;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[i][j] = make_uint4(0, 0, 0, 0);
+        if (t >= 0 && c0 + 32 * j < q16) v[i][j] = __ldg(s + c0 + 32 * j);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint4* d = dst_q + (r0 + i) * q16;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (r0 + i < rend && c0 + 32 * j < q16) d[c0 + 32 * j] = v[i][j];
+    }
+    return;
   }
-  // scale tiles: word w of a tile holds row (w % 4) * 32 + w / 4
+  // word w of a tile holds row (w % 4) * 32 + w / 4
   const long long cpad = (K / 32 + 3) / 4 * 4, ntiles = cpad / 4;
-  const long long rt = rbase >> 7;
+  const long long groups = (ntiles + kGatherTiles - 1) / kGatherTiles;
+  const long long b = blockIdx.x - code_blocks, rt = b / groups, g0 = (b - rt * groups) * kGatherTiles;
   const int w = threadIdx.x & 127;
-  const int r = (w & 3) * 32 + (w >> 2);
-  if (r >= nrows) return;
-  const long long t = tok[r];
-  for (long long g = threadIdx.x >> 7; g < ntiles; g += 2) {
-    uint32_t v = 0;
-    if (t >= 0) v = *reinterpret_cast<const uint32_t*>(src_s + sf_offset(t, g * 4, cpad));
-    reinterpret_cast<uint32_t*>(dst_s + (rt * ntiles + g) * 512)[w] = v;
+  const long long row = rt * 128 + (w & 3) * 32 + (w >> 2);
+  const int f = row < cap ? perm[row] : -1;
+  if (row >= min((long long)*seg_end, cap)) return;
+  int t = f >= 0 ? f / k : -1;
+  if (t >= T) t = -1;                            // reported by the row's code block
+  uint32_t v[kGatherTiles / 2];
+#pragma unroll
+  for (int j = 0; j < kGatherTiles / 2; ++j) {
+    const long long g = g0 + (threadIdx.x >> 7) + 2 * j;
+    v[j] = 0;
+    if (t >= 0 && g < ntiles) v[j] = *reinterpret_cast<const uint32_t*>(src_s + sf_offset(t, g * 4, cpad));
+  }
+#pragma unroll
+  for (int j = 0; j < kGatherTiles / 2; ++j) {
+    const long long g = g0 + (threadIdx.x >> 7) + 2 * j;
+    if (g < ntiles) reinterpret_cast<uint32_t*>(dst_s + (rt * ntiles + g) * 512)[w] = v[j];
   }
 }
 
@@ -607,10 +637,14 @@ cudaError_t launch_combine(const void* y, const int* inv, long long T, int k, lo
 cudaError_t launch_gather_mxfp8(const uint8_t* q, const uint8_t* sc, long long T, long long K, int k,
                                 const int* perm, const int* seg_end, long long cap, uint8_t* dst_q,
                                 uint8_t* dst_s, int* status, cudaStream_t s) {
-  gather_mxfp8_kernel<<<(unsigned)((cap + 127) / 128), 256, 0, s>>>(
-      reinterpret_cast<const uint4*>(q), sc, T, K, k, perm, seg_end, cap,
-      reinterpret_cast<uint4*>(dst_q), dst_s, status);
-  return cudaGetLastError();
+  const long long chunks = (K / 16 + kGatherChunk - 1) / kGatherChunk;
+  const long long code_blocks = (cap + kGatherRows - 1) / kGatherRows * chunks;
+  const long long ntiles = (K / 32 + 3) / 4, groups = (ntiles + kGatherTiles - 1) / kGatherTiles;
+  const long long blocks = code_blocks + (cap + 127) / 128 * groups;
+  if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  return launch_serial(gather_mxfp8_kernel, dim3((unsigned)blocks), dim3(256), 0, s,
+                       reinterpret_cast<const uint4*>(q), sc, (int)T, K, k, perm, seg_end, cap,
+                       code_blocks, reinterpret_cast<uint4*>(dst_q), dst_s, status);
 }
 
 cudaError_t launch_combine_dprob(const void* dout, const void* y, const int* inv, const float* prob,
