@@ -491,7 +491,7 @@ mpm_status mpm_moe_route_backward(const void* logits_dev, int logits_dtype, int6
  * that y_perm is linear in it.  0 where inv_perm is negative or prob is 0; a
  * row index >= capacity sets MPM_ERR_DEVICE_BOUNDS and gives 0.  dout bf16
  * [T, H] and y_perm bf16 [capacity, H] dense, prob and dprob fp32 [T, k].
- * Requirements: T, k, capacity >= 1, T * k <= 2^30, H >= 8, H % 8 == 0,
+ * Requirements: T, k, capacity >= 1, T * k <= 2^30, 8 <= H <= 2^30, H % 8 == 0,
  * dout_dev and y_perm_dev 16-byte aligned.
  */
 mpm_status mpm_moe_combine_dprob(const void* dout_dev, const void* y_perm_dev,

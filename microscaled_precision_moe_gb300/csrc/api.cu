@@ -494,7 +494,8 @@ mpm_status mpm_moe_combine_dprob(const void* dout, const void* y, const int32_t*
                                  const float* prob, int64_t T, int k, int64_t H, int64_t cap,
                                  float* dprob, cudaStream_t stream) {
   if (!dout || !y || !inv || !prob || !dprob) return MPM_ERR_NULL;
-  if (T < 1 || k < 1 || T > (1ll << 30) / k || H < 8 || H % 8 != 0 || cap < 1) return MPM_ERR_SHAPE;
+  if (T < 1 || k < 1 || T > (1ll << 30) / k || H < 8 || H % 8 != 0 || H > (1ll << 30) || cap < 1)
+    return MPM_ERR_SHAPE;
   if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(inv, 4) || !aligned(prob, 4) ||
       !aligned(dprob, 4))
     return MPM_ERR_ALIGN;
