@@ -7,6 +7,7 @@ where every step runs in CUDA kernels.  Tensors must live on a CUDA device.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import torch
 
@@ -27,11 +28,12 @@ def _dp(t):
 def _mat(t, name, M, K):
     """Row pitch in elements of a bf16 [M, K] with dense rows (torch leaves the
     stride of a one-row matrix open)."""
-    if t.dtype is not _BF16 or t.shape != (M, K) or t.stride(1) != 1:
+    if t.dtype is not _BF16 or t.shape != (M, K):
         _check_rows(t, name)
-        if t.shape != (M, K):
-            raise ValueError(f"{name}: expected shape {(M, K)}, got {tuple(t.shape)}")
-    ld = t.stride(0)
+        raise ValueError(f"{name}: expected shape {(M, K)}, got {tuple(t.shape)}")
+    ld, one = t.stride()
+    if one != 1 and K != 1:
+        _check_rows(t, name)
     return ld if ld >= K or M > 1 else K
 
 
@@ -78,6 +80,7 @@ def _check_rows(x, name):
         raise ValueError(f"{name}: rows must be dense (stride(1) == 1)")
 
 
+@functools.lru_cache(maxsize=4096)
 def scale_bytes(rows: int, cols: int) -> int:
     return int(L.load().mpm_scale_bytes(rows, cols))
 
@@ -477,7 +480,7 @@ def add_rmsnorm(x, weight, residual=None, eps=1e-6, want_y=True, quantize=False,
     if quantize:
         if K % 32 != 0:
             raise ValueError(f"x: K = {K} is not a multiple of the 32-value MXFP8 block")
-        sb = lib.mpm_scale_bytes(M, K // 32)
+        sb = scale_bytes(M, K // 32)
         q, s = o.get("row_q"), o.get("row_s")
         if q is None:
             q = o["row_q"] = torch.empty(M, K, dtype=_U8, device=dev)
@@ -496,6 +499,7 @@ def add_rmsnorm(x, weight, residual=None, eps=1e-6, want_y=True, quantize=False,
     return o
 
 
+@functools.lru_cache(maxsize=4096)
 def add_rmsnorm_backward_workspace_bytes(M: int, K: int) -> int:
     return int(L.load().mpm_add_rmsnorm_backward_workspace_bytes(M, K))
 
@@ -530,7 +534,7 @@ def add_rmsnorm_backward(dy, h, rstd, weight, dy2=None, dh=None, want_dw=True, o
         else:
             dw = None
     if want_dw:
-        wsb = lib.mpm_add_rmsnorm_backward_workspace_bytes(M, K)
+        wsb = add_rmsnorm_backward_workspace_bytes(M, K)
         if ws is None:
             ws = torch.empty(wsb, dtype=_U8, device=dev)
         else:
@@ -578,6 +582,7 @@ def _route_args(logits, score, bias, token_mask):
     return T, E, ld if ld >= E or T > 1 else E, sc, L.DTYPE_F32 if dt is _F32 else L.DTYPE_BF16
 
 
+@functools.lru_cache(maxsize=4096)
 def moe_route_workspace_bytes(T: int, E: int) -> int:
     return int(L.load().mpm_moe_route_workspace_bytes(T, E))
 
@@ -612,7 +617,7 @@ def moe_route(logits, k: int, score="softmax", normalize=True, scale=1.0, bias=N
             _check(out[name], name, dt, contiguous=True, min_numel=n)
         ids, prob, counts, load, n_tokens, loss = (out[n] for n in ("ids", "prob", "counts", "load",
                                                                     "n_tokens", "loss"))
-    wsb = lib.mpm_moe_route_workspace_bytes(T, E)
+    wsb = moe_route_workspace_bytes(T, E)
     if ws is None:
         if wsb:
             ws = torch.empty(wsb, dtype=_U8, device=dev)
