@@ -30,6 +30,7 @@
 // Sums over tokens go through per-block partials added in a fixed order (no
 // floating-point atomics).
 #include "router.cuh"
+#include "launch.cuh"
 
 namespace mpm {
 
@@ -350,8 +351,10 @@ __global__ void __launch_bounds__(32 * route_warps(NE)) route_kernel(const Route
   const int step = gridDim.x * W, T = (int)a.T;         // T k <= 2^30
   int t = blockIdx.x * W + warp;
   RawLogits<NE, BF16> raw;
-  if (t < T) raw.load(a, t, lane);
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) sh_counts[e] = 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (t < T) raw.load(a, t, lane);
   float load[NE], bias[NE];
 #pragma unroll
   for (int i = 0; i < NE; ++i) load[i] = 0.0f;
@@ -365,7 +368,6 @@ __global__ void __launch_bounds__(32 * route_warps(NE)) route_kernel(const Route
     n += on ? 1 : 0;
     t = next;
   }
-  if (!a.cluster) pdl_launch_dependents();
   if (lane == 0) sh_n[warp] = n;
   __syncthreads();                       // the region is free
 #pragma unroll
@@ -443,6 +445,7 @@ __global__ void __launch_bounds__(1024) route_finish_kernel(const RouteArgs a, i
   __shared__ int sh_n[32];
   __shared__ float sh_loss;
   pdl_wait();
+  pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   int n = 0;
@@ -514,6 +517,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps) route_bwd_kernel(const RouteAr
   const int step = gridDim.x * kBwdWarps, T = (int)a.T;      // T k <= 2^30
   int t = blockIdx.x * kBwdWarps + warp;
   RawLogits<NE, BF16> raw;
+  pdl_wait();
+  pdl_launch_dependents();
   if (t < T) raw.load(a, t, lane);
   float dp[NE], bias[NE];                         // dP of the lane's experts
   const uint32_t dead_bias = SIG ? route_bias<NE, BF16>(a, lane, bias) : 0u;
@@ -673,25 +678,25 @@ static cudaError_t route_forward(RouteArgs a, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.blockDim = dim3(32 * W);
   cfg.dynamicSmemBytes = smem;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kClusterCtas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kClusterCtas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   if (small) {
     cfg.gridDim = dim3(kClusterCtas);
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     a.cluster = 1;
     return cudaLaunchKernelEx(&cfg, route_kernel<NE, SIG, BF16>, a);
   }
   const int parts = route_parts(a.T, a.E);
   cfg.gridDim = dim3((unsigned)parts);
-  cfg.numAttrs = 0;
+  cfg.numAttrs = 1;
   cudaError_t err = cudaLaunchKernelEx(&cfg, route_kernel<NE, SIG, BF16>, a);
   if (err != cudaSuccess) return err;
   cfg.gridDim = dim3(kClusterCtas);
   cfg.blockDim = dim3(1024);
   cfg.dynamicSmemBytes = 0;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, route_finish_kernel, a, parts);
 }
@@ -699,9 +704,8 @@ static cudaError_t route_forward(RouteArgs a, cudaStream_t st) {
 template <int NE, bool SIG, bool BF16>
 static cudaError_t route_backward(RouteArgs a, cudaStream_t st) {
   const long long n = (a.T + kBwdWarps - 1) / kBwdWarps, most = 152 * 6;
-  route_bwd_kernel<NE, SIG, BF16><<<(unsigned)(n < most ? n : most), 32 * kBwdWarps,
-                                    (size_t)kBwdWarps * 32 * NE * 4, st>>>(a);
-  return cudaGetLastError();
+  return launch_serial(route_bwd_kernel<NE, SIG, BF16>, dim3((unsigned)(n < most ? n : most)),
+                       dim3(32 * kBwdWarps), (size_t)kBwdWarps * 32 * NE * 4, st, a);
 }
 
 #define MPM_ROUTE_NE(CALL, NE)                                               \
