@@ -209,10 +209,19 @@ MPM_DEV void route_token(const RouteArgs& a, int t, int next, int lane, RawLogit
   uint32_t o = ordered_bits(top);
   uint32_t tau = __reduce_max_sync(0xFFFFFFFFu, o);
   float m = ordered_value(tau);
-#pragma unroll 4
-  for (int j = 1; j < a.k; ++j) {
-    if (o == tau) o = 0;
-    tau = __reduce_max_sync(0xFFFFFFFFu, o);
+  if (a.k <= 8) {                        // without branches: all of eight rounds, the k-th kept
+    uint32_t v = tau;
+#pragma unroll
+    for (int j = 1; j < 8; ++j) {
+      if (o == v) o = 0;
+      v = __reduce_max_sync(0xFFFFFFFFu, o);
+      if (j < a.k) tau = v;
+    }
+  } else {
+    for (int j = 1; j < a.k; ++j) {
+      if (o == tau) o = 0;
+      tau = __reduce_max_sync(0xFFFFFFFFu, o);
+    }
   }
   const float least = ordered_value(tau);               // tau = 0 (lanes ran out): NaN
   bool quick = least > kDeadLogit && a.k <= 32;
@@ -268,7 +277,9 @@ MPM_DEV void route_token(const RouteArgs& a, int t, int next, int lane, RawLogit
       sh.cand[lane] = c;
       __syncwarp();
       int place = 0;
-      for (int j = 0; j < n; j += 4) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        if (j == 16 && n <= 16) break;
         const float4 q = *reinterpret_cast<const float4*>(&sh.cand[j]);
         place += (q.x > c ? 1 : 0) + (q.y > c ? 1 : 0) + (q.z > c ? 1 : 0) + (q.w > c ? 1 : 0);
       }
