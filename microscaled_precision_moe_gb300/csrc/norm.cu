@@ -12,6 +12,7 @@
 // A row is held in the registers of the threads of one block (VEC consecutive
 // elements per load, IT loads per thread and operand), R rows at a time with all
 // their loads in flight together, so every operand is read once.
+#include <atomic>
 #include "norm.cuh"
 #include "launch.cuh"
 #include "mxfp8.cuh"
@@ -20,8 +21,8 @@ namespace mpm {
 
 constexpr int kNormMaxThreads = 512;
 constexpr int kNormMaxWarps = kNormMaxThreads / 32;
+constexpr int kNormTeams = 4;            // rows of one warp each in a block
 constexpr int kRowsAtATime = 4;          // rows of up to 8 values a thread
-constexpr int kBwdThreads = 512;         // of the backward on each SM (rows in registers)
 constexpr int kRingStages = 8;           // most stages of the backward's ring
 
 MPM_DEV uint32_t pack_bf16(float lo, float hi) {
@@ -57,6 +58,9 @@ struct RawBf16 {
   }
 };
 
+MPM_DEV float bf16_f(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+MPM_DEV uint16_t f_bf16(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+
 // two fp32 operations at once, each lane the IEEE result of the scalar one
 MPM_DEV uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
@@ -90,16 +94,28 @@ MPM_DEV void load_weight(const void* w, int f32, int k, float (&v)[VEC]) {
   }
 }
 
-// R sums over the block's threads, in a fixed order; every thread gets them.
-// sh: the caller alternates between two, so one barrier a call suffices.
-template <int R>
-MPM_DEV void block_sums(float (&v)[R], float (*sh)[kNormMaxWarps]) {
+// The threads that share a row: a block, or (WARP, rows short enough) a warp of
+// a block of kNormTeams
+template <bool WARP>
+struct RowTeam {
+  int t, nt;
+  long long index;                       // of the grid's teams
+  MPM_DEV RowTeam() {
+    t = WARP ? threadIdx.x & 31 : threadIdx.x;
+    nt = WARP ? 32 : blockDim.x;
+    index = WARP ? (long long)blockIdx.x * kNormTeams + (threadIdx.x >> 5) : blockIdx.x;
+  }
+};
+
+// R sums over a row's threads, in a fixed order; every thread gets them
+template <bool WARP, int R>
+MPM_DEV void row_sums(float (&v)[R], float (*sh)[kNormMaxWarps]) {
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v[r] = __fadd_rn(v[r], __shfl_xor_sync(0xFFFFFFFFu, v[r], o));
+  if constexpr (WARP) return;
   const int nw = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (nw == 1) return;
 #pragma unroll
   for (int r = 0; r < R; ++r)
     if (lane == 0) sh[r][warp] = v[r];
@@ -111,13 +127,44 @@ MPM_DEV void block_sums(float (&v)[R], float (*sh)[kNormMaxWarps]) {
   }
 }
 
-template <int VEC, int IT, int R>
-__global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_kernel(const NormFwd p) {
+// Sum over the block's threads where every thread also says whether its wait
+// went well; false if any did not.  sh: the caller
+// alternates between two, so one barrier a call suffices.
+MPM_DEV bool block_sum_ok(float& v, float* sh, bool ok) {
+  const int nw = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  if (lane == 0) sh[warp] = v;
+  if (__syncthreads_or(!ok)) return false;
+  v = lane < nw ? sh[lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return true;
+}
+
+// A ring of S stages whose copies are waited for in order; the place of row
+// number `it` of a block
+struct RingCursor {
+  int s = 0;
+  uint32_t phase = 0;
+  MPM_DEV void next(int S) { if (++s == S) { s = 0; phase ^= 1; } }
+  // lets the copies of the rows after a failed wait land (bounded), from thread 0
+  MPM_DEV void drain(uint32_t bar0, int S, int outstanding, long long row, long long step, long long M) {
+    for (int j = 0; j < outstanding && row < M; ++j, row += step) {
+      mbar_wait(bar0 + 8 * s, phase, nullptr);
+      next(S);
+    }
+  }
+};
+
+template <int VEC, int IT, int R, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) add_rmsnorm_kernel(const NormFwd p) {
   __shared__ float sh[R][kNormMaxWarps];
   pdl_wait();
   pdl_launch_dependents();
-  const long long row0 = (long long)blockIdx.x * R;
-  const int t = threadIdx.x, nt = blockDim.x;
+  const RowTeam<WARP> team;
+  const int t = team.t, nt = team.nt;
+  const long long row0 = team.index * R;
   RawBf16<VEC> x[R][IT], res[R][IT];
 #pragma unroll
   for (int r = 0; r < R; ++r)
@@ -144,7 +191,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_kernel(const Norm
         ss[r] = __fmaf_rn(h[r][i][j], h[r][i][j], ss[r]);
       }
   }
-  block_sums<R>(ss, sh);
+  row_sums<WARP, R>(ss, sh);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     ss[r] = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss[r], (float)p.K), p.eps));
@@ -194,8 +241,9 @@ __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_kernel(const Norm
   const int nblk = p.K >> 5;
 #pragma unroll
   for (int r = 0; r < R; ++r)
-    for (int c = (row0 + r < p.M ? nblk : 0) + t; c < (int)p.s_cols_pad; c += nt)
-      p.s[sf_offset(row0 + r, c, p.s_cols_pad)] = 0;
+    if (row0 + r < (p.M + 127) / 128 * 128)
+      for (int c = (row0 + r < p.M ? nblk : 0) + t; c < (int)p.s_cols_pad; c += nt)
+        p.s[sf_offset(row0 + r, c, p.s_cols_pad)] = 0;
 }
 
 // ---------------------------------------------------------------- backward
@@ -219,7 +267,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_ring_kernel(const NormBw
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float sh[2][32];
   __shared__ __align__(8) uint64_t bars[kRingStages];
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, nw = blockDim.x >> 5;
+  const int t = threadIdx.x;
   const uint32_t row_bytes = (uint32_t)p.K * 2, stage_bytes = NT * row_bytes;
   const uint32_t base = smem_u32(ring), bar0 = smem_u32(bars);
   const int k = t * 8;
@@ -254,14 +302,14 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_ring_kernel(const NormBw
   }
   __syncthreads();
   const float rk = __fdiv_rn(1.0f, (float)p.K);
-  int s = 0, it = 0;
-  uint32_t phase = 0;
+  RingCursor cur;
+  int it = 0;
   long long row = blockIdx.x;
   float rstd = row < p.M ? p.rstd[row] : 0.0f;
   for (; row < p.M; row += step, ++it) {
     const float next_rstd = row + step < p.M ? p.rstd[row + step] : 0.0f;
-    const bool ok = mbar_wait(bar0 + 8 * s, phase, p.status);
-    const uint8_t* st = ring + s * stage_bytes + t * 16;
+    const bool ok = mbar_wait(bar0 + 8 * cur.s, cur.phase, p.status);
+    const uint8_t* st = ring + cur.s * stage_bytes + t * 16;
     RawBf16<8> a, b, h;
     a.zero(); b.zero(); h.zero();
     if (in) {
@@ -282,26 +330,16 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_ring_kernel(const NormBw
     float c, chi;
     f32x2_split(c2, c, chi);
     c = __fadd_rn(c, chi);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) c = __fadd_rn(c, __shfl_xor_sync(0xFFFFFFFFu, c, o));
-    if (lane == 0) sh[it & 1][warp] = c;
-    if (__syncthreads_or(!ok)) {
-      // a copy did not arrive in time (reported): let the others land (bounded), no result
-      if (t == 0)
-        for (int j = it > 0 ? 1 : 0, i = s; j < S && row < p.M; ++j, row += step) {
-          mbar_wait(bar0 + 8 * i, phase, nullptr);
-          if (++i == S) { i = 0; phase ^= 1; }
-        }
+    if (!block_sum_ok(c, sh[it & 1], ok)) {
+      // a copy did not arrive in time (reported): no result
+      if (t == 0) cur.drain(bar0, S, it > 0 ? S - 1 : S, row, step, p.M);
       return;
     }
     // the previous row's stage has been read by every thread
     if (t == 0 && it > 0) {
       const long long ahead = row + (long long)(S - 1) * step;
-      if (ahead < p.M) issue(ahead, s == 0 ? S - 1 : s - 1);
+      if (ahead < p.M) issue(ahead, cur.s == 0 ? S - 1 : cur.s - 1);
     }
-    c = lane < nw ? sh[it & 1][lane] : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) c = __fadd_rn(c, __shfl_xor_sync(0xFFFFFFFFu, c, o));
     const float f = -__fmul_rn(__fmul_rn(rstd, rstd), __fmul_rn(c, rk));
     if (in) {
       RawBf16<8> r, o;
@@ -318,7 +356,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_ring_kernel(const NormBw
       o.store(p.dx + row * p.lddx + k);
     }
     rstd = next_rstd;
-    if (++s == S) { s = 0; phase ^= 1; }
+    cur.next(S);
   }
   pdl_launch_dependents();
   if (!p.dw || !in) return;
@@ -332,136 +370,123 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_ring_kernel(const NormBw
   for (int j = 0; j < 4; ++j) f32x2_split(dw[j], out[2 * j], out[2 * j + 1]);
 }
 
-// The other forms hold R rows in registers, all their loads in flight together.
-// WIDE rows (32 values a thread) would not fit in registers with all operands
-// and the weight: the gradients of y are added as they arrive, dh is loaded
-// after the reduction and the weight is read again for every row.
-template <int VEC, int IT, int R>
-__global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_bwd_kernel(const NormBwd p) {
-  constexpr bool WIDE = VEC * IT > 16 || IT > 4;
-  __shared__ float sh[2][R][kNormMaxWarps];
-  const int t = threadIdx.x, nt = blockDim.x;
+// The other rows take two kernels: dx from one row a block (short rows: one a
+// warp), held in registers with all its loads in flight, and dw's partials from
+// blocks of columns.  They read dy and h twice, but the ring needs rows that
+// start on 16 bytes, and a register form that kept dw beside one row at a time
+// per SM was slower (216 against 72 us at 3000 x 4161).  WIDE rows (32 values a
+// thread) would not fit in registers with all operands: there the gradients of y
+// are added as they arrive and dh is loaded after the reduction.
+template <int VEC, int IT, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) rmsnorm_dx_kernel(const NormBwd p) {
+  constexpr bool WIDE = VEC * IT > 16;
+  constexpr int ITR = WIDE ? 1 : IT;
+  __shared__ float sh[1][kNormMaxWarps];
   pdl_wait();
-  float dw[IT][VEC], w[WIDE ? 1 : IT][VEC];
-#pragma unroll
-  for (int i = 0; i < IT; ++i) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) dw[i][j] = 0.0f;
-    if constexpr (!WIDE) {
-      const int k = (i * nt + t) * VEC;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) w[i][j] = 0.0f;
-      if (k < p.K) load_weight<VEC>(p.w, p.w_f32, k, w[i]);
-    }
-  }
-  int parity = 0;
-  for (long long row0 = (long long)blockIdx.x * R; row0 < p.M; row0 += (long long)gridDim.x * R, parity ^= 1) {
-    constexpr int ITR = WIDE ? 1 : IT;
-    RawBf16<VEC> dy[R][ITR], dy2[R][ITR], h[R][IT], dh[R][ITR];
-    float g[R][WIDE ? IT : 1][VEC];                 // WIDE: dy + dy2
-    float rstd[R], c[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const long long row = row0 + r;
-      rstd[r] = row < p.M ? p.rstd[row] : 0.0f;
-#pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        const int k = (i * nt + t) * VEC, iw = WIDE ? 0 : i;
-        dy[r][iw].zero(); dy2[r][iw].zero(); h[r][i].zero(); dh[r][iw].zero();
-        if (k < p.K && row < p.M) {
-          dy[r][iw].load(p.dy + row * p.lddy + k);
-          h[r][i].load(p.h + row * p.ldh + k);
-          if (p.dy2) dy2[r][iw].load(p.dy2 + row * p.lddy2 + k);
-          if (!WIDE && p.dh) dh[r][iw].load(p.dh + row * p.lddh + k);
-        }
-        if constexpr (WIDE) {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) g[r][i][j] = __fadd_rn(dy[r][0].value(j), dy2[r][0].value(j));
-        }
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      c[r] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        const int k = (i * nt + t) * VEC, iw = WIDE ? 0 : i;
-        if constexpr (WIDE) {
-          if (k < p.K) load_weight<VEC>(p.w, p.w_f32, k, w[0]);
-        }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float y = WIDE ? g[r][WIDE ? i : 0][j] : __fadd_rn(dy[r][iw].value(j), dy2[r][iw].value(j));
-          const float u = __fmul_rn(y, rstd[r]);
-          dw[i][j] = __fmaf_rn(u, h[r][i].value(j), dw[i][j]);
-          if (!WIDE || k < p.K) c[r] = __fmaf_rn(__fmul_rn(u, w[iw][j]), h[r][i].value(j), c[r]);
-        }
-      }
-    }
-    block_sums<R>(c, sh[parity]);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const long long row = row0 + r;
-      const float f = -__fmul_rn(__fmul_rn(rstd[r], rstd[r]), __fdiv_rn(c[r], (float)p.K));
-#pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        const int k = (i * nt + t) * VEC, iw = WIDE ? 0 : i;
-        if (k >= p.K || row >= p.M) continue;
-        if constexpr (WIDE) {
-          load_weight<VEC>(p.w, p.w_f32, k, w[0]);
-          dh[r][0].zero();
-          if (p.dh) dh[r][0].load(p.dh + row * p.lddh + k);
-        }
-        float d[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float y = WIDE ? g[r][WIDE ? i : 0][j] : __fadd_rn(dy[r][iw].value(j), dy2[r][iw].value(j));
-          const float u = __fmul_rn(__fmul_rn(y, rstd[r]), w[iw][j]);
-          d[j] = __fadd_rn(__fmaf_rn(h[r][i].value(j), f, u), dh[r][iw].value(j));
-        }
-        RawBf16<VEC> o;
-        o.set(d);
-        o.store(p.dx + row * p.lddx + k);
-      }
-    }
-  }
   pdl_launch_dependents();
-  if (!p.dw) return;
-  float* out = gridDim.x == 1 ? p.dw : p.part + (long long)blockIdx.x * p.K;
+  const RowTeam<WARP> team;
+  const int t = team.t, nt = team.nt;
+  const long long row = team.index;
+  const bool live = row < p.M;
+  const float rstd = live ? p.rstd[row] : 0.0f;
+  RawBf16<VEC> dy[ITR], dy2[ITR], h[IT], dh[ITR];
+  float u[IT][VEC], c[1] = {0.0f};
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    const int k = (i * nt + t) * VEC;
-    if (k >= p.K) continue;
-    if (VEC == 8 && reinterpret_cast<uintptr_t>(out) % 16 == 0) {
-#pragma unroll
-      for (int j = 0; j < VEC; j += 4)
-        *reinterpret_cast<float4*>(out + k + j) =
-            make_float4(dw[i][j], dw[i][(j + 1) % VEC], dw[i][(j + 2) % VEC], dw[i][(j + 3) % VEC]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) out[k + j] = dw[i][j];
+    const int k = (i * nt + t) * VEC, iw = WIDE ? 0 : i;
+    dy[iw].zero(); dy2[iw].zero(); h[i].zero(); dh[iw].zero();
+    if (k < p.K && live) {
+      dy[iw].load(p.dy + row * p.lddy + k);
+      h[i].load(p.h + row * p.ldh + k);
+      if (p.dy2) dy2[iw].load(p.dy2 + row * p.lddy2 + k);
+      if (!WIDE && p.dh) dh[iw].load(p.dh + row * p.lddh + k);
     }
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) u[i][j] = __fadd_rn(dy[0].value(j), dy2[0].value(j));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int k = (i * nt + t) * VEC, iw = WIDE ? 0 : i;
+    float w[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) w[j] = 0.0f;
+    if (k < p.K) load_weight<VEC>(p.w, p.w_f32, k, w);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      if (!WIDE) u[i][j] = __fadd_rn(dy[iw].value(j), dy2[iw].value(j));
+      u[i][j] = __fmul_rn(__fmul_rn(u[i][j], rstd), w[j]);
+      c[0] = __fmaf_rn(u[i][j], h[i].value(j), c[0]);
+    }
+  }
+  row_sums<WARP, 1>(c, sh);
+  const float f = -__fmul_rn(__fmul_rn(rstd, rstd), __fdiv_rn(c[0], (float)p.K));
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int k = (i * nt + t) * VEC, iw = WIDE ? 0 : i;
+    if (k >= p.K || !live) continue;
+    if (WIDE && p.dh) dh[0].load(p.dh + row * p.lddh + k);
+    float d[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) d[j] = __fadd_rn(__fmaf_rn(h[i].value(j), f, u[i][j]), dh[iw].value(j));
+    RawBf16<VEC> o;
+    o.set(d);
+    o.store(p.dx + row * p.lddx + k);
   }
 }
 
-// dw = the sum of the partials: 32 columns a block, warp w the parts w, w + 32, ...
-__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* part, int parts, int K, float* dw) {
-  __shared__ float sh[32][33];
+// Partials of dw = sum over rows of dy h rstd: one column a thread, the rows
+// blockIdx.y, blockIdx.y + gridDim.y, ..., eight of them in flight
+__global__ void __launch_bounds__(256) rmsnorm_dw_rows_kernel(const NormBwd p) {
   pdl_wait();
   pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int k = blockIdx.x * 32 + lane;
+  const int k = blockIdx.x * blockDim.x + threadIdx.x;
+  if (k >= p.K) return;
+  const long long step = gridDim.y;
+  float s = 0.0f;
+  for (long long row0 = blockIdx.y; row0 < p.M; row0 += 8 * step) {
+    float y[8], h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const long long row = row0 + i * step;
+      y[i] = h[i] = 0.0f;
+      if (row < p.M) {
+        y[i] = bf16_f(p.dy[row * p.lddy + k]);
+        if (p.dy2) y[i] = __fadd_rn(y[i], bf16_f(p.dy2[row * p.lddy2 + k]));
+        h[i] = __fmul_rn(bf16_f(p.h[row * p.ldh + k]), p.rstd[row]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = __fmaf_rn(y[i], h[i], s);
+  }
+  (gridDim.y == 1 ? p.dw : p.part + (long long)blockIdx.y * p.K)[k] = s;
+}
+
+// dw = the sum of the partials: C columns a block (few where there are few
+// columns), 1024 / C partials at a time
+template <int C>
+__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* part, int parts, int K, float* dw) {
+  constexpr int G = 1024 / C;
+  __shared__ float sh[C][G + 1];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int c = threadIdx.x % C, g = threadIdx.x / C, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int k = blockIdx.x * C + c;
   float s = 0.0f;
   if (k < K) {
 #pragma unroll 8
-    for (int i = warp; i < parts; i += 32) s = __fadd_rn(s, part[(long long)i * K + k]);
+    for (int i = g; i < parts; i += G) s = __fadd_rn(s, part[(long long)i * K + k]);
   }
-  sh[warp][lane] = s;
+  sh[c][g] = s;
   __syncthreads();
-  s = sh[lane][warp];                    // warp w: the 32 partial sums of column w
+  if (warp >= C || blockIdx.x * C + warp >= K) return;
+  s = 0.0f;                              // warp w: column w
+#pragma unroll
+  for (int i = lane; i < G; i += 32) s = __fadd_rn(s, sh[warp][i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
-  if (lane == 0 && blockIdx.x * 32 + warp < K) dw[blockIdx.x * 32 + warp] = s;
+  if (lane == 0) dw[blockIdx.x * C + warp] = s;
 }
 
 // ---------------------------------------------------------------- launchers
@@ -473,102 +498,118 @@ static unsigned norm_threads(int K, int per_thread) {
   return (unsigned)((n + 31) / 32 * 32);
 }
 
-template <int VEC, int IT, int R>
-static cudaError_t norm_fwd(const NormFwd& p, cudaStream_t st) {
-  const long long rows = p.q ? (p.M + 127) / 128 * 128 : p.M;
-  return launch_serial(add_rmsnorm_kernel<VEC, IT, R>, dim3((unsigned)((rows + R - 1) / R)),
-                       dim3(norm_threads(p.K, VEC * IT)), 0, st, p);
+// Rings: as many blocks an SM as 1024 threads make, each with `stages` stages of
+// `stage` bytes (0 stages: rows too long for two)
+struct NormRing { unsigned threads; int blocks, stages, smem; };
+static NormRing norm_ring(int K, int per_thread, int stage) {
+  NormRing r{norm_threads(K, per_thread), 0, 0, 0};
+  if (r.threads > 1024) return r;
+  r.blocks = 1024 / (int)r.threads;
+  r.stages = (222 * 1024 / r.blocks - 1024) / stage;
+  if (r.stages > kRingStages) r.stages = kRingStages;
+  if (r.stages < 2) r.stages = 0;
+  r.smem = r.stages * stage;
+  return r;
+}
+template <auto kernel, typename P>
+static cudaError_t launch_ring(const NormRing& r, long long blocks, const P& p, cudaStream_t st) {
+  static std::atomic<bool> set[64];      // per device
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev >= 64 || !set[dev].load()) {
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024);
+    if (err != cudaSuccess) return err;
+    if (dev < 64) set[dev].store(true);
+  }
+  return launch_serial(kernel, dim3((unsigned)blocks), dim3(r.threads), (size_t)r.smem, st, p, r.stages);
 }
 
-// Values a thread holds of a row of K (VEC * IT): few, so that many threads
-// share it, up to 512 of them
-static int norm_per_thread(int K, bool vec) {
-  if (vec) return K <= 8 * kNormMaxThreads ? 8 : (K <= 16 * kNormMaxThreads ? 16 : 32);
-  return K <= 4 * kNormMaxThreads ? 4 : (K <= 16 * kNormMaxThreads ? 16 : 32);
+template <int VEC, int IT, int R, bool WARP>
+static cudaError_t norm_fwd(const NormFwd& p, cudaStream_t st) {
+  const long long rows = p.q ? (p.M + 127) / 128 * 128 : p.M, per = WARP ? R * kNormTeams : R;
+  return launch_serial(add_rmsnorm_kernel<VEC, IT, R, WARP>, dim3((unsigned)((rows + per - 1) / per)),
+                       dim3(WARP ? 32 * kNormTeams : norm_threads(p.K, VEC * IT)), 0, st, p);
 }
 
 cudaError_t launch_add_rmsnorm(const NormFwd& p, cudaStream_t st) {
   const bool v = p.K % 8 == 0 && vec8(p.x, p.ldx) && vec8(p.r, p.ldr) && vec8(p.h, p.ldh) &&
                  vec8(p.y, p.ldy) && vec8(p.w, 0);
-  const int per = norm_per_thread(p.K, v);
+  // rows kRowsAtATime at a time where that leaves four blocks for every SM
+  const bool many = p.M >= kRowsAtATime * 152 * 4;
   if (v) {
-    if (per == 8) return p.M >= kRowsAtATime * 152 * 4 ? norm_fwd<8, 1, kRowsAtATime>(p, st) : norm_fwd<8, 1, 1>(p, st);
-    return per == 16 ? norm_fwd<8, 2, 1>(p, st) : norm_fwd<8, 4, 1>(p, st);
+    if (p.K <= 256)
+      return p.M >= kRowsAtATime * kNormTeams * 152 ? norm_fwd<8, 1, kRowsAtATime, true>(p, st)
+                                                    : norm_fwd<8, 1, 1, true>(p, st);
+    if (p.K <= 8 * kNormMaxThreads)
+      return many ? norm_fwd<8, 1, kRowsAtATime, false>(p, st) : norm_fwd<8, 1, 1, false>(p, st);
+    return p.K <= 16 * kNormMaxThreads ? norm_fwd<8, 2, 1, false>(p, st) : norm_fwd<8, 4, 1, false>(p, st);
   }
-  if (per == 4) return norm_fwd<1, 4, 1>(p, st);
-  return per == 16 ? norm_fwd<1, 16, 1>(p, st) : norm_fwd<1, 32, 1>(p, st);
+  if (p.K <= 128) return norm_fwd<1, 4, 1, true>(p, st);
+  if (p.K <= 4 * kNormMaxThreads) return norm_fwd<1, 4, 1, false>(p, st);
+  return p.K <= 16 * kNormMaxThreads ? norm_fwd<1, 16, 1, false>(p, st) : norm_fwd<1, 32, 1, false>(p, st);
 }
 
-// The ring form: 16-byte aligned rows of 512 to 8192 elements, as many blocks an
-// SM as 1024 threads make, and the stages that fit beside one another.
-struct NormRing { int blocks, stages, smem; };
-static NormRing bwd_ring(int K, int operands) {
-  NormRing r{0, 0, 0};
-  if (K % 8 != 0 || K < 512 || K > 8192) return r;
-  r.blocks = 1024 / (int)norm_threads(K, 8);
-  const int row = 2 * K * operands;
-  r.stages = (222 * 1024 / r.blocks - 1024) / row;
-  if (r.stages > kRingStages) r.stages = kRingStages;
-  r.smem = r.stages * row;
-  return r;
-}
-
-// Blocks of the backward, each with its own partial dw
-static long long bwd_parts(long long M, int K, int per_thread) {
-  const int n = kBwdThreads / (int)norm_threads(K, per_thread);
-  const long long most = 152ll * (n < 1 ? 1 : n);
-  return M < most ? M : most;
-}
+// Blocks of the backward's ring, each with its own partial dw (the two-kernel
+// form makes no more)
 long long rmsnorm_backward_parts(long long M, int K) {
-  long long n = bwd_parts(M, K, norm_per_thread(K, true));
-  const long long b = bwd_parts(M, K, norm_per_thread(K, false)), c = 152ll * bwd_ring(K, 4).blocks;
-  if (b > n) n = b;
-  if (c > n) n = c;
-  return n < M ? n : M;
+  const int threads = (int)norm_threads(K, 8);
+  const long long most = 152ll * (threads < 1024 ? 1024 / threads : 1);
+  return M < most ? M : most;
 }
 
 static cudaError_t norm_dw(const NormBwd& p, long long parts, cudaStream_t st) {
   if (!p.dw || parts == 1) return cudaSuccess;
-  return launch_serial(rmsnorm_dw_kernel, dim3((unsigned)((p.K + 31) / 32)), dim3(1024), 0, st,
+  if (p.K <= 1024)
+    return launch_serial(rmsnorm_dw_kernel<8>, dim3((unsigned)((p.K + 7) / 8)), dim3(1024), 0, st,
+                         (const float*)p.part, (int)parts, p.K, p.dw);
+  return launch_serial(rmsnorm_dw_kernel<32>, dim3((unsigned)((p.K + 31) / 32)), dim3(1024), 0, st,
                        (const float*)p.part, (int)parts, p.K, p.dw);
 }
 
-template <bool TWO, bool RES>
-static cudaError_t norm_bwd_ring(const NormBwd& p, const NormRing& r, cudaStream_t st) {
-  const auto kernel = add_rmsnorm_bwd_ring_kernel<TWO, RES>;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, r.smem);
-  if (err != cudaSuccess) return err;
-  const long long parts = p.M < 152ll * r.blocks ? p.M : 152ll * r.blocks;
-  err = launch_serial(kernel, dim3((unsigned)parts), dim3(norm_threads(p.K, 8)), (size_t)r.smem, st, p, r.stages);
-  return err != cudaSuccess ? err : norm_dw(p, parts, st);
+template <auto kernel>
+static cudaError_t norm_bwd_ring(const NormBwd& p, int operands, cudaStream_t st) {
+  const NormRing r = norm_ring(p.K, 8, 2 * p.K * operands);
+  const long long blocks = rmsnorm_backward_parts(p.M, p.K);
+  const cudaError_t err = launch_ring<kernel>(r, blocks, p, st);
+  return err != cudaSuccess ? err : norm_dw(p, blocks, st);
 }
 
-template <int VEC, int IT, int R>
-static cudaError_t norm_bwd(const NormBwd& p, cudaStream_t st) {
-  long long parts = bwd_parts(p.M, p.K, VEC * IT);
-  if (parts > (p.M + R - 1) / R) parts = (p.M + R - 1) / R;
-  cudaError_t err = launch_serial(add_rmsnorm_bwd_kernel<VEC, IT, R>, dim3((unsigned)parts),
-                                  dim3(norm_threads(p.K, VEC * IT)), 0, st, p);
-  return err != cudaSuccess ? err : norm_dw(p, parts, st);
+template <int VEC, int IT, bool WARP>
+static cudaError_t norm_bwd_two(const NormBwd& p, cudaStream_t st) {
+  if (p.dw) {
+    // first dw: dx may replace one of its operands.  About 2048 threads an SM,
+    // eight rows a block at least
+    const unsigned threads = p.K < 256 ? norm_threads(p.K, 1) : 256u, gx = ((unsigned)p.K + threads - 1) / threads;
+    long long parts = 152ll * (2048 / threads) / gx;
+    const long long most = rmsnorm_backward_parts(p.M, p.K);
+    if (parts > (p.M + 7) / 8) parts = (p.M + 7) / 8;
+    if (parts > most) parts = most;
+    if (parts < 1) parts = 1;
+    cudaError_t err = launch_serial(rmsnorm_dw_rows_kernel, dim3(gx, (unsigned)parts), dim3(threads), 0, st, p);
+    if (err == cudaSuccess) err = norm_dw(p, parts, st);
+    if (err != cudaSuccess) return err;
+  }
+  const long long per = WARP ? kNormTeams : 1;
+  return launch_serial(rmsnorm_dx_kernel<VEC, IT, WARP>, dim3((unsigned)((p.M + per - 1) / per)),
+                       dim3(WARP ? 32 * kNormTeams : norm_threads(p.K, VEC * IT)), 0, st, p);
 }
 
 cudaError_t launch_add_rmsnorm_backward(const NormBwd& p, cudaStream_t st) {
   const bool v = p.K % 8 == 0 && vec8(p.dy, p.lddy) && vec8(p.dy2, p.lddy2) && vec8(p.h, p.ldh) &&
                  vec8(p.dh, p.lddh) && vec8(p.dx, p.lddx) && vec8(p.w, 0);
-  const int per = norm_per_thread(p.K, v);
   if (v) {
-    const NormRing r = bwd_ring(p.K, 2 + (p.dy2 != nullptr) + (p.dh != nullptr));
-    if (r.stages >= 3) {
-      if (p.dy2) return p.dh ? norm_bwd_ring<true, true>(p, r, st) : norm_bwd_ring<true, false>(p, r, st);
-      return p.dh ? norm_bwd_ring<false, true>(p, r, st) : norm_bwd_ring<false, false>(p, r, st);
-    }
-    // kRowsAtATime rows at a time where every block gets some
-    if (per == 8)
-      return p.M >= kRowsAtATime * bwd_parts(p.M, p.K, 8) ? norm_bwd<8, 1, kRowsAtATime>(p, st) : norm_bwd<8, 1, 1>(p, st);
-    return per == 16 ? norm_bwd<8, 2, 1>(p, st) : norm_bwd<8, 4, 1>(p, st);
+    if (p.K <= 256) return norm_bwd_two<8, 1, true>(p, st);
+    if (p.K > 8192) return norm_bwd_two<8, 4, false>(p, st);
+    if (p.dy2)
+      return p.dh ? norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<true, true>>(p, 4, st)
+                  : norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<true, false>>(p, 3, st);
+    return p.dh ? norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<false, true>>(p, 3, st)
+                : norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<false, false>>(p, 2, st);
   }
-  if (per == 4) return norm_bwd<1, 4, 1>(p, st);
-  return per == 16 ? norm_bwd<1, 16, 1>(p, st) : norm_bwd<1, 32, 1>(p, st);
+  if (p.K <= 128) return norm_bwd_two<1, 4, true>(p, st);
+  if (p.K <= 4 * kNormMaxThreads) return norm_bwd_two<1, 4, false>(p, st);
+  return p.K <= 16 * kNormMaxThreads ? norm_bwd_two<1, 16, false>(p, st) : norm_bwd_two<1, 32, false>(p, st);
 }
 
 }  // namespace mpm

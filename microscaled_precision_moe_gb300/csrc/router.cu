@@ -26,7 +26,7 @@
 // With k > 32, more than 32 such keys (masses of ties) or fewer than k lanes with
 // an expert in reach, the warp takes k maxima one after the other instead.
 // Softmax scores use the hardware exponential (a few ulp); sigmoid scores expf
-// and IEEE division, since with a bias the choice depends on their last bit.
+// and the IEEE reciprocal, since with a bias the choice depends on their last bit.
 // Sums over tokens go through per-block partials added in a fixed order (no
 // floating-point atomics).
 #include "router.cuh"
@@ -174,6 +174,13 @@ struct __align__(16) RouteWarp {
   float cand[32];
 };
 
+// what the choice compares: the logits, or sigmoid scores with their bias
+template <bool SIG, int NE>
+MPM_DEV float (&route_keys(float (&l)[NE], float (&sig_key)[SIG ? NE : 1]))[NE] {
+  if constexpr (SIG) return sig_key;
+  else return l;
+}
+
 // One token: ids and weights to global memory, counts to sh_counts, shares
 // added to load.  raw: its logits; replaced by those of token `next`.
 template <int NE, bool SIG, bool BF16>
@@ -197,15 +204,13 @@ MPM_DEV void route_token(const RouteArgs& a, int t, int next, int lane, RawLogit
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
       // l = -inf: expf gives inf and the score is 0
-      s[i] = __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l[i])));
+      s[i] = __frcp_rn(__fadd_rn(1.0f, expf(-l[i])));
       sum = __fadd_rn(sum, s[i]);
       sig_key[i] = l[i] > -INFINITY ? __fadd_rn(s[i], bias[i]) : -INFINITY;
       top = fmaxf(top, sig_key[i]);
     }
   }
-  float (&key)[NE] = [&]() -> float (&)[NE] {
-    if constexpr (SIG) return sig_key; else return l;
-  }();
+  float (&key)[NE] = route_keys<SIG, NE>(l, sig_key);
   uint32_t o = ordered_bits(top);
   uint32_t tau = __reduce_max_sync(0xFFFFFFFFu, o);
   float m = ordered_value(tau);
@@ -299,7 +304,7 @@ MPM_DEV void route_token(const RouteArgs& a, int t, int next, int lane, RawLogit
           float v;
           if constexpr (BF16) v = bf16lo(static_cast<const uint16_t*>(a.logits)[t * a.ld + e]);
           else v = static_cast<const float*>(a.logits)[t * a.ld + e];
-          w = __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-fminf(v, kLargest))));
+          w = __frcp_rn(__fadd_rn(1.0f, expf(-fminf(v, kLargest))));
         } else {
           w = exp2_ftz(__fmaf_rn(c, kLog2e, -m2));
         }

@@ -134,6 +134,20 @@ def test_in_place_residual(K):
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
 
 
+@pytest.mark.parametrize("M,K", [(40, 100), (700, 176), (300, 1001), (200, 2048), (20, 9001), (20, 9008)])
+@pytest.mark.parametrize("onto", ["dy", "dy2", "h", "dh"])
+def test_in_place_gradient(M, K, onto):
+    """dx in the place of any of its operands."""
+    ops = _ops()
+    t = {n: _rows(40 + i, M, K, std=1e-2 if n != "h" else 1.0) for i, n in enumerate(("dy", "dy2", "h", "dh"))}
+    w = _weight(44, K, True)
+    rstd = ops.add_rmsnorm(t["h"], w)["rstd"]
+    ref = ops.add_rmsnorm_backward(t["dy"], t["h"], rstd, w, dy2=t["dy2"], dh=t["dh"])
+    dx, dw = ops.add_rmsnorm_backward(t["dy"], t["h"], rstd, w, dy2=t["dy2"], dh=t["dh"],
+                                      out=(t[onto], torch.empty(K, device="cuda")))
+    assert dx is t[onto] and torch.equal(dx, ref[0]) and torch.equal(dw, ref[1])
+
+
 def test_rows_of_zeros_infinities_and_nan():
     """A zero row gives zeros; NaN and infinities stay in their rows."""
     K = 256
