@@ -482,8 +482,8 @@ mpm_status mpm_moe_route_backward(const void* logits_dev, int logits_dtype, int6
                                   const float* bias_dev, const uint8_t* token_mask_dev,
                                   const int32_t* ids_dev, const int32_t* counts_dev,
                                   const int32_t* n_tokens_dev, const float* dprob_dev,
-                                  const float* dloss_dev, void* dlogits_dev, int64_t ldd,
-                                  cudaStream_t stream);
+                                  const float* dloss_dev, void* dlogits_dev, int dlogits_dtype,
+                                  int64_t ldd, cudaStream_t stream);
 
 /*
  * Gradient of the routing weights: dprob[t, j] = <dout[t], y_perm[inv_perm[t*k+j]]>

@@ -84,7 +84,7 @@ _SIGS = {
     "mpm_moe_route": (_int, [_vp, _int, _i64, _i64, _i64, _int, _int, _int, _f32, _vp, _vp, _vp, _vp,
                              _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "mpm_moe_route_backward": (_int, [_vp, _int, _i64, _i64, _i64, _int, _int, _int, _f32, _vp, _vp,
-                                      _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+                                      _vp, _vp, _vp, _vp, _vp, _vp, _int, _i64, _vp]),
     "mpm_moe_combine_dprob": (_int, [_vp, _vp, _vp, _vp, _i64, _int, _i64, _i64, _vp, _vp]),
     "mpm_moe_gather_mxfp8": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _vp, _i64, _i64, _vp, _vp, _vp]),
     "mpm_nvfp4_dequantize": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp]),

@@ -474,19 +474,20 @@ mpm_status mpm_moe_route_backward(const void* logits, int logits_dtype, int64_t 
                                   const float* bias, const uint8_t* mask, const int32_t* ids,
                                   const int32_t* counts, const int32_t* n_tokens,
                                   const float* dprob, const float* dloss, void* dlogits,
-                                  int64_t ldd, cudaStream_t stream) {
+                                  int dlogits_dtype, int64_t ldd, cudaStream_t stream) {
   if (!dlogits || (dprob && !ids) || (dloss && (!counts || !n_tokens))) return MPM_ERR_NULL;
   mpm::RouteArgs a{};
   const mpm_status st = route_args(a, logits, logits_dtype, T, E, ld, k, score, normalize, scale,
                                    bias, mask);
   if (st != MPM_OK) return st;
+  if (dlogits_dtype != MPM_DTYPE_BF16 && dlogits_dtype != MPM_DTYPE_F32) return MPM_ERR_UNSUPPORTED;
   if (ldd < E) return MPM_ERR_SHAPE;
-  if (!aligned(dlogits, logits_dtype == MPM_DTYPE_F32 ? 4 : 2) || !aligned(ids, 4) ||
+  if (!aligned(dlogits, dlogits_dtype == MPM_DTYPE_F32 ? 4 : 2) || !aligned(ids, 4) ||
       !aligned(counts, 4) || !aligned(n_tokens, 4) || !aligned(dprob, 4) || !aligned(dloss, 4))
     return MPM_ERR_ALIGN;
   a.in_ids = ids; a.in_counts = counts; a.in_n = n_tokens;
   a.dprob = dprob; a.dloss = dloss;
-  a.dlogits = dlogits; a.ldd = ldd;
+  a.dlogits = dlogits; a.ldd = ldd; a.out_bf16 = dlogits_dtype == MPM_DTYPE_BF16;
   return cuda_status(mpm::launch_route_backward(a, stream));
 }
 

@@ -640,23 +640,23 @@ __global__ void __launch_bounds__(32 * kBwdWarps) route_bwd_kernel(const RouteAr
     }
 #pragma unroll
     for (int i = 0; i < NE; ++i) dl[i] = (on && l[i] > -INFINITY) ? dl[i] : 0.0f;
-    if constexpr (BF16) {
+    if (a.out_bf16) {
       __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.dlogits) + t * a.ldd;
 #pragma unroll
-      for (int i = 0; i < NE; i += 2) {
+      for (int i = 0; i < NE; i += BF16 ? 2 : 1) {
         const int e = expert_of<BF16>(i, lane);
-        if (a.vec) {
-          if (e < a.E) *reinterpret_cast<__nv_bfloat162*>(p + e) = __floats2bfloat162_rn(dl[i], dl[i + 1]);
+        if (BF16 && a.vec_out) {               // even E, 4-byte aligned rows
+          if (e < a.E) *reinterpret_cast<__nv_bfloat162*>(p + e) = __floats2bfloat162_rn(dl[i], dl[(i + 1) % NE]);
         } else {
           if (e < a.E) p[e] = __float2bfloat16_rn(dl[i]);
-          if (e + 1 < a.E) p[e + 1] = __float2bfloat16_rn(dl[i + 1]);
+          if (BF16 && e + 1 < a.E) p[e + 1] = __float2bfloat16_rn(dl[(i + 1) % NE]);
         }
       }
     } else {
-      float* p = static_cast<float*>(a.dlogits) + t * a.ldd + lane;
+      float* p = static_cast<float*>(a.dlogits) + t * a.ldd;
 #pragma unroll
       for (int i = 0; i < NE; ++i)
-        if (i * 32 + lane < a.E) p[i * 32] = dl[i];
+        if (expert_of<BF16>(i, lane) < a.E) p[expert_of<BF16>(i, lane)] = dl[i];
     }
     t = next;
   }
@@ -748,7 +748,8 @@ cudaError_t launch_route(const RouteArgs& in, void* ws, cudaStream_t st) {
 
 cudaError_t launch_route_backward(const RouteArgs& in, cudaStream_t st) {
   RouteArgs a = in;
-  a.vec = route_vec(a.logits, a.ld, a.bf16, a.E) && route_vec(a.dlogits, a.ldd, a.bf16, a.E);
+  a.vec = route_vec(a.logits, a.ld, a.bf16, a.E);
+  a.vec_out = route_vec(a.dlogits, a.ldd, 1, a.E);
   MPM_ROUTE_DISPATCH(route_backward)
 }
 

@@ -18,9 +18,10 @@ struct RouteArgs {
   // backward
   const int* in_ids; const int* in_counts; const int* in_n;
   const float* dprob; const float* dloss;  // [T, k], [1] (nullable)
-  void* dlogits; long long ldd;
+  void* dlogits; long long ldd; int out_bf16;
   int* status;
-  int vec, cluster;                        // set by the launchers: aligned rows; one cluster
+  int vec, vec_out, cluster;               // set by the launchers: rows read and written by
+                                           // words; one cluster routes everything
 };
 size_t route_ws_bytes(long long T, int E);
 cudaError_t launch_route(const RouteArgs& a, void* ws, cudaStream_t st);

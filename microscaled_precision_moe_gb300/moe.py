@@ -214,6 +214,11 @@ class NVFP4MoE:
         mark(6)
         return dst
 
+    def prob_grad(self, dout, topk_prob, out=None):
+        """The gradient of topk_prob [T, k] (fp32) after forward, from dout
+        [T, H] bf16: <dout, y> / prob of the rows the forward combined."""
+        return ops.moe_combine_dprob(dout, self.y, self.seg[2], topk_prob, out=out)
+
     # kernels launched by one forward: the segment build (one cooperative
     # kernel, after an 8-byte memset of its barrier words), the quantiser into
     # the routed rows (two kernels), FC1, the quantiser of D, FC2, combine
@@ -400,6 +405,34 @@ class MXFP8MoE:
         mark(6)
         ops.moe_combine(self.y, inv, T, k, out=self.out)
         return self.out
+
+    def forward_quantized(self, x_q, x_s, topk_ids, topk_prob):
+        """The forward for rollout, on tokens that are MXFP8 already: row-wise
+        codes x_q [T, H] and tiled scales x_s, as ops.add_rmsnorm or
+        ops.mxfp8_quantize write them.  Their bytes are gathered into the
+        expert order and no operand of the backward is kept: the same out as
+        forward gives for the bf16 rows they were quantised from."""
+        T, H, I, E, k, cap = self.T, self.H, self.I, self.E, self.k, self.cap
+        seg, perm, inv, rp = self.seg
+        ops.moe_build_segments(topk_ids, topk_prob, E, out=self.seg, ws=self.seg_ws,
+                               pad=self.tile_m)
+        xq, xs, dq = self.xq["row_q"], self.xq["row_s"], self.dq
+        ops.moe_gather_mxfp8(x_q, x_s, perm, seg, E, k, cap, out=(xq, xs))
+        ops.moe_grouped_gemm(L.KIND_MXFP8, L.GROUP_M, L.EPI_SWIGLU, E, cap, 2 * I, H, seg, xq,
+                             self.w1["row_q"], xs, H // 32, self.w1["row_s"], H // 32, self.d,
+                             b_rows_per_expert=2 * I, row_prob=rp, out2=self.d, tile_m=self.tile_m)
+        ops.mxfp8_quantize(self.d, colwise=False, m_valid=seg[E:],
+                           out={"row_q": dq["row_q"], "row_s": dq["row_s"]})
+        ops.moe_grouped_gemm(L.KIND_MXFP8, L.GROUP_M, L.EPI_BF16, E, cap, H, I, seg, dq["row_q"],
+                             self.w2["row_q"], dq["row_s"], I // 32, self.w2["row_s"], I // 32,
+                             self.y, b_rows_per_expert=H, tile_m=self.tile_m)
+        ops.moe_combine(self.y, inv, T, k, out=self.out)
+        return self.out
+
+    def prob_grad(self, dout, topk_prob, out=None):
+        """The gradient of topk_prob [T, k] (fp32) after a forward, from dout
+        [T, H] bf16: <dout, y> / prob of the rows it combined."""
+        return ops.moe_combine_dprob(dout, self.y, self.seg[2], topk_prob, out=out)
 
     def backward(self, dy, mark=None):
         """``mark(i)`` (optional) before STEP_STAGES[i] for i = 7..13 and once

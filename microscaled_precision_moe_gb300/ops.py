@@ -635,9 +635,10 @@ def moe_route(logits, k: int, score="softmax", normalize=True, scale=1.0, bias=N
 
 def moe_route_backward(logits, ids, counts, n_tokens, dprob=None, dloss=None, score="softmax",
                        normalize=True, scale=1.0, bias=None, token_mask=None, out=None):
-    """dlogits [T, E] (the logits' type) of moe_route with the same arguments,
-    from dprob fp32 [T, k] and / or dloss fp32 [1]; ids, counts and n_tokens
-    are the forward's.  The choice and the counts are constants."""
+    """dlogits [T, E] (the logits' type, or that of ``out``, bf16 or fp32) of
+    moe_route with the same arguments, from dprob fp32 [T, k] and / or dloss
+    fp32 [1]; ids, counts and n_tokens are the forward's.  The choice and the
+    counts are constants."""
     lib = L.load()
     T, E, ld, sc, ldt = _route_args(logits, score, bias, token_mask)
     dev = logits.device
@@ -654,9 +655,11 @@ def moe_route_backward(logits, ids, counts, n_tokens, dprob=None, dloss=None, sc
     if dloss is not None:
         _check(dloss, "dloss", _F32, min_numel=1)
     if out is None:
-        out, ldd = torch.empty(T, E, dtype=logits.dtype, device=dev), E
+        out, ldd, odt = torch.empty(T, E, dtype=logits.dtype, device=dev), E, ldt
     else:
-        _check(out, "out", logits.dtype, dim=2)
+        if out.dtype is not _F32 and out.dtype is not _BF16:
+            raise TypeError(f"out: expected bf16 or fp32, got {out.dtype}")
+        odt = L.DTYPE_F32 if out.dtype is _F32 else L.DTYPE_BF16
         if out.shape != logits.shape or (out.stride(1) != 1 and E != 1):
             raise ValueError(f"out: expected {tuple(logits.shape)} with dense rows")
         ldd = max(out.stride(0), E) if T == 1 else out.stride(0)
@@ -664,7 +667,7 @@ def moe_route_backward(logits, ids, counts, n_tokens, dprob=None, dloss=None, sc
     st = lib.mpm_moe_route_backward(logits.data_ptr(), ldt, T, E, ld, k, sc, 1 if normalize else 0,
                                     scale, _dp(bias), _dp(token_mask), ids.data_ptr(),
                                     counts.data_ptr(), n_tokens.data_ptr(), _dp(dprob), _dp(dloss),
-                                    out.data_ptr(), ldd, _raw_stream(dev))
+                                    out.data_ptr(), odt, ldd, _raw_stream(dev))
     if st:
         L.check(st, "mpm_moe_route_backward")
     return out

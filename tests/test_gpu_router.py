@@ -220,6 +220,24 @@ def test_in_place_gradient_stream_and_graph():
         assert torch.equal(a, dref)
 
 
+@pytest.mark.parametrize("T,E,pad", [(100, 128, 0), (77, 33, 0), (64, 160, 96), (50, 61, 3)])
+def test_gradient_type_of_its_own(T, E, pad):
+    """bf16 gradients of fp32 logits are the fp32 ones rounded once, and the
+    other way round the fp32 gradients of bf16 logits round to the bf16 ones."""
+    ops = _ops()
+    for bf16 in (False, True):
+        l = _logits(20 + T, T, E, bf16)
+        o = ops.moe_route(l, 4)
+        g = torch.Generator(device="cuda").manual_seed(T)
+        kw = dict(dprob=torch.randn(T, 4, device="cuda", generator=g), dloss=torch.ones(1, device="cuda"))
+        a = (l, o["ids"], o["counts"], o["n_tokens"])
+        full = ops.moe_route_backward(*a, out=torch.empty(T, E, device="cuda"), **kw)
+        buf = torch.full((T, E + pad), 7.0, dtype=torch.bfloat16, device="cuda")
+        ops.moe_route_backward(*a, out=buf[:, :E], **kw)
+        assert torch.equal(buf[:, :E], full.to(torch.bfloat16)) and (buf[:, E:] == 7).all()
+        assert torch.equal(ops.moe_route_backward(*a, **kw), full.to(l.dtype))
+
+
 def test_nothing_outside_the_gradient_is_written_and_bad_ids():
     ops = _ops()
     buf = torch.full((12, 40), 7.0, device="cuda")

@@ -160,13 +160,13 @@ def test_router_refusals(lib):
     assert lib.mpm_moe_route_workspace_bytes(0, 16) == 0
     assert f(l=Q) == ALIGN and f(bias=Q, sc=1) == ALIGN and f(ws=Q) == ALIGN
 
-    def b(l=P, dt=1, T=4, E=16, ld=16, k=2, ids=P, counts=P, n=P, dprob=P, dloss=P, out=P, ldd=16):
+    def b(l=P, dt=1, T=4, E=16, ld=16, k=2, ids=P, counts=P, n=P, dprob=P, dloss=P, out=P, odt=1, ldd=16):
         return lib.mpm_moe_route_backward(l, dt, T, E, ld, k, 0, 1, 1.0, None, None, ids, counts, n, dprob,
-                                          dloss, out, ldd, None)
+                                          dloss, out, odt, ldd, None)
 
     assert b(l=None) == NULL and b(out=None) == NULL and b(ids=None) == NULL
     assert b(counts=None) == NULL and b(n=None) == NULL
-    assert b(ldd=15) == SHAPE and b(T=0) == SHAPE and b(k=20) == SHAPE
+    assert b(odt=2) == UNSUP and b(ldd=15) == SHAPE and b(T=0) == SHAPE and b(k=20) == SHAPE
     assert b(out=Q) == ALIGN and b(dprob=Q) == ALIGN
 
     def d(dout=P, T=4, k=2, H=64, cap=128, y=P):
@@ -230,7 +230,7 @@ def test_binding_refusals(lib):
     with pytest.raises(ValueError, match="dprob"):
         ops.moe_route_backward(l, ids, c, n, dprob=torch.zeros(4, 3))
     with pytest.raises(TypeError, match="out"):
-        ops.moe_route_backward(l, ids, c, n, out=torch.zeros(4, 16, dtype=bf))
+        ops.moe_route_backward(l, ids, c, n, out=torch.zeros(4, 16).half())
     with pytest.raises(ValueError, match="match"):
         ops.moe_combine_dprob(x, torch.zeros(128, 32, dtype=bf), ids.view(-1), torch.zeros(4, 2))
     with pytest.raises(ValueError, match="inv_perm"):
