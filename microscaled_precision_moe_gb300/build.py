@@ -1,8 +1,11 @@
-"""Build libmpm.so in-tree with nvcc for sm_103a (no cmake, no torch extension).
+"""Build libmpm.so and its torch binding in-tree (nvcc for sm_103a and g++; no
+cmake).
 
 Each .cu file compiles to an object in parallel; the objects link into
-``microscaled_precision_moe_gb300/libmpm.so``.  Rebuilds only when a source or
-header is newer than the library.
+``microscaled_precision_moe_gb300/libmpm.so``.  ``csrc/binding.cpp``, which
+marshals torch tensors into some of the library's calls, compiles beside them
+against the headers of the running torch and links into ``_binding.so``.
+Rebuilds only when a source or header is newer than either.
 
     python -m microscaled_precision_moe_gb300.build [--force] [--verbose]
 """
@@ -15,12 +18,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmpm.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -44,38 +50,59 @@ def _headers():
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(f) > t for f in _sources() + _headers() + [__file__])
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    return any(os.path.getmtime(f) > t for f in _sources() + _headers() + [BINDING_SRC, __file__])
 
 
-def _compile(src: str, verbose: bool, extra) -> str:
-    obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-    cmd = [nvcc(), *ARCH, *NVCC_FLAGS, *extra, "-c", src, "-o", obj]
+def _run(cmd, what: str, verbose: bool = False):
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
     if verbose and (r.stdout or r.stderr):
         print(r.stdout + r.stderr, flush=True)
+
+
+def _compile(src: str, verbose: bool, extra) -> str:
+    obj = os.path.join(BUILD, os.path.basename(src) + ".o")
+    _run([nvcc(), *ARCH, *NVCC_FLAGS, *extra, "-c", src, "-o", obj], f"nvcc {src}", verbose)
+    return obj
+
+
+def _compile_binding(verbose: bool) -> str:
+    from torch.utils.cpp_extension import include_paths
+    import torch
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    obj = os.path.join(BUILD, "binding.cpp.o")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+          "-I", os.path.join(ROOT, "include"), *[f for p in inc for f in ("-isystem", p)],
+          "-c", BINDING_SRC, "-o", obj], f"g++ {BINDING_SRC}", verbose)
     return obj
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not needs_build():
         return LIB
+    from torch.utils.cpp_extension import library_paths
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_compile_binding, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose, list(extra)), srcs))
+        binding = binding.result()
     tmp = LIB + ".tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], "link of libmpm.so")
     os.replace(tmp, LIB)
+    tmp = BINDING + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, binding, "-L", PKG, "-l:libmpm.so",
+          *[f for p in library_paths() for f in ("-L", p)], "-lc10", "-lc10_cuda", "-ltorch_cpu",
+          "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "link of _binding.so")
+    os.replace(tmp, BINDING)
     return LIB
 
 

@@ -13,38 +13,31 @@ import torch
 
 from . import _lib as L
 
-_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-
 
 def _ptr(t):
     return None if t is None else C.c_void_p(t.data_ptr())
-
-
-def _dp(t):
-    """A nullable tensor's address."""
-    return None if t is None else t.data_ptr()
-
-
-def _mat(t, name, M, K):
-    """Row pitch in elements of a bf16 [M, K] with dense rows (torch leaves the
-    stride of a one-row matrix open)."""
-    if t.dtype is not _BF16 or t.shape != (M, K):
-        _check_rows(t, name)
-        raise ValueError(f"{name}: expected shape {(M, K)}, got {tuple(t.shape)}")
-    ld, one = t.stride()
-    if one != 1 and K != 1:
-        _check_rows(t, name)
-    return ld if ld >= K or M > 1 else K
 
 
 def _stream(dev=None):
     return C.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _raw_stream(dev):
-    """The device's current stream as an integer: the address _stream gives,
-    without building a Stream object (0.1 against 2.1 us a call on the host)."""
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+_native_module = None
+
+
+def _native():
+    """The C++ binding of the norm and router calls (csrc/binding.cpp): the
+    same kind of checks and allocations as below, in a third of the time."""
+    global _native_module
+    if _native_module is None:
+        L.load()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise L.MpmError(f"_binding.so not usable ({e}); build it with "
+                             f"`python -m microscaled_precision_moe_gb300.build`") from e
+        _native_module = _binding
+    return _native_module
 
 
 def _need_cuda(*ts):
@@ -367,26 +360,7 @@ def moe_gather_mxfp8(q, s, perm, seg, E: int, k: int, cap: int, out=None):
     """Row-wise MXFP8 rows (codes [T, K], tiled scales) -> the same two in the
     permuted layout of cap rows: the row-wise bytes mxfp8_quantize_gather gives
     for the bf16 rows they came from."""
-    lib = L.load()
-    _check(q, "q", torch.uint8, dim=2, contiguous=True)
-    T, K = q.shape
-    if K % 32 != 0:
-        raise ValueError(f"q: K = {K} is not a multiple of the 32-value MXFP8 block")
-    _check(s, "s", torch.uint8, contiguous=True, min_numel=scale_bytes(T, K // 32))
-    _check_route(perm, seg, E, cap)
-    dev = q.device
-    if out is None:
-        out = (torch.empty(cap, K, dtype=torch.uint8, device=dev),
-               torch.empty(scale_bytes(cap, K // 32), dtype=torch.uint8, device=dev))
-    dq, ds = out
-    _check(dq, "out codes", torch.uint8, contiguous=True, min_numel=cap * K)
-    _check(ds, "out scales", torch.uint8, contiguous=True, min_numel=scale_bytes(cap, K // 32))
-    _need_cuda(q, s, perm, seg, dq, ds)
-    st = lib.mpm_moe_gather_mxfp8(q.data_ptr(), s.data_ptr(), T, K, k, perm.data_ptr(),
-                                  seg.data_ptr(), E, cap, dq.data_ptr(), ds.data_ptr(),
-                                  _raw_stream(dev))
-    L.check(st, "mpm_moe_gather_mxfp8")
-    return dq, ds
+    return (_native_module or _native()).moe_gather_mxfp8(q, s, perm, seg, E, k, cap, out)
 
 
 def moe_combine(y_perm, inv_perm, T: int, k: int, out=None):
@@ -409,36 +383,10 @@ def moe_combine_dprob(dout, y_perm, inv_perm, prob, out=None):
     """dprob fp32 [T, k]: the gradient of the routing weights prob [T, k] from
     dout bf16 [T, H] and the expert outputs y_perm bf16 [capacity, H] that the
     forward combined (0 where the weight is 0 or the slot has no row)."""
-    lib = L.load()
-    _check(dout, "dout", torch.bfloat16, dim=2, contiguous=True)
-    _check(y_perm, "y_perm", torch.bfloat16, dim=2, contiguous=True)
-    _check(prob, "prob", torch.float32, dim=2, contiguous=True)
-    T, k = prob.shape
-    H = dout.shape[1]
-    if dout.shape[0] != T or y_perm.shape[1] != H:
-        raise ValueError(f"dout {tuple(dout.shape)} and y_perm {tuple(y_perm.shape)} do not match "
-                         f"prob {tuple(prob.shape)}")
-    _check(inv_perm, "inv_perm", torch.int32, contiguous=True, min_numel=T * k)
-    if out is None:
-        out = torch.empty(T, k, dtype=torch.float32, device=dout.device)
-    _check(out, "out", torch.float32, contiguous=True, min_numel=T * k)
-    _need_cuda(dout, y_perm, inv_perm, prob, out)
-    st = lib.mpm_moe_combine_dprob(dout.data_ptr(), y_perm.data_ptr(), inv_perm.data_ptr(),
-                                   prob.data_ptr(), T, k, H, y_perm.shape[0], out.data_ptr(),
-                                   _raw_stream(dout.device))
-    L.check(st, "mpm_moe_combine_dprob")
-    return out
+    return (_native_module or _native()).moe_combine_dprob(dout, y_perm, inv_perm, prob, out)
 
 
 # ------------------------------------------------------------------ residual RMSNorm
-
-def _weight_dtype(weight, K):
-    if weight.dtype is not _F32 and weight.dtype is not _BF16:
-        raise TypeError(f"weight: expected bf16 or fp32, got {weight.dtype}")
-    if weight.shape != (K,) or not weight.is_contiguous():
-        raise ValueError(f"weight: expected a contiguous [{K}], got shape {tuple(weight.shape)}")
-    return L.DTYPE_F32 if weight.dtype is _F32 else L.DTYPE_BF16
-
 
 def add_rmsnorm(x, weight, residual=None, eps=1e-6, want_y=True, quantize=False, out=None):
     """h = x + residual and y = h / rms(h) * weight of bf16 [M, K] rows.
@@ -446,57 +394,9 @@ def add_rmsnorm(x, weight, residual=None, eps=1e-6, want_y=True, quantize=False,
     Returns a dict (``out`` when given, its buffers reused): y bf16 [M, K]
     (unless want_y is False), h bf16 [M, K] (with a residual), rstd fp32 [M],
     and with ``quantize`` row_q u8 [M, K], row_s (tiled [M, K/32]): the bytes
-    mxfp8_quantize(y, colwise=False) gives.  weight: bf16 or fp32 [K]."""
-    lib = L.load()
-    if x.dim() != 2:
-        _check_rows(x, "x")
-    M, K = x.shape
-    ldx = _mat(x, "x", M, K)
-    wdt = _weight_dtype(weight, K)
-    dev = x.device
-    y = h = q = s = None
-    ldr = ldh = ldy = 0
-    o = {} if out is None else out
-    if residual is not None:
-        ldr = _mat(residual, "residual", M, K)
-        h = o.get("h")
-        if h is None:
-            h = o["h"] = torch.empty(M, K, dtype=_BF16, device=dev)
-            ldh = K
-        else:
-            ldh = _mat(h, "h", M, K)
-    if want_y:
-        y = o.get("y")
-        if y is None:
-            y = o["y"] = torch.empty(M, K, dtype=_BF16, device=dev)
-            ldy = K
-        else:
-            ldy = _mat(y, "y", M, K)
-    rstd = o.get("rstd")
-    if rstd is None:
-        rstd = o["rstd"] = torch.empty(M, dtype=_F32, device=dev)
-    else:
-        _check(rstd, "rstd", _F32, contiguous=True, min_numel=M)
-    if quantize:
-        if K % 32 != 0:
-            raise ValueError(f"x: K = {K} is not a multiple of the 32-value MXFP8 block")
-        sb = scale_bytes(M, K // 32)
-        q, s = o.get("row_q"), o.get("row_s")
-        if q is None:
-            q = o["row_q"] = torch.empty(M, K, dtype=_U8, device=dev)
-        else:
-            _check(q, "row_q", _U8, contiguous=True, min_numel=M * K)
-        if s is None:
-            s = o["row_s"] = torch.empty(sb, dtype=_U8, device=dev)
-        else:
-            _check(s, "row_s", _U8, contiguous=True, min_numel=sb)
-    _need_cuda(x, weight, residual, y, h, rstd, q, s)
-    st = lib.mpm_add_rmsnorm(x.data_ptr(), M, K, ldx, _dp(residual), ldr, weight.data_ptr(), wdt, eps,
-                             _dp(h), ldh, _dp(y), ldy, rstd.data_ptr(), _dp(q), _dp(s),
-                             _raw_stream(dev))
-    if st:
-        L.check(st, "mpm_add_rmsnorm")
-    return o
+    mxfp8_quantize(y, colwise=False) gives.  Entries of ``out`` that the call
+    does not make stay as they are.  weight: bf16 or fp32 [K]."""
+    return (_native_module or _native()).add_rmsnorm(x, weight, residual, eps, want_y, quantize, out)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -511,76 +411,11 @@ def add_rmsnorm_backward(dy, h, rstd, weight, dy2=None, dh=None, want_dw=True, o
     residual stream; h, rstd: the forward's (h = x without a residual).
     ``out``: (dx, dw) buffers; ws: uint8 workspace of
     add_rmsnorm_backward_workspace_bytes(M, K)."""
-    lib = L.load()
-    if dy.dim() != 2:
-        _check_rows(dy, "dy")
-    M, K = dy.shape
-    lddy = _mat(dy, "dy", M, K)
-    ldh = _mat(h, "h", M, K)
-    wdt = _weight_dtype(weight, K)
-    _check(rstd, "rstd", _F32, contiguous=True, min_numel=M)
-    lddy2 = 0 if dy2 is None else _mat(dy2, "dy2", M, K)
-    lddh = 0 if dh is None else _mat(dh, "dh", M, K)
-    dev = dy.device
-    wsb = 0
-    if out is None:
-        dx, lddx = torch.empty(M, K, dtype=_BF16, device=dev), K
-        dw = torch.empty(K, dtype=_F32, device=dev) if want_dw else None
-    else:
-        dx, dw = out
-        lddx = _mat(dx, "dx", M, K)
-        if want_dw:
-            _check(dw, "dw", _F32, contiguous=True, min_numel=K)
-        else:
-            dw = None
-    if want_dw:
-        wsb = add_rmsnorm_backward_workspace_bytes(M, K)
-        if ws is None:
-            ws = torch.empty(wsb, dtype=_U8, device=dev)
-        else:
-            _check(ws, "ws", _U8, contiguous=True, min_numel=wsb)
-    else:
-        ws = None
-    _need_cuda(dy, h, rstd, weight, dy2, dh, dx, dw, ws)
-    st = lib.mpm_add_rmsnorm_backward(dy.data_ptr(), lddy, _dp(dy2), lddy2, h.data_ptr(), ldh,
-                                      rstd.data_ptr(), weight.data_ptr(), wdt, _dp(dh), lddh, M, K,
-                                      dx.data_ptr(), lddx, _dp(dw), _dp(ws), wsb, _raw_stream(dev))
-    if st:
-        L.check(st, "mpm_add_rmsnorm_backward")
-    return dx, dw
+    return (_native_module or _native()).add_rmsnorm_backward(dy, h, rstd, weight, dy2, dh, want_dw,
+                                                              out, ws)
 
 
 # ------------------------------------------------------------------ router
-
-_SCORES = {"softmax": L.SCORE_SOFTMAX, "sigmoid": L.SCORE_SIGMOID}
-
-
-def _route_args(logits, score, bias, token_mask):
-    """(T, E, row pitch, score code, logits dtype code) of a router call, its
-    inputs checked."""
-    dt = logits.dtype
-    if dt is not _F32 and dt is not _BF16:
-        raise TypeError(f"logits: expected bf16 or fp32, got {dt}")
-    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] != 1):
-        raise ValueError(f"logits: expected [T, E] with dense rows, got shape {tuple(logits.shape)}")
-    sc = _SCORES.get(score)
-    if sc is None:
-        raise ValueError(f"score must be one of {tuple(_SCORES)}, got {score!r}")
-    T, E = logits.shape
-    if bias is not None:
-        _check(bias, "bias", _F32, contiguous=True)
-        if bias.shape != (E,):
-            raise ValueError(f"bias: expected [{E}], got shape {tuple(bias.shape)}")
-        if score != "sigmoid":
-            raise ValueError("bias: the choice bias belongs to sigmoid scores")
-    if token_mask is not None:
-        if token_mask.dtype is not torch.bool and token_mask.dtype is not _U8:
-            raise TypeError(f"token_mask: expected bool or uint8, got {token_mask.dtype}")
-        if token_mask.shape != (T,) or not token_mask.is_contiguous():
-            raise ValueError(f"token_mask: expected a contiguous [{T}], got {tuple(token_mask.shape)}")
-    ld = logits.stride(0)
-    return T, E, ld if ld >= E or T > 1 else E, sc, L.DTYPE_F32 if dt is _F32 else L.DTYPE_BF16
-
 
 @functools.lru_cache(maxsize=4096)
 def moe_route_workspace_bytes(T: int, E: int) -> int:
@@ -599,38 +434,8 @@ def moe_route(logits, k: int, score="softmax", normalize=True, scale=1.0, bias=N
     that get weight 0 and are not counted.  Experts masked with -inf or the
     type's lowest value are out of reach.  ws: uint8 workspace of
     moe_route_workspace_bytes(T, E)."""
-    lib = L.load()
-    T, E, ld, sc, ldt = _route_args(logits, score, bias, token_mask)
-    dev = logits.device
-    if out is None:
-        ids = torch.empty(T, k, dtype=_I32, device=dev)
-        prob = torch.empty(T, k, dtype=_F32, device=dev)
-        counts = torch.empty(E, dtype=_I32, device=dev)
-        load = torch.empty(E, dtype=_F32, device=dev)
-        n_tokens = torch.empty(1, dtype=_I32, device=dev)
-        loss = torch.empty(1, dtype=_F32, device=dev)
-        out = {"ids": ids, "prob": prob, "counts": counts, "load": load, "n_tokens": n_tokens,
-               "loss": loss}
-    else:
-        for name, dt, n in (("ids", _I32, T * k), ("prob", _F32, T * k), ("counts", _I32, E),
-                            ("load", _F32, E), ("n_tokens", _I32, 1), ("loss", _F32, 1)):
-            _check(out[name], name, dt, contiguous=True, min_numel=n)
-        ids, prob, counts, load, n_tokens, loss = (out[n] for n in ("ids", "prob", "counts", "load",
-                                                                    "n_tokens", "loss"))
-    wsb = moe_route_workspace_bytes(T, E)
-    if ws is None:
-        if wsb:
-            ws = torch.empty(wsb, dtype=_U8, device=dev)
-    else:
-        _check(ws, "ws", _U8, contiguous=True, min_numel=wsb)
-    _need_cuda(logits, bias, token_mask, ws, ids, prob, counts, load, n_tokens, loss)
-    st = lib.mpm_moe_route(logits.data_ptr(), ldt, T, E, ld, k, sc, 1 if normalize else 0, scale,
-                           _dp(bias), _dp(token_mask), ids.data_ptr(), prob.data_ptr(),
-                           counts.data_ptr(), load.data_ptr(), n_tokens.data_ptr(), loss.data_ptr(),
-                           _dp(ws), wsb, _raw_stream(dev))
-    if st:
-        L.check(st, "mpm_moe_route")
-    return out
+    return (_native_module or _native()).moe_route(logits, k, score, normalize, scale, bias,
+                                                   token_mask, out, ws)
 
 
 def moe_route_backward(logits, ids, counts, n_tokens, dprob=None, dloss=None, score="softmax",
@@ -639,38 +444,9 @@ def moe_route_backward(logits, ids, counts, n_tokens, dprob=None, dloss=None, sc
     moe_route with the same arguments, from dprob fp32 [T, k] and / or dloss
     fp32 [1]; ids, counts and n_tokens are the forward's.  The choice and the
     counts are constants."""
-    lib = L.load()
-    T, E, ld, sc, ldt = _route_args(logits, score, bias, token_mask)
-    dev = logits.device
-    _check(ids, "ids", _I32, dim=2, contiguous=True)
-    k = ids.shape[1]
-    if ids.shape[0] != T:
-        raise ValueError(f"ids: expected [{T}, k], got shape {tuple(ids.shape)}")
-    _check(counts, "counts", _I32, contiguous=True, min_numel=E)
-    _check(n_tokens, "n_tokens", _I32, min_numel=1)
-    if dprob is not None:
-        _check(dprob, "dprob", _F32, contiguous=True)
-        if dprob.shape != ids.shape:
-            raise ValueError(f"dprob: expected {tuple(ids.shape)}, got shape {tuple(dprob.shape)}")
-    if dloss is not None:
-        _check(dloss, "dloss", _F32, min_numel=1)
-    if out is None:
-        out, ldd, odt = torch.empty(T, E, dtype=logits.dtype, device=dev), E, ldt
-    else:
-        if out.dtype is not _F32 and out.dtype is not _BF16:
-            raise TypeError(f"out: expected bf16 or fp32, got {out.dtype}")
-        odt = L.DTYPE_F32 if out.dtype is _F32 else L.DTYPE_BF16
-        if out.shape != logits.shape or (out.stride(1) != 1 and E != 1):
-            raise ValueError(f"out: expected {tuple(logits.shape)} with dense rows")
-        ldd = max(out.stride(0), E) if T == 1 else out.stride(0)
-    _need_cuda(logits, ids, counts, n_tokens, dprob, dloss, bias, token_mask, out)
-    st = lib.mpm_moe_route_backward(logits.data_ptr(), ldt, T, E, ld, k, sc, 1 if normalize else 0,
-                                    scale, _dp(bias), _dp(token_mask), ids.data_ptr(),
-                                    counts.data_ptr(), n_tokens.data_ptr(), _dp(dprob), _dp(dloss),
-                                    out.data_ptr(), odt, ldd, _raw_stream(dev))
-    if st:
-        L.check(st, "mpm_moe_route_backward")
-    return out
+    return (_native_module or _native()).moe_route_backward(logits, ids, counts, n_tokens, dprob,
+                                                            dloss, score, normalize, scale, bias,
+                                                            token_mask, out)
 
 
 # ------------------------------------------------------------------ GEMM
