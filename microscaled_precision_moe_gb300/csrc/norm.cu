@@ -24,6 +24,7 @@ constexpr int kNormMaxWarps = kNormMaxThreads / 32;
 constexpr int kNormTeams = 4;            // rows of one warp each in a block
 constexpr int kRowsAtATime = 4;          // rows of up to 8 values a thread
 constexpr int kRingStages = 8;           // most stages of the backward's ring
+constexpr int kRingWords = 2;            // 16-byte words of each operand a thread takes there
 
 MPM_DEV uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -258,20 +259,18 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) add_
 
 // Rows of 16-byte aligned operands stream through a ring of S stages in shared
 // memory, one row's operands each, by bulk copies that thread 0 issues: S - 1
-// rows are in flight whatever the threads are doing.  One thread per 8 columns.
-// A stage is refilled after the block barrier of the next row's reduction, by
-// when every thread is past its last read of it.
-template <bool TWO, bool RES>
-__global__ void __launch_bounds__(1024) add_rmsnorm_bwd_ring_kernel(const NormBwd p, int S) {
+// rows are in flight whatever the threads are doing.  A thread takes C words of
+// 8 columns.  A stage is refilled after the block barrier of the next row's
+// reduction, by when every thread is past its last read of it.
+template <int C, bool TWO, bool RES>
+__global__ void __launch_bounds__(1024 / C) add_rmsnorm_bwd_ring_kernel(const NormBwd p, int S) {
   constexpr int NT = 2 + (TWO ? 1 : 0) + (RES ? 1 : 0);
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float sh[2][32];
   __shared__ __align__(8) uint64_t bars[kRingStages];
-  const int t = threadIdx.x;
+  const int t = threadIdx.x, nt = blockDim.x;
   const uint32_t row_bytes = (uint32_t)p.K * 2, stage_bytes = NT * row_bytes;
   const uint32_t base = smem_u32(ring), bar0 = smem_u32(bars);
-  const int k = t * 8;
-  const bool in = k < p.K;
   if (t == 0) {
     for (int s = 0; s < S; ++s) mbar_init(bar0 + 8 * s, 1);
     fence_mbar_init();
@@ -291,14 +290,16 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_ring_kernel(const NormBw
     long long row = blockIdx.x;
     for (int s = 0; s < S && row < p.M; ++s, row += step) issue(row, s);
   }
-  uint64_t w[4], dw[4];
-  {
+  uint64_t w[C][4], dw[C][4];
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int k = (i * nt + t) * 8;
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    if (in) load_weight<8>(p.w, p.w_f32, k, v);
+    if (k < p.K) load_weight<8>(p.w, p.w_f32, k, v);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) { w[j] = f32x2(v[2 * j], v[2 * j + 1]); dw[j] = 0; }
+    for (int j = 0; j < 4; ++j) { w[i][j] = f32x2(v[2 * j], v[2 * j + 1]); dw[i][j] = 0; }
   }
   __syncthreads();
   const float rk = __fdiv_rn(1.0f, (float)p.K);
@@ -309,23 +310,28 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_ring_kernel(const NormBw
   for (; row < p.M; row += step, ++it) {
     const float next_rstd = row + step < p.M ? p.rstd[row + step] : 0.0f;
     const bool ok = mbar_wait(bar0 + 8 * cur.s, cur.phase, p.status);
-    const uint8_t* st = ring + cur.s * stage_bytes + t * 16;
-    RawBf16<8> a, b, h;
-    a.zero(); b.zero(); h.zero();
-    if (in) {
-      a.load(reinterpret_cast<const uint16_t*>(st));
-      h.load(reinterpret_cast<const uint16_t*>(st + row_bytes));
-      if (TWO) b.load(reinterpret_cast<const uint16_t*>(st + 2 * row_bytes));
-    }
-    uint64_t u[4], c2 = 0;
+    const uint8_t* st = ring + cur.s * stage_bytes;
+    RawBf16<8> h[C];
+    uint64_t u[C][4], c2 = 0;
     const uint64_t rstd2 = f32x2(rstd, rstd);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint64_t y = TWO ? add2(widen2(a.w[j]), widen2(b.w[j])) : widen2(a.w[j]);
-      const uint64_t hh = widen2(h.w[j]), v = mul_f32x2(y, rstd2);
-      dw[j] = fma2(v, hh, dw[j]);
-      u[j] = mul_f32x2(v, w[j]);
-      c2 = fma2(u[j], hh, c2);
+    for (int i = 0; i < C; ++i) {
+      const int k = (i * nt + t) * 8;
+      RawBf16<8> a, b;
+      a.zero(); b.zero(); h[i].zero();
+      if (k < p.K) {
+        a.load(reinterpret_cast<const uint16_t*>(st) + k);
+        h[i].load(reinterpret_cast<const uint16_t*>(st + row_bytes) + k);
+        if (TWO) b.load(reinterpret_cast<const uint16_t*>(st + 2 * row_bytes) + k);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t y = TWO ? add2(widen2(a.w[j]), widen2(b.w[j])) : widen2(a.w[j]);
+        const uint64_t hh = widen2(h[i].w[j]), v = mul_f32x2(y, rstd2);
+        dw[i][j] = fma2(v, hh, dw[i][j]);
+        u[i][j] = mul_f32x2(v, w[i][j]);
+        c2 = fma2(u[i][j], hh, c2);
+      }
     }
     float c, chi;
     f32x2_split(c2, c, chi);
@@ -341,13 +347,16 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_ring_kernel(const NormBw
       if (ahead < p.M) issue(ahead, cur.s == 0 ? S - 1 : cur.s - 1);
     }
     const float f = -__fmul_rn(__fmul_rn(rstd, rstd), __fmul_rn(c, rk));
-    if (in) {
+    const uint64_t f2 = f32x2(f, f);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int k = (i * nt + t) * 8;
+      if (k >= p.K) continue;
       RawBf16<8> r, o;
-      if (RES) r.load(reinterpret_cast<const uint16_t*>(st + (NT - 1) * row_bytes));
-      const uint64_t f2 = f32x2(f, f);
+      if (RES) r.load(reinterpret_cast<const uint16_t*>(st + (NT - 1) * row_bytes) + k);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        uint64_t d = fma2(widen2(h.w[j]), f2, u[j]);
+        uint64_t d = fma2(widen2(h[i].w[j]), f2, u[i][j]);
         if (RES) d = add2(d, widen2(r.w[j]));
         float lo, hi;
         f32x2_split(d, lo, hi);
@@ -359,15 +368,20 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_ring_kernel(const NormBw
     cur.next(S);
   }
   pdl_launch_dependents();
-  if (!p.dw || !in) return;
-  float* out = (gridDim.x == 1 ? p.dw : p.part + (long long)blockIdx.x * p.K) + k;
-  if (reinterpret_cast<uintptr_t>(out) % 16 == 0) {
-    reinterpret_cast<ulonglong2*>(out)[0] = make_ulonglong2(dw[0], dw[1]);
-    reinterpret_cast<ulonglong2*>(out)[1] = make_ulonglong2(dw[2], dw[3]);
-    return;
-  }
+  if (!p.dw) return;
+  float* out = gridDim.x == 1 ? p.dw : p.part + (long long)blockIdx.x * p.K;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) f32x2_split(dw[j], out[2 * j], out[2 * j + 1]);
+  for (int i = 0; i < C; ++i) {
+    const int k = (i * nt + t) * 8;
+    if (k >= p.K) continue;
+    if (reinterpret_cast<uintptr_t>(out) % 16 == 0) {
+      reinterpret_cast<ulonglong2*>(out + k)[0] = make_ulonglong2(dw[i][0], dw[i][1]);
+      reinterpret_cast<ulonglong2*>(out + k)[1] = make_ulonglong2(dw[i][2], dw[i][3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f32x2_split(dw[i][j], out[k + 2 * j], out[k + 2 * j + 1]);
+    }
+  }
 }
 
 // The other rows take two kernels: dx from one row a block (short rows: one a
@@ -498,16 +512,19 @@ static unsigned norm_threads(int K, int per_thread) {
   return (unsigned)((n + 31) / 32 * 32);
 }
 
-// Rings: as many blocks an SM as 1024 threads make, each with `stages` stages of
-// `stage` bytes (0 stages: rows too long for two)
+// The ring form: blocks an SM, and the stages that fit beside one another
 struct NormRing { unsigned threads; int blocks, stages, smem; };
+// 512 threads an SM, 16 columns each (8 columns and 1024 threads: 15.8 against
+// 15.1 us at 4093 x 1544, the same at 8192 x 2048)
+static int ring_blocks(int K) {
+  const int n = 512 / (int)norm_threads(K, 8 * kRingWords);
+  return n < 1 ? 1 : n;
+}
 static NormRing norm_ring(int K, int per_thread, int stage) {
   NormRing r{norm_threads(K, per_thread), 0, 0, 0};
-  if (r.threads > 1024) return r;
-  r.blocks = 1024 / (int)r.threads;
+  r.blocks = ring_blocks(K);
   r.stages = (222 * 1024 / r.blocks - 1024) / stage;
   if (r.stages > kRingStages) r.stages = kRingStages;
-  if (r.stages < 2) r.stages = 0;
   r.smem = r.stages * stage;
   return r;
 }
@@ -553,8 +570,7 @@ cudaError_t launch_add_rmsnorm(const NormFwd& p, cudaStream_t st) {
 // Blocks of the backward's ring, each with its own partial dw (the two-kernel
 // form makes no more)
 long long rmsnorm_backward_parts(long long M, int K) {
-  const int threads = (int)norm_threads(K, 8);
-  const long long most = 152ll * (threads < 1024 ? 1024 / threads : 1);
+  const long long most = 152ll * ring_blocks(K);
   return M < most ? M : most;
 }
 
@@ -569,7 +585,7 @@ static cudaError_t norm_dw(const NormBwd& p, long long parts, cudaStream_t st) {
 
 template <auto kernel>
 static cudaError_t norm_bwd_ring(const NormBwd& p, int operands, cudaStream_t st) {
-  const NormRing r = norm_ring(p.K, 8, 2 * p.K * operands);
+  const NormRing r = norm_ring(p.K, 8 * kRingWords, 2 * p.K * operands);
   const long long blocks = rmsnorm_backward_parts(p.M, p.K);
   const cudaError_t err = launch_ring<kernel>(r, blocks, p, st);
   return err != cudaSuccess ? err : norm_dw(p, blocks, st);
@@ -602,10 +618,10 @@ cudaError_t launch_add_rmsnorm_backward(const NormBwd& p, cudaStream_t st) {
     if (p.K <= 256) return norm_bwd_two<8, 1, true>(p, st);
     if (p.K > 8192) return norm_bwd_two<8, 4, false>(p, st);
     if (p.dy2)
-      return p.dh ? norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<true, true>>(p, 4, st)
-                  : norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<true, false>>(p, 3, st);
-    return p.dh ? norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<false, true>>(p, 3, st)
-                : norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<false, false>>(p, 2, st);
+      return p.dh ? norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<kRingWords, true, true>>(p, 4, st)
+                  : norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<kRingWords, true, false>>(p, 3, st);
+    return p.dh ? norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<kRingWords, false, true>>(p, 3, st)
+                : norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<kRingWords, false, false>>(p, 2, st);
   }
   if (p.K <= 128) return norm_bwd_two<1, 4, true>(p, st);
   if (p.K <= 4 * kNormMaxThreads) return norm_bwd_two<1, 4, false>(p, st);
