@@ -384,7 +384,7 @@ mpm_status mpm_add_rmsnorm(const void* x, int64_t M, int64_t K, int64_t ldx, con
   p.h = static_cast<uint16_t*>(h); p.ldh = ldh;
   p.y = static_cast<uint16_t*>(y); p.ldy = ldy;
   p.rstd = rstd; p.q = row_q; p.s = row_s; p.s_cols_pad = pad_to(K / 32, 4);
-  p.M = M; p.K = (int)K;
+  p.M = M; p.K = (int)K; p.rk = 1.0f / (float)K;
   return cuda_status(mpm::launch_add_rmsnorm(p, stream));
 }
 

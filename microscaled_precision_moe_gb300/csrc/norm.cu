@@ -9,9 +9,8 @@
 // makes of y: a rollout that reads these codes and a training step that
 // quantises the stored y then run on the same operands.
 //
-// A row is held in the registers of the threads of one block (VEC consecutive
-// elements per load, IT loads per thread and operand), R rows at a time with all
-// their loads in flight together, so every operand is read once.
+// A row is held in the registers of the threads of one block, or of one warp, so
+// every operand is read once.
 #include <atomic>
 #include "norm.cuh"
 #include "launch.cuh"
@@ -22,7 +21,6 @@ namespace mpm {
 constexpr int kNormMaxThreads = 512;
 constexpr int kNormMaxWarps = kNormMaxThreads / 32;
 constexpr int kNormTeams = 4;            // rows of one warp each in a block
-constexpr int kRowsAtATime = 4;          // rows of up to 8 values a thread
 constexpr int kRingStages = 8;           // most stages of the backward's ring
 constexpr int kRingWords = 2;            // 16-byte words of each operand a thread takes there
 
@@ -75,6 +73,34 @@ MPM_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 }
 // a pair of bf16 as two fp32
 MPM_DEV uint64_t widen2(uint32_t w) { return f32x2(bf16lo(w), bf16hi(w)); }
+
+// What a vector is computed in: pairs of fp32 (VEC = 8), or one
+template <int VEC>
+struct Lanes {
+  using T = uint64_t;
+  static constexpr int N = VEC / 2;
+  static MPM_DEV T widen(uint32_t w) { return widen2(w); }
+  static MPM_DEV T splat(float v) { return f32x2(v, v); }
+  static MPM_DEV T pick(const float (&v)[VEC], int j) { return f32x2(v[2 * j], v[2 * j + 1]); }
+  static MPM_DEV T add(T a, T b) { return add2(a, b); }
+  static MPM_DEV T mul(T a, T b) { return mul_f32x2(a, b); }
+  static MPM_DEV T fma(T a, T b, T c) { return fma2(a, b, c); }
+  static MPM_DEV float sum(T v) { float lo, hi; f32x2_split(v, lo, hi); return __fadd_rn(lo, hi); }
+  static MPM_DEV uint32_t bf16(T v) { float lo, hi; f32x2_split(v, lo, hi); return pack_bf16(lo, hi); }
+};
+template <>
+struct Lanes<1> {
+  using T = float;
+  static constexpr int N = 1;
+  static MPM_DEV T widen(uint32_t w) { return bf16lo(w); }
+  static MPM_DEV T splat(float v) { return v; }
+  static MPM_DEV T pick(const float (&v)[1], int) { return v[0]; }
+  static MPM_DEV T add(T a, T b) { return __fadd_rn(a, b); }
+  static MPM_DEV T mul(T a, T b) { return __fmul_rn(a, b); }
+  static MPM_DEV T fma(T a, T b, T c) { return __fmaf_rn(a, b, c); }
+  static MPM_DEV float sum(T v) { return v; }
+  static MPM_DEV uint32_t bf16(T v) { return pack_bf16(v, 0.0f); }
+};
 
 template <int VEC>
 MPM_DEV void load_weight(const void* w, int f32, int k, float (&v)[VEC]) {
@@ -158,8 +184,17 @@ struct RingCursor {
   }
 };
 
+// VEC consecutive elements per load, IT loads per thread and operand, R rows per
+// team, all their loads in flight together.  Bound by the bytes: with a residual
+// and the 8-bit copy 9 + 1/32 bytes an element (x, r in; y, h, codes and scales
+// out).  16384 x 2048 takes 46.0 us and 32768 x 7168 takes 306.7 us, 6.6 and 6.9
+// TB/s.  The arithmetic is nearly as long as the copies, hence pairs of fp32:
+// with single ones and 8 columns a thread the two took 48.6 and 315 us (16
+// columns a thread alone: 47.6 and 312).
 template <int VEC, int IT, int R, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) add_rmsnorm_kernel(const NormFwd p) {
+  using L = Lanes<VEC>;
+  using T = typename L::T;
   __shared__ float sh[R][kNormMaxWarps];
   pdl_wait();
   pdl_launch_dependents();
@@ -168,56 +203,66 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) add_
   const long long row0 = team.index * R;
   RawBf16<VEC> x[R][IT], res[R][IT];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int r = 0; r < R; ++r) {
+    const uint16_t* px = p.x + (row0 + r) * p.ldx;
+    const uint16_t* pr = p.r + (row0 + r) * p.ldr;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
       const int k = (i * nt + t) * VEC;
       x[r][i].zero();
       res[r][i].zero();
       if (k < p.K && row0 + r < p.M) {
-        x[r][i].load(p.x + (row0 + r) * p.ldx + k);
-        if (p.r) res[r][i].load(p.r + (row0 + r) * p.ldr + k);
+        x[r][i].load(px + k);
+        if (p.r) res[r][i].load(pr + k);
       }
     }
-  float h[R][IT][VEC], ss[R];
+  }
+  T h[R][IT][L::N];
+  float ss[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    ss[r] = 0.0f;
+    T s2 = L::splat(0.0f);
 #pragma unroll
     for (int i = 0; i < IT; ++i)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
+      for (int j = 0; j < L::N; ++j) {
         // x + 0 is x: no branch on whether there is a residual
-        h[r][i][j] = __fadd_rn(x[r][i].value(j), res[r][i].value(j));
-        ss[r] = __fmaf_rn(h[r][i][j], h[r][i][j], ss[r]);
+        h[r][i][j] = L::add(L::widen(x[r][i].w[j]), L::widen(res[r][i].w[j]));
+        s2 = L::fma(h[r][i][j], h[r][i][j], s2);
       }
+    ss[r] = L::sum(s2);
   }
   row_sums<WARP, R>(ss, sh);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    ss[r] = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss[r], (float)p.K), p.eps));
+    ss[r] = rsqrtf(__fmaf_rn(ss[r], p.rk, p.eps));
     if (t == 0 && p.rstd && row0 + r < p.M) p.rstd[row0 + r] = ss[r];
   }
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     const int k = (i * nt + t) * VEC;
     const bool in = k < p.K;
-    float w[VEC];
+    T w[L::N];
+    {
+      float v[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) w[j] = 0.0f;
-    if (in) load_weight<VEC>(p.w, p.w_f32, k, w);
+      for (int j = 0; j < VEC; ++j) v[j] = 0.0f;
+      if (in) load_weight<VEC>(p.w, p.w_f32, k, v);
+#pragma unroll
+      for (int j = 0; j < L::N; ++j) w[j] = L::pick(v, j);
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const long long row = row0 + r;
       const bool live = in && row < p.M;
-      RawBf16<VEC> o;
-      if (p.h && live) {
-        o.set(h[r][i]);
-        o.store(p.h + row * p.ldh + k);
-      }
+      const T rstd = L::splat(ss[r]);
+      RawBf16<VEC> oh, o;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) h[r][i][j] = __fmul_rn(__fmul_rn(h[r][i][j], ss[r]), w[j]);
-      o.set(h[r][i]);
+      for (int j = 0; j < L::N; ++j) {
+        oh.w[j] = L::bf16(h[r][i][j]);
+        o.w[j] = L::bf16(L::mul(L::mul(h[r][i][j], rstd), w[j]));
+      }
+      if (p.h && live) oh.store(p.h + row * p.ldh + k);
       if (p.y && live) o.store(p.y + row * p.ldy + k);
       if (!p.q) continue;
       // K % 32 == 0: a block of 32 lies in 32 / VEC neighbouring lanes
@@ -552,14 +597,14 @@ static cudaError_t norm_fwd(const NormFwd& p, cudaStream_t st) {
 cudaError_t launch_add_rmsnorm(const NormFwd& p, cudaStream_t st) {
   const bool v = p.K % 8 == 0 && vec8(p.x, p.ldx) && vec8(p.r, p.ldr) && vec8(p.h, p.ldh) &&
                  vec8(p.y, p.ldy) && vec8(p.w, 0);
-  // rows kRowsAtATime at a time where that leaves four blocks for every SM
-  const bool many = p.M >= kRowsAtATime * 152 * 4;
   if (v) {
-    if (p.K <= 256)
-      return p.M >= kRowsAtATime * kNormTeams * 152 ? norm_fwd<8, 1, kRowsAtATime, true>(p, st)
-                                                    : norm_fwd<8, 1, 1, true>(p, st);
-    if (p.K <= 8 * kNormMaxThreads)
-      return many ? norm_fwd<8, 1, kRowsAtATime, false>(p, st) : norm_fwd<8, 1, 1, false>(p, st);
+    // Short rows leave most of a block idle at its barrier: a warp each, two at a
+    // time where one has a load each at most.  Warp against block: 18.0 and 20.1
+    // us at 16384 x 768, but 25.6 and 24.4 at 16384 x 1024; two rows against one:
+    // 11.5 and 12.2 us at 32768 x 256, 9.1 and 10.1 at 32768 x 128.
+    if (p.K <= 256) return norm_fwd<8, 1, 2, true>(p, st);
+    if (p.K <= 512) return norm_fwd<8, 2, 1, true>(p, st);
+    if (p.K <= 768) return norm_fwd<8, 3, 1, true>(p, st);
     return p.K <= 16 * kNormMaxThreads ? norm_fwd<8, 2, 1, false>(p, st) : norm_fwd<8, 4, 1, false>(p, st);
   }
   if (p.K <= 128) return norm_fwd<1, 4, 1, true>(p, st);

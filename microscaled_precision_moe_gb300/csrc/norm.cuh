@@ -13,7 +13,7 @@ struct NormFwd {
   uint16_t* y; long long ldy;              // bf16 (nullable)
   float* rstd;                             // fp32 [M] (nullable)
   uint8_t* q; uint8_t* s; long long s_cols_pad;   // MXFP8 row copy of y (nullable)
-  long long M; int K;
+  long long M; int K; float rk;            // rk = 1 / K
 };
 cudaError_t launch_add_rmsnorm(const NormFwd& p, cudaStream_t st);
 
