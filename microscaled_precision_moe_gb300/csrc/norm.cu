@@ -15,6 +15,7 @@
 #include "norm.cuh"
 #include "launch.cuh"
 #include "mxfp8.cuh"
+#include "packed.cuh"
 
 namespace mpm {
 
@@ -60,20 +61,6 @@ struct RawBf16 {
 MPM_DEV float bf16_f(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 MPM_DEV uint16_t f_bf16(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
-// two fp32 operations at once, each lane the IEEE result of the scalar one
-MPM_DEV uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-MPM_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-// a pair of bf16 as two fp32
-MPM_DEV uint64_t widen2(uint32_t w) { return f32x2(bf16lo(w), bf16hi(w)); }
-
 // What a vector is computed in: pairs of fp32 (VEC = 8), or one
 template <int VEC>
 struct Lanes {
@@ -118,6 +105,58 @@ MPM_DEV void load_weight(const void* w, int f32, int k, float (&v)[VEC]) {
     r.load(static_cast<const uint16_t*>(w) + k);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) v[j] = r.value(j);
+  }
+}
+
+// Rows that start anywhere are taken by the aligned words of 8 that they touch:
+// where a row starts `off` columns into a word, word v holds columns 8 v - off
+// and on, and the words at its ends have columns outside [0, K).  (Forward at
+// 22524 x 4161: 146 us; by single elements 213, bound by their instructions.)
+MPM_DEV int word_offset(const uint16_t* row) { return (int)(reinterpret_cast<uintptr_t>(row) & 15) >> 1; }
+MPM_DEV bool whole_word(int k, int K) { return k >= 0 && k + 8 <= K; }
+
+// Columns k .. k + VEC - 1 of a row, zero outside [0, K); OFF: k is one of a
+// word as above, else K is a multiple of VEC
+template <int VEC, bool OFF>
+MPM_DEV void load_columns(RawBf16<VEC>& v, const uint16_t* row, int k, int K) {
+  if constexpr (!OFF) {
+    if (k < K) v.load(row + k);
+  } else {
+    if (whole_word(k, K)) {
+      v.load(row + k);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if ((unsigned)(k + j) < (unsigned)K) v.w[j / 2] |= (uint32_t)row[k + j] << (j % 2 * 16);
+    }
+  }
+}
+template <int VEC, bool OFF>
+MPM_DEV void store_columns(const RawBf16<VEC>& v, uint16_t* row, int k, int K) {
+  if constexpr (!OFF) {
+    if (k < K) v.store(row + k);
+  } else {
+    if (whole_word(k, K)) {
+      v.store(row + k);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if ((unsigned)(k + j) < (unsigned)K) row[k + j] = (uint16_t)(v.w[j / 2] >> (j % 2 * 16));
+    }
+  }
+}
+// the weight's, zero outside; OFF: from any alignment
+template <int VEC, bool OFF>
+MPM_DEV void load_weight_columns(const void* w, int f32, int k, int K, float (&v)[VEC]) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) v[j] = 0.0f;
+  if constexpr (!OFF) {
+    if (k < K) load_weight<VEC>(w, f32, k, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if ((unsigned)(k + j) < (unsigned)K)
+        v[j] = f32 ? static_cast<const float*>(w)[k + j] : bf16_f(static_cast<const uint16_t*>(w)[k + j]);
   }
 }
 
@@ -191,7 +230,7 @@ struct RingCursor {
 // TB/s.  The arithmetic is nearly as long as the copies, hence pairs of fp32:
 // with single ones and 8 columns a thread the two took 48.6 and 315 us (16
 // columns a thread alone: 47.6 and 312).
-template <int VEC, int IT, int R, bool WARP>
+template <int VEC, int IT, int R, bool WARP, bool OFF>
 __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) add_rmsnorm_kernel(const NormFwd p) {
   using L = Lanes<VEC>;
   using T = typename L::T;
@@ -202,18 +241,20 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) add_
   const int t = team.t, nt = team.nt;
   const long long row0 = team.index * R;
   RawBf16<VEC> x[R][IT], res[R][IT];
+  int off[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const uint16_t* px = p.x + (row0 + r) * p.ldx;
     const uint16_t* pr = p.r + (row0 + r) * p.ldr;
+    off[r] = OFF ? word_offset(px) : 0;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int k = (i * nt + t) * VEC;
+      const int k = (i * nt + t) * VEC - off[r];
       x[r][i].zero();
       res[r][i].zero();
-      if (k < p.K && row0 + r < p.M) {
-        x[r][i].load(px + k);
-        if (p.r) res[r][i].load(pr + k);
+      if (row0 + r < p.M) {
+        load_columns<VEC, OFF>(x[r][i], px, k, p.K);
+        if (p.r) load_columns<VEC, OFF>(res[r][i], pr, k, p.K);
       }
     }
   }
@@ -240,21 +281,20 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) add_
   }
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    const int k = (i * nt + t) * VEC;
-    const bool in = k < p.K;
     T w[L::N];
-    {
+    auto weight = [&](int k) {
       float v[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) v[j] = 0.0f;
-      if (in) load_weight<VEC>(p.w, p.w_f32, k, v);
+      load_weight_columns<VEC, OFF>(p.w, p.w_f32, k, p.K, v);
 #pragma unroll
       for (int j = 0; j < L::N; ++j) w[j] = L::pick(v, j);
-    }
+    };
+    if (!OFF) weight((i * nt + t) * VEC);          // the same for all rows
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const long long row = row0 + r;
-      const bool live = in && row < p.M;
+      const int k = (i * nt + t) * VEC - off[r];
+      if (OFF) weight(k);
+      const bool live = k < p.K && row < p.M;
       const T rstd = L::splat(ss[r]);
       RawBf16<VEC> oh, o;
 #pragma unroll
@@ -262,9 +302,9 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) add_
         oh.w[j] = L::bf16(h[r][i][j]);
         o.w[j] = L::bf16(L::mul(L::mul(h[r][i][j], rstd), w[j]));
       }
-      if (p.h && live) oh.store(p.h + row * p.ldh + k);
-      if (p.y && live) o.store(p.y + row * p.ldy + k);
-      if (!p.q) continue;
+      if (p.h && live) store_columns<VEC, OFF>(oh, p.h + row * p.ldh, k, p.K);
+      if (p.y && live) store_columns<VEC, OFF>(o, p.y + row * p.ldy, k, p.K);
+      if (OFF || !p.q) continue;
       // K % 32 == 0: a block of 32 lies in 32 / VEC neighbouring lanes
       uint32_t m = VEC == 8 ? absmax_bf16x2_packed(o.w) : o.w[0] & 0x7FFFu;
 #pragma unroll
@@ -282,7 +322,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) add_
       if (k % 32 == 0) p.s[sf_offset(row, k >> 5, p.s_cols_pad)] = (uint8_t)(e + 127);
     }
   }
-  if (!p.q) return;
+  if (OFF || !p.q) return;
   // zero the padding of the scale tiles: past K, and rows past M
   const int nblk = p.K >> 5;
 #pragma unroll
@@ -307,14 +347,28 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) add_
 // rows are in flight whatever the threads are doing.  A thread takes C words of
 // 8 columns.  A stage is refilled after the block barrier of the next row's
 // reduction, by when every thread is past its last read of it.
-template <int C, bool TWO, bool RES>
+//
+// Bound by the bytes, 8 an element with dh: 8192 x 2048 takes 30.4 us with the
+// sum of the partials (floor 24.8), 4093 x 1544 takes 15.0 (7.5), of which about
+// 5 are start, fill and that sum.  Rows held in registers with one in flight took
+// 89.6 and 45.6; one block of 1024 threads an SM in teams, 31.1 and 17.4.
+//
+// OFF: rows that start anywhere, by their words.  A block's rows start at one
+// place of a word (the blocks are a multiple of 8, or have one row each), so its
+// threads keep their columns (8000 x 1003 takes 19.4 us, 43 by single elements).  A copy takes whole words, and with them a few
+// elements of the rows beside it, which are masked; at the ends of the operand,
+// where there may be nothing beside it, it takes the row's own elements.
+template <int C, bool TWO, bool RES, bool OFF>
 __global__ void __launch_bounds__(1024 / C) add_rmsnorm_bwd_ring_kernel(const NormBwd p, int S) {
   constexpr int NT = 2 + (TWO ? 1 : 0) + (RES ? 1 : 0);
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float sh[2][32];
   __shared__ __align__(8) uint64_t bars[kRingStages];
   const int t = threadIdx.x, nt = blockDim.x;
-  const uint32_t row_bytes = (uint32_t)p.K * 2, stage_bytes = NT * row_bytes;
+  const int off = OFF ? word_offset(p.dy + blockIdx.x * p.lddy) : 0;
+  const int end = off + p.K;                               // in elements of the row's words
+  const uint32_t row_bytes = OFF ? (uint32_t)(end + 7) / 8 * 16 : (uint32_t)p.K * 2;
+  const uint32_t stage_bytes = NT * row_bytes;
   const uint32_t base = smem_u32(ring), bar0 = smem_u32(bars);
   if (t == 0) {
     for (int s = 0; s < S; ++s) mbar_init(bar0 + 8 * s, 1);
@@ -323,12 +377,34 @@ __global__ void __launch_bounds__(1024 / C) add_rmsnorm_bwd_ring_kernel(const No
   }
   pdl_wait();
   auto issue = [&](long long row, int s) {
-    const uint32_t dst = base + s * stage_bytes, bar = bar0 + 8 * s;
-    mbar_arrive_expect_tx(bar, stage_bytes);
-    bulk_load(dst, p.dy + row * p.lddy, row_bytes, bar);
-    bulk_load(dst + row_bytes, p.h + row * p.ldh, row_bytes, bar);
-    if (TWO) bulk_load(dst + 2 * row_bytes, p.dy2 + row * p.lddy2, row_bytes, bar);
-    if (RES) bulk_load(dst + (NT - 1) * row_bytes, p.dh + row * p.lddh, row_bytes, bar);
+    const uint32_t bar = bar0 + 8 * s;
+    uint32_t lo = 0, hi = row_bytes;                       // of the words, what is copied whole
+    if (OFF) {
+      if (row == 0 && off > 0) lo = 16;
+      if (row == p.M - 1 && end % 8 != 0) hi -= 16;
+    }
+    auto copy = [&](int operand, const uint16_t* src) {
+      const uint32_t to = s * stage_bytes + operand * row_bytes;
+      if (OFF && hi - lo != row_bytes) {
+        uint16_t* dst = reinterpret_cast<uint16_t*>(ring + to);
+        for (int j = off; j < (int)lo / 2; ++j) dst[j] = src[j - off];
+        for (int j = (int)hi / 2; j < end; ++j) dst[j] = src[j - off];
+        fence_proxy_async();                               // before a later copy over them
+      }
+      return base + to;
+    };
+    const uint16_t* src[NT];
+    src[0] = p.dy + row * p.lddy;
+    src[1] = p.h + row * p.ldh;
+    if (TWO) src[2] = p.dy2 + row * p.lddy2;
+    if (RES) src[NT - 1] = p.dh + row * p.lddh;
+    uint32_t dst[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) dst[i] = copy(i, src[i]);
+    mbar_arrive_expect_tx(bar, NT * (hi - lo));            // releases the elements above
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      bulk_load(dst[i] + lo, reinterpret_cast<const uint8_t*>(src[i] - off) + lo, hi - lo, bar);
   };
   const long long step = gridDim.x;
   if (t == 0) {
@@ -338,11 +414,8 @@ __global__ void __launch_bounds__(1024 / C) add_rmsnorm_bwd_ring_kernel(const No
   uint64_t w[C][4], dw[C][4];
 #pragma unroll
   for (int i = 0; i < C; ++i) {
-    const int k = (i * nt + t) * 8;
     float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    if (k < p.K) load_weight<8>(p.w, p.w_f32, k, v);
+    load_weight_columns<8, OFF>(p.w, p.w_f32, (i * nt + t) * 8 - off, p.K, v);
 #pragma unroll
     for (int j = 0; j < 4; ++j) { w[i][j] = f32x2(v[2 * j], v[2 * j + 1]); dw[i][j] = 0; }
   }
@@ -361,13 +434,22 @@ __global__ void __launch_bounds__(1024 / C) add_rmsnorm_bwd_ring_kernel(const No
     const uint64_t rstd2 = f32x2(rstd, rstd);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const int k = (i * nt + t) * 8;
+      const int at = (i * nt + t) * 8;
       RawBf16<8> a, b;
       a.zero(); b.zero(); h[i].zero();
-      if (k < p.K) {
-        a.load(reinterpret_cast<const uint16_t*>(st) + k);
-        h[i].load(reinterpret_cast<const uint16_t*>(st + row_bytes) + k);
-        if (TWO) b.load(reinterpret_cast<const uint16_t*>(st + 2 * row_bytes) + k);
+      if (at < end) {
+        a.load(reinterpret_cast<const uint16_t*>(st) + at);
+        h[i].load(reinterpret_cast<const uint16_t*>(st + row_bytes) + at);
+        if (TWO) b.load(reinterpret_cast<const uint16_t*>(st + 2 * row_bytes) + at);
+        if (OFF && !whole_word(at - off, p.K)) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int k = at - off + 2 * j;
+            const uint32_t m = ((unsigned)k < (unsigned)p.K ? 0xFFFFu : 0u) |
+                               ((unsigned)(k + 1) < (unsigned)p.K ? 0xFFFF0000u : 0u);
+            a.w[j] &= m; b.w[j] &= m; h[i].w[j] &= m;
+          }
+        }
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -395,10 +477,10 @@ __global__ void __launch_bounds__(1024 / C) add_rmsnorm_bwd_ring_kernel(const No
     const uint64_t f2 = f32x2(f, f);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const int k = (i * nt + t) * 8;
-      if (k >= p.K) continue;
+      const int at = (i * nt + t) * 8;
+      if (at >= end) continue;
       RawBf16<8> r, o;
-      if (RES) r.load(reinterpret_cast<const uint16_t*>(st + (NT - 1) * row_bytes) + k);
+      if (RES) r.load(reinterpret_cast<const uint16_t*>(st + (NT - 1) * row_bytes) + at);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint64_t d = fma2(widen2(h[i].w[j]), f2, u[i][j]);
@@ -407,7 +489,7 @@ __global__ void __launch_bounds__(1024 / C) add_rmsnorm_bwd_ring_kernel(const No
         f32x2_split(d, lo, hi);
         o.w[j] = pack_bf16(lo, hi);
       }
-      o.store(p.dx + row * p.lddx + k);
+      store_columns<8, OFF>(o, p.dx + row * p.lddx, at - off, p.K);
     }
     rstd = next_rstd;
     cur.next(S);
@@ -415,27 +497,49 @@ __global__ void __launch_bounds__(1024 / C) add_rmsnorm_bwd_ring_kernel(const No
   pdl_launch_dependents();
   if (!p.dw) return;
   float* out = gridDim.x == 1 ? p.dw : p.part + (long long)blockIdx.x * p.K;
+  if constexpr (OFF) {
+    // through the ring, whose copies have all been read, for stores in a row
+    float* sum = reinterpret_cast<float*>(ring);
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const int k = (i * nt + t) * 8;
-    if (k >= p.K) continue;
-    if (reinterpret_cast<uintptr_t>(out) % 16 == 0) {
-      reinterpret_cast<ulonglong2*>(out + k)[0] = make_ulonglong2(dw[i][0], dw[i][1]);
-      reinterpret_cast<ulonglong2*>(out + k)[1] = make_ulonglong2(dw[i][2], dw[i][3]);
-    } else {
+    for (int i = 0; i < C; ++i) {
+      float v[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f32x2_split(dw[i][j], out[k + 2 * j], out[k + 2 * j + 1]);
+      for (int j = 0; j < 4; ++j) f32x2_split(dw[i][j], v[2 * j], v[2 * j + 1]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = (i * nt + t) * 8 - off + j;
+        if ((unsigned)k < (unsigned)p.K) sum[k] = v[j];
+      }
+    }
+    __syncthreads();
+    for (int k = t; k < p.K; k += nt) out[k] = sum[k];
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int k = (i * nt + t) * 8;
+      if (k >= p.K) continue;
+      if (reinterpret_cast<uintptr_t>(out) % 16 == 0) {
+        reinterpret_cast<ulonglong2*>(out + k)[0] = make_ulonglong2(dw[i][0], dw[i][1]);
+        reinterpret_cast<ulonglong2*>(out + k)[1] = make_ulonglong2(dw[i][2], dw[i][3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f32x2_split(dw[i][j], out[k + 2 * j], out[k + 2 * j + 1]);
+      }
     }
   }
 }
 
-// The other rows take two kernels: dx from one row a block (short rows: one a
-// warp), held in registers with all its loads in flight, and dw's partials from
-// blocks of columns.  They read dy and h twice, but the ring needs rows that
-// start on 16 bytes, and a register form that kept dw beside one row at a time
-// per SM was slower (216 against 72 us at 3000 x 4161).  WIDE rows (32 values a
-// thread) would not fit in registers with all operands: there the gradients of y
-// are added as they arrive and dh is loaded after the reduction.
+// What the ring does not take (rows of up to 256 columns, of more than 8192, and
+// operands that start at different places of a word) has two kernels: dx from
+// one row a block (short rows: one a warp), held in registers with all its loads
+// in flight, and dw's partials from blocks of columns.  They read dy and h
+// twice; short rows are bound by latency there (19074 x 176: 16.3 us), single
+// elements by instructions (3000 x 4161 at different offsets: 72 us, where a
+// register form that kept dw beside one row at a time took 216 and the ring, at
+// equal offsets, takes 30).  WIDE rows (32 values a thread) would not fit in
+// registers with all operands: there the gradients of y are added as they
+// arrive and dh is loaded after the reduction.
 template <int VEC, int IT, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) rmsnorm_dx_kernel(const NormBwd p) {
   constexpr bool WIDE = VEC * IT > 16;
@@ -496,7 +600,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) rmsn
 }
 
 // Partials of dw = sum over rows of dy h rstd: one column a thread, the rows
-// blockIdx.y, blockIdx.y + gridDim.y, ..., eight of them in flight
+// blockIdx.y, blockIdx.y + gridDim.y, ..., eight of them in flight, which is
+// what its time goes by: 95 of the 256 us at 12000 x 4161
 __global__ void __launch_bounds__(256) rmsnorm_dw_rows_kernel(const NormBwd p) {
   pdl_wait();
   pdl_launch_dependents();
@@ -523,7 +628,8 @@ __global__ void __launch_bounds__(256) rmsnorm_dw_rows_kernel(const NormBwd p) {
 }
 
 // dw = the sum of the partials: C columns a block (few where there are few
-// columns), 1024 / C partials at a time
+// columns, to have blocks for all SMs), 1024 / C partials at a time.  1.2 MB from
+// L2 at K = 2048; bound by the latency of two dependent steps, about 2 us.
 template <int C>
 __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* part, int parts, int K, float* dw) {
   constexpr int G = 1024 / C;
@@ -552,6 +658,11 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* part, int
 static bool vec8(const void* p, long long ld) {
   return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0);
 }
+// whether every row of both starts at the same place of a 16-byte word
+static bool same_words(const void* a, long long lda, const void* b, long long ldb) {
+  return b == nullptr || ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) % 16 == 0 &&
+                          (lda - ldb) % 8 == 0);
+}
 static unsigned norm_threads(int K, int per_thread) {
   const int n = (K + per_thread - 1) / per_thread;
   return (unsigned)((n + 31) / 32 * 32);
@@ -561,7 +672,7 @@ static unsigned norm_threads(int K, int per_thread) {
 struct NormRing { unsigned threads; int blocks, stages, smem; };
 // 512 threads an SM, 16 columns each (8 columns and 1024 threads: 15.8 against
 // 15.1 us at 4093 x 1544, the same at 8192 x 2048)
-static int ring_blocks(int K) {
+static int ring_blocks(int K) {          // K: columns of the words that a row touches
   const int n = 512 / (int)norm_threads(K, 8 * kRingWords);
   return n < 1 ? 1 : n;
 }
@@ -587,29 +698,38 @@ static cudaError_t launch_ring(const NormRing& r, long long blocks, const P& p, 
   return launch_serial(kernel, dim3((unsigned)blocks), dim3(r.threads), (size_t)r.smem, st, p, r.stages);
 }
 
-template <int VEC, int IT, int R, bool WARP>
+template <int VEC, int IT, int R, bool WARP, bool OFF>
 static cudaError_t norm_fwd(const NormFwd& p, cudaStream_t st) {
   const long long rows = p.q ? (p.M + 127) / 128 * 128 : p.M, per = WARP ? R * kNormTeams : R;
-  return launch_serial(add_rmsnorm_kernel<VEC, IT, R, WARP>, dim3((unsigned)((rows + per - 1) / per)),
-                       dim3(WARP ? 32 * kNormTeams : norm_threads(p.K, VEC * IT)), 0, st, p);
+  return launch_serial(add_rmsnorm_kernel<VEC, IT, R, WARP, OFF>, dim3((unsigned)((rows + per - 1) / per)),
+                       dim3(WARP ? 32 * kNormTeams : norm_threads(OFF ? p.K + 7 : p.K, VEC * IT)), 0, st, p);
+}
+
+// Short rows leave most of a block idle at its barrier: a warp each, two at a
+// time where one has a load each at most.  Warp against block: 18.0 and 20.1
+// us at 16384 x 768, but 25.6 and 24.4 at 16384 x 1024; two rows against one:
+// 11.5 and 12.2 us at 32768 x 256, 9.1 and 10.1 at 32768 x 128.
+template <bool OFF>
+static cudaError_t norm_fwd_words(const NormFwd& p, cudaStream_t st) {
+  const int n = OFF ? p.K + 7 : p.K;     // columns of the words that a row touches
+  if (n <= 256) return norm_fwd<8, 1, 2, true, OFF>(p, st);
+  if (n <= 512) return norm_fwd<8, 2, 1, true, OFF>(p, st);
+  if (n <= 768) return norm_fwd<8, 3, 1, true, OFF>(p, st);
+  return n <= 16 * kNormMaxThreads ? norm_fwd<8, 2, 1, false, OFF>(p, st) : norm_fwd<8, 4, 1, false, OFF>(p, st);
 }
 
 cudaError_t launch_add_rmsnorm(const NormFwd& p, cudaStream_t st) {
-  const bool v = p.K % 8 == 0 && vec8(p.x, p.ldx) && vec8(p.r, p.ldr) && vec8(p.h, p.ldh) &&
-                 vec8(p.y, p.ldy) && vec8(p.w, 0);
-  if (v) {
-    // Short rows leave most of a block idle at its barrier: a warp each, two at a
-    // time where one has a load each at most.  Warp against block: 18.0 and 20.1
-    // us at 16384 x 768, but 25.6 and 24.4 at 16384 x 1024; two rows against one:
-    // 11.5 and 12.2 us at 32768 x 256, 9.1 and 10.1 at 32768 x 128.
-    if (p.K <= 256) return norm_fwd<8, 1, 2, true>(p, st);
-    if (p.K <= 512) return norm_fwd<8, 2, 1, true>(p, st);
-    if (p.K <= 768) return norm_fwd<8, 3, 1, true>(p, st);
-    return p.K <= 16 * kNormMaxThreads ? norm_fwd<8, 2, 1, false>(p, st) : norm_fwd<8, 4, 1, false>(p, st);
-  }
-  if (p.K <= 128) return norm_fwd<1, 4, 1, true>(p, st);
-  if (p.K <= 4 * kNormMaxThreads) return norm_fwd<1, 4, 1, false>(p, st);
-  return p.K <= 16 * kNormMaxThreads ? norm_fwd<1, 16, 1, false>(p, st) : norm_fwd<1, 32, 1, false>(p, st);
+  if (p.K % 8 == 0 && vec8(p.x, p.ldx) && vec8(p.r, p.ldr) && vec8(p.h, p.ldh) && vec8(p.y, p.ldy) && vec8(p.w, 0))
+    return norm_fwd_words<false>(p, st);
+  // by words, but the shortest rows by single elements, where few lanes would
+  // have a word (18434 rows of 127: 6.2 and 7.7 us; of 143: 19.3 and 7.8)
+  if (!p.q && p.K > 128 && p.K + 7 <= 32 * kNormMaxThreads && same_words(p.x, p.ldx, p.r, p.ldr) &&
+      same_words(p.x, p.ldx, p.h, p.ldh) && same_words(p.x, p.ldx, p.y, p.ldy))
+    return norm_fwd_words<true>(p, st);
+  if (p.K <= 128) return norm_fwd<1, 4, 1, true, false>(p, st);
+  if (p.K <= 4 * kNormMaxThreads) return norm_fwd<1, 4, 1, false, false>(p, st);
+  return p.K <= 16 * kNormMaxThreads ? norm_fwd<1, 16, 1, false, false>(p, st)
+                                     : norm_fwd<1, 32, 1, false, false>(p, st);
 }
 
 // Blocks of the backward's ring, each with its own partial dw (the two-kernel
@@ -628,10 +748,11 @@ static cudaError_t norm_dw(const NormBwd& p, long long parts, cudaStream_t st) {
                        (const float*)p.part, (int)parts, p.K, p.dw);
 }
 
-template <auto kernel>
+template <auto kernel, bool OFF>
 static cudaError_t norm_bwd_ring(const NormBwd& p, int operands, cudaStream_t st) {
-  const NormRing r = norm_ring(p.K, 8 * kRingWords, 2 * p.K * operands);
-  const long long blocks = rmsnorm_backward_parts(p.M, p.K);
+  const int n = OFF ? (p.K + 14) / 8 * 8 : p.K;      // columns of the words that a row touches, at most
+  const NormRing r = norm_ring(n, 8 * kRingWords, 2 * n * operands);
+  const long long blocks = rmsnorm_backward_parts(p.M, n);       // no more than of K
   const cudaError_t err = launch_ring<kernel>(r, blocks, p, st);
   return err != cudaSuccess ? err : norm_dw(p, blocks, st);
 }
@@ -656,18 +777,29 @@ static cudaError_t norm_bwd_two(const NormBwd& p, cudaStream_t st) {
                        dim3(WARP ? 32 * kNormTeams : norm_threads(p.K, VEC * IT)), 0, st, p);
 }
 
+template <bool OFF>
+static cudaError_t norm_bwd_words(const NormBwd& p, cudaStream_t st) {
+  if (p.dy2)
+    return p.dh ? norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<kRingWords, true, true, OFF>, OFF>(p, 4, st)
+                : norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<kRingWords, true, false, OFF>, OFF>(p, 3, st);
+  return p.dh ? norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<kRingWords, false, true, OFF>, OFF>(p, 3, st)
+              : norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<kRingWords, false, false, OFF>, OFF>(p, 2, st);
+}
+
 cudaError_t launch_add_rmsnorm_backward(const NormBwd& p, cudaStream_t st) {
   const bool v = p.K % 8 == 0 && vec8(p.dy, p.lddy) && vec8(p.dy2, p.lddy2) && vec8(p.h, p.ldh) &&
                  vec8(p.dh, p.lddh) && vec8(p.dx, p.lddx) && vec8(p.w, 0);
   if (v) {
     if (p.K <= 256) return norm_bwd_two<8, 1, true>(p, st);
     if (p.K > 8192) return norm_bwd_two<8, 4, false>(p, st);
-    if (p.dy2)
-      return p.dh ? norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<kRingWords, true, true>>(p, 4, st)
-                  : norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<kRingWords, true, false>>(p, 3, st);
-    return p.dh ? norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<kRingWords, false, true>>(p, 3, st)
-                : norm_bwd_ring<add_rmsnorm_bwd_ring_kernel<kRingWords, false, false>>(p, 2, st);
+    return norm_bwd_words<false>(p, st);
   }
+  // The same for rows that start anywhere; few short ones are quicker in two
+  // kernels (2000 x 143: 6.9 against 8.3 us; 18434 x 143: 30.1 against 16.0)
+  if ((p.K > 256 || (p.K > 128 && p.M >= 4096)) && p.K + 7 <= 8192 && same_words(p.dy, p.lddy, p.dy2, p.lddy2) &&
+      same_words(p.dy, p.lddy, p.h, p.ldh) && same_words(p.dy, p.lddy, p.dh, p.lddh) &&
+      same_words(p.dy, p.lddy, p.dx, p.lddx))
+    return norm_bwd_words<true>(p, st);
   if (p.K <= 128) return norm_bwd_two<1, 4, true>(p, st);
   if (p.K <= 4 * kNormMaxThreads) return norm_bwd_two<1, 4, false>(p, st);
   return p.K <= 16 * kNormMaxThreads ? norm_bwd_two<1, 16, false>(p, st) : norm_bwd_two<1, 32, false>(p, st);

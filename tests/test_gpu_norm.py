@@ -148,6 +148,49 @@ def test_in_place_gradient(M, K, onto):
     assert dx is t[onto] and torch.equal(dx, ref[0]) and torch.equal(dw, ref[1])
 
 
+@pytest.mark.parametrize("M,K,pad,off", [(1, 257, 0, 3), (1, 100, 0, 7), (40, 300, 0, 1), (77, 241, 5, 2), (2000, 1003, 0, 0),
+                                         (700, 521, 3, 5), (3, 2048, 0, 1), (300, 4161, 8, 0), (9, 8185, 1, 7),
+                                         (9, 8186, 0, 1), (2, 16377, 0, 4), (2, 16378, 0, 4)])
+@pytest.mark.parametrize("two,res,f32", [(True, True, False), (False, True, True), (True, False, True),
+                                         (False, False, False)])
+def test_rows_off_the_alignment(M, K, pad, off, two, res, f32):
+    """All operands off by the same, forward and backward; the elements beside
+    the rows are NaN and stay out of them."""
+    ops = _ops()
+
+    def rows(seed, std=1.0):
+        buf = torch.full((M * (K + pad) + off + 9,), float("nan"), dtype=torch.bfloat16, device="cuda")
+        v = buf[off:off + M * (K + pad)].view(M, K + pad)[:, :K]
+        v.copy_(_rows(seed, M, K, std=std))
+        return v
+
+    x, r, w = rows(50), rows(51, 3.0) if res else None, _weight(52, K, f32)
+    o = ops.add_rmsnorm(x, w, residual=r, out={"y": rows(53), **({"h": rows(54)} if res else {})})
+    _check_forward(o, x, w, r, 1e-6, False)
+    h = o["h"] if res else x
+    dy, dy2, dh = rows(55, 1e-2), rows(56, 1e-2) if two else None, rows(57, 1e-2) if res else None
+    dx, dw = ops.add_rmsnorm_backward(dy, h, o["rstd"], w, dy2=dy2, dh=dh, out=(rows(58), torch.empty(K, device="cuda")))
+    total = np_bf16(dy).astype(np.float64) + (np_bf16(dy2) if two else 0.0)
+    rx, rw, mx, mw = N.add_rmsnorm_backward(total, np_bf16(h), o["rstd"].cpu().numpy(), w.float().cpu().numpy(),
+                                            np_bf16(dh) if res else None)
+    _within(np_bf16(dx), rx, BF16 * np.abs(rx) + DX * mx + 1e-38, "dx")
+    _within(dw.cpu().numpy(), rw, DW * mw + 1e-38, "dw")
+
+
+def test_a_row_of_nan_stays_out_of_its_neighbours():
+    ops = _ops()
+    M, K = 600, 1003
+    h, dy, w = _rows(60, M, K), _rows(61, M, K, std=1e-2), _weight(62, K, True)
+    ref = ops.add_rmsnorm(h, w)
+    dref, _ = ops.add_rmsnorm_backward(dy, h, ref["rstd"], w, want_dw=False)
+    h[300], dy[300] = float("nan"), float("nan")
+    o = ops.add_rmsnorm(h, w)
+    dx, _ = ops.add_rmsnorm_backward(dy, h, o["rstd"], w, want_dw=False)
+    keep = [m for m in range(M) if m != 300]
+    assert torch.equal(o["y"][keep], ref["y"][keep]) and torch.equal(dx[keep], dref[keep])
+    assert torch.isnan(o["y"][300]).all() and torch.isnan(dx[300]).all()
+
+
 def test_rows_of_zeros_infinities_and_nan():
     """A zero row gives zeros; NaN and infinities stay in their rows."""
     K = 256
