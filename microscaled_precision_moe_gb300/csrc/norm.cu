@@ -348,9 +348,9 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) add_
 // 8 columns.  A stage is refilled after the block barrier of the next row's
 // reduction, by when every thread is past its last read of it.
 //
-// Bound by the bytes, 8 an element with dh: 8192 x 2048 takes 30.4 us with the
-// sum of the partials (floor 24.8), 4093 x 1544 takes 15.0 (7.5), of which about
-// 5 are start, fill and that sum.  Rows held in registers with one in flight took
+// Bound by the bytes, 8 an element with dh, 10 with dy2 too: 8192 x 2048 with
+// both takes 30.1 us, the sum of the partials included (floor 24.8), 4093 x 1544
+// with dh 14.5 (7.5).  Rows held in registers with one in flight took
 // 89.6 and 45.6; one block of 1024 threads an SM in teams, 31.1 and 17.4.
 //
 // OFF: rows that start anywhere, by their words.  A block's rows start at one
@@ -627,9 +627,9 @@ __global__ void __launch_bounds__(256) rmsnorm_dw_rows_kernel(const NormBwd p) {
   (gridDim.y == 1 ? p.dw : p.part + (long long)blockIdx.y * p.K)[k] = s;
 }
 
-// dw = the sum of the partials: C columns a block (few where there are few
-// columns, to have blocks for all SMs), 1024 / C partials at a time.  1.2 MB from
-// L2 at K = 2048; bound by the latency of two dependent steps, about 2 us.
+// dw = the sum of the partials: C columns a block, 1024 / C partials at a time.
+// 608 partials, 5 MB in L2, at K = 2048; with the writing of the partials it adds
+// 3.4 us, most of it latency: the end of one kernel and a chain of two steps.
 template <int C>
 __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* part, int parts, int K, float* dw) {
   constexpr int G = 1024 / C;
@@ -741,11 +741,15 @@ long long rmsnorm_backward_parts(long long M, int K) {
 
 static cudaError_t norm_dw(const NormBwd& p, long long parts, cudaStream_t st) {
   if (!p.dw || parts == 1) return cudaSuccess;
-  if (p.K <= 1024)
-    return launch_serial(rmsnorm_dw_kernel<8>, dim3((unsigned)((p.K + 7) / 8)), dim3(1024), 0, st,
+  // the fewest columns a block that need no more blocks than there are SMs (8, 16
+  // and 32: 9.8, 11.5, 13.4 us in all at 8192 x 512; 14.7, 13.8, 14.5 at 4093 x
+  // 1544; 26.5, 25.7, 24.6 at 2000 x 7168)
+  auto sum = [&](auto kernel, int columns) {
+    return launch_serial(kernel, dim3((unsigned)((p.K + columns - 1) / columns)), dim3(1024), 0, st,
                          (const float*)p.part, (int)parts, p.K, p.dw);
-  return launch_serial(rmsnorm_dw_kernel<32>, dim3((unsigned)((p.K + 31) / 32)), dim3(1024), 0, st,
-                       (const float*)p.part, (int)parts, p.K, p.dw);
+  };
+  if (p.K <= 8 * 152) return sum(rmsnorm_dw_kernel<8>, 8);
+  return p.K <= 16 * 152 ? sum(rmsnorm_dw_kernel<16>, 16) : sum(rmsnorm_dw_kernel<32>, 32);
 }
 
 template <auto kernel, bool OFF>
