@@ -20,17 +20,20 @@
 //   1. tau: the k-th largest of the 32 lanes' own maxima (k warp maxima; equal
 //      lane maxima leave together, which can only lower tau).  At least k keys
 //      are >= tau, and few more: about 10 of 256 for k = 8.
-//   2. Those keys move to one lane each (ballots and shared memory), and each
-//      lane counts the keys above its own, its place among the choices; only
-//      where places collide are equal keys told apart by expert.
+//   2. Those keys move to one lane each (their number in the lanes before by
+//      ballots, the keys through shared memory), and each lane counts the keys
+//      above its own, its place among the choices; only where places collide are
+//      equal keys told apart by expert.
 // With k > 32, more than 32 such keys (masses of ties) or fewer than k lanes with
 // an expert in reach, the warp takes k maxima one after the other instead.
 // Softmax scores use the hardware exponential (a few ulp); sigmoid scores expf
 // and the IEEE reciprocal, since with a bias the choice depends on their last bit.
 // Sums over tokens go through per-block partials added in a fixed order (no
 // floating-point atomics).
+#include <algorithm>
 #include "router.cuh"
 #include "launch.cuh"
+#include "packed.cuh"
 
 namespace mpm {
 
@@ -61,6 +64,17 @@ MPM_DEV float warp_max(float v) { return ordered_value(__reduce_max_sync(0xFFFFF
 
 // exp(v) for v <= 0, by the change of base 2^(v log2 e); -inf gives 0
 MPM_DEV float exp_neg(float v) { return exp2_ftz(__fmul_rn(v, kLog2e)); }
+
+// of a lane's NE (even) values
+template <int NE>
+MPM_DEV float lane_sum(const float (&v)[NE]) {
+  uint64_t acc = f32x2(v[0], v[1]);
+#pragma unroll
+  for (int i = 2; i < NE; i += 2) acc = add2(acc, f32x2(v[i], v[i + 1]));
+  float lo, hi;
+  f32x2_split(acc, lo, hi);
+  return __fadd_rn(lo, hi);
+}
 
 // the lane's i-th expert
 template <bool BF16>
@@ -165,14 +179,26 @@ MPM_DEV void route_one_by_one(const RouteArgs& a, int t, int lane, const float (
   if (lane + 32 < a.k) a.prob[t * a.k + 32 + lane] = __fmul_rn(w1, sc);
 }
 
-// a warp's shared memory in the token loop, NE * 32 + 64 words: its keys by
-// slot, the candidates' slots, the candidates' keys
-template <int NE>
+// a warp's shared memory in the token loop: the candidates' keys and experts
 struct __align__(16) RouteWarp {
-  float key[NE * 32];
-  int slot[32];
-  float cand[32];
+  float key[32];
+  int expert[32];
 };
+
+// The lane's keys >= least, and their experts, to the places from `to` (shared
+// memory) on.  Two predicated stores and an addition a key: as a conditional the
+// compiler spent twice as many instructions.
+template <int NE, bool BF16>
+MPM_DEV void put_candidates(const float (&key)[NE], float least, int lane, uint32_t to) {
+#pragma unroll
+  for (int i = 0; i < NE; ++i)
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ge.f32 p, %1, %2;\n\t"
+                 "@p st.shared.f32 [%0], %1;\n\t"
+                 "@p st.shared.u32 [%0 + 128], %3;\n\t"
+                 "@p add.u32 %0, %0, 4;\n\t}"
+                 : "+r"(to) : "f"(key[i]), "f"(least), "r"(expert_of<BF16>(i, lane)) : "memory");
+}
 
 // what the choice compares: the logits, or sigmoid scores with their bias
 template <bool SIG, int NE>
@@ -186,17 +212,17 @@ MPM_DEV float (&route_keys(float (&l)[NE], float (&sig_key)[SIG ? NE : 1]))[NE] 
 template <int NE, bool SIG, bool BF16>
 MPM_DEV void route_token(const RouteArgs& a, int t, int next, int lane, RawLogits<NE, BF16>& raw,
                          bool on, uint32_t dead_bias, const float (&bias)[NE], float (&load)[NE],
-                         int* sh_counts, RouteWarp<NE>& sh) {
+                         int* sh_counts, RouteWarp& sh) {
   float l[NE], s[NE], sig_key[SIG ? NE : 1];
   float top = -INFINITY, sum = 0.0f;
   if constexpr (SIG) {
     route_logits<NE, BF16>(raw, dead_bias, l);
   } else {
-    // NaN becomes -inf here; the other ways out of reach show in tau and the maximum
+    // What is out of reach shows later: NaN in the sum, the rest in tau and the maximum
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      l[i] = fmaxf(raw.value(i), -INFINITY);
-      top = fmaxf(top, l[i]);
+      l[i] = raw.value(i);
+      top = fmaxf(top, l[i]);            // the number, where one is NaN
     }
   }
   if (next < (int)a.T) raw.load(a, next, lane);
@@ -205,7 +231,6 @@ MPM_DEV void route_token(const RouteArgs& a, int t, int next, int lane, RawLogit
     for (int i = 0; i < NE; ++i) {
       // l = -inf: expf gives inf and the score is 0
       s[i] = __frcp_rn(__fadd_rn(1.0f, expf(-l[i])));
-      sum = __fadd_rn(sum, s[i]);
       sig_key[i] = l[i] > -INFINITY ? __fadd_rn(s[i], bias[i]) : -INFINITY;
       top = fmaxf(top, sig_key[i]);
     }
@@ -236,66 +261,91 @@ MPM_DEV void route_token(const RouteArgs& a, int t, int next, int lane, RawLogit
       // exp(l - m) as 2^(l log2 e - m log2 e), the product exact within the
       // FMA: the rounding of m log2 e is one factor, below 1.003, of all s
       m2 = __fmul_rn(m, kLog2e);
+      const uint64_t scale2 = f32x2(kLog2e, kLog2e), from2 = f32x2(-m2, -m2);
 #pragma unroll
-      for (int i = 0; i < NE; ++i) s[i] = exp2_ftz(__fmaf_rn(l[i], kLog2e, -m2));
+      for (int i = 0; i < NE; i += 2) {
+        f32x2_split(fma2(f32x2(l[i], l[i + 1]), scale2, from2), s[i], s[i + 1]);
+        s[i] = exp2_ftz(s[i]);
+        s[i + 1] = exp2_ftz(s[i + 1]);
+      }
+      sum = warp_sum(lane_sum(s));
+      quick = sum == sum;
     } else {
       quick = false;
+    }
+    if (!quick) {
       RawLogits<NE, BF16> again;
       again.load(a, t, lane);
       route_logits<NE, BF16>(again, 0u, l);
       m = fminf(fmaxf(m, -kLargest), kLargest);         // none in reach: exp(-inf) = 0
 #pragma unroll
       for (int i = 0; i < NE; ++i) s[i] = exp_neg(__fsub_rn(l[i], m));
+      sum = warp_sum(lane_sum(s));
     }
-#pragma unroll
-    for (int i = 0; i < NE; ++i) sum = __fadd_rn(sum, s[i]);
+  } else {
+    sum = warp_sum(lane_sum(s));
   }
-  sum = warp_sum(sum);
   const float share = on && sum > 0.0f ? rcp_ftz(sum) : 0.0f;
+  const uint64_t share2 = f32x2(share, share);
 #pragma unroll
-  for (int i = 0; i < NE; ++i) load[i] = __fmaf_rn(s[i], share, load[i]);
+  for (int i = 0; i < NE; i += 2)
+    f32x2_split(fma2(f32x2(s[i], s[i + 1]), share2, f32x2(load[i], load[i + 1])), load[i], load[i + 1]);
   // a weight before normalisation is s times this
   const float unit = SIG ? 1.0f : share;
   if (quick) {
-    __syncwarp();                        // the previous token's candidates have been read
     const uint32_t below_lane = (1u << lane) - 1u;
-    uint32_t mine = 0;                   // the lane's candidates by slot
+    int c = 0;                           // the lane's candidates
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      sh.key[i * 32 + lane] = key[i];
-      if (key[i] >= least) mine |= 1u << i;
-    }
-    int n = 0;
-    for (uint32_t b = __ballot_sync(0xFFFFFFFFu, mine != 0); b && n <= 32;
-         b = __ballot_sync(0xFFFFFFFFu, mine != 0)) {
-      const int at = n + __popc(b & below_lane);
-      if (mine && at < 32) sh.slot[at] = (__ffs(mine) - 1) * 32 + lane;
-      mine &= mine - 1;
-      n += __popc(b);
-    }
+    for (int i = 0; i < NE; ++i) c += key[i] >= least ? 1 : 0;
+    // the sum of c over the lanes before, bit by bit: seldom more than two
+    int at = 0, n = 0;
+    auto add_bit = [&](int bit) {
+      const uint32_t b = __ballot_sync(0xFFFFFFFFu, c >> bit & 1);
+      at += __popc(b & below_lane) << bit;
+      n += __popc(b) << bit;
+    };
+    add_bit(0);
+    add_bit(1);
+    for (int bit = 2; __any_sync(0xFFFFFFFFu, c >> bit); ++bit) add_bit(bit);
     if (n <= 32) {
+      __syncwarp();                      // the previous token's candidates have been read
+      put_candidates<NE, BF16>(key, least, lane, smem_u32(&sh.key[at]));
+      if (lane >= n) sh.key[lane] = -INFINITY;
       __syncwarp();
-      // lane c has candidate c, in no particular order
-      const int slot = lane < n ? sh.slot[lane] : 0;
-      const float c = lane < n ? sh.key[slot] : -INFINITY;
-      const int e = expert_of<BF16>(slot >> 5, slot & 31);
-      sh.cand[lane] = c;
-      __syncwarp();
+      // lane j has candidate j, in no particular order; of 16 or fewer, lane j + 16
+      // has it too and looks at the other half of them
+      const bool few = n <= 16;
+      const float own = sh.key[few ? lane & 15 : lane];
+      const int e = sh.expert[few ? lane & 15 : lane];
       int place = 0;
+      auto count = [&](int j) {
+        const float4 q = *reinterpret_cast<const float4*>(&sh.key[j]);
+        place += (q.x > own ? 1 : 0) + (q.y > own ? 1 : 0) + (q.z > own ? 1 : 0) + (q.w > own ? 1 : 0);
+      };
+      if (few) {
+        const int j0 = lane >> 4 << 3;
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        if (j == 16 && n <= 16) break;
-        const float4 q = *reinterpret_cast<const float4*>(&sh.cand[j]);
-        place += (q.x > c ? 1 : 0) + (q.y > c ? 1 : 0) + (q.z > c ? 1 : 0) + (q.w > c ? 1 : 0);
+        for (int j = 0; j < 8; j += 4) count(j0 + j);
+        place += __shfl_xor_sync(0xFFFFFFFFu, place, 16);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) count(j);
       }
       bool chosen = lane < n && place < a.k;
-      // equal keys share a place: then k lanes do not hold the k places
-      const uint32_t held = __reduce_or_sync(0xFFFFFFFFu, chosen ? 1u << place : 0u);
-      if (__popc(held) != a.k || __popc(__ballot_sync(0xFFFFFFFFu, chosen)) != a.k) {
-        for (int j = 0; j < n; ++j) {
-          const int ej = __shfl_sync(0xFFFFFFFFu, e, j);
-          place += sh.cand[j] == c && ej < e ? 1 : 0;
-        }
+      // Equal keys share a place: then k lanes do not hold the k places.  Where k
+      // lanes are chosen, their places' powers of two add up to 2^k - 1 only if
+      // no two are the same (k <= 16: with their number in the bits above).
+      bool apart;
+      if (a.k <= 16) {
+        const uint32_t held = __reduce_add_sync(0xFFFFFFFFu, chosen ? (1u << place) + (1u << 24) : 0u);
+        apart = held == (1u << a.k) - 1u + ((uint32_t)a.k << 24);
+      } else {
+        const uint32_t held = __reduce_or_sync(0xFFFFFFFFu, chosen ? 1u << place : 0u);
+        apart = __popc(held) == a.k && __popc(__ballot_sync(0xFFFFFFFFu, chosen)) == a.k;
+      }
+      if (!apart) {
+        for (int j = 0; j < n; ++j)
+          place += sh.key[j] == own && sh.expert[j] < e ? 1 : 0;
         chosen = lane < n && place < a.k;
       }
       float w = 0.0f;
@@ -306,7 +356,7 @@ MPM_DEV void route_token(const RouteArgs& a, int t, int next, int lane, RawLogit
           else v = static_cast<const float*>(a.logits)[t * a.ld + e];
           w = __frcp_rn(__fadd_rn(1.0f, expf(-fminf(v, kLargest))));
         } else {
-          w = exp2_ftz(__fmaf_rn(c, kLog2e, -m2));
+          w = exp2_ftz(__fmaf_rn(own, kLog2e, -m2));
         }
       }
       float f = unit;
@@ -350,8 +400,14 @@ MPM_DEV uint32_t ld_cluster_u32(const void* p, uint32_t rank) {
   return v;
 }
 
+// Bound by its instructions, about 420 a token at E = 256, k = 8 (80 % of the
+// issue slots; DRAM at a quarter): 32768 tokens take 18.5 us, 3.7 of them in the
+// sum over blocks below, where reading the logits would take 5.  Slopes: 1.9 us
+// per 4864 tokens, 1.5 at E = 64, k = 4, the same for k = 1: mostly a token's
+// fixed steps.  A warp per token and k arg-max rounds over all keys took 110 us.
+//
 // Shared memory: the block's loads [E] and counts [E], then a region that
-// holds the warps' keys and candidates during the token loop and their lanes' loads
+// holds the warps' candidates during the token loop and their lanes' loads
 // [warps][E] after it
 template <int NE, bool SIG, bool BF16>
 __global__ void __launch_bounds__(32 * route_warps(NE)) route_kernel(const RouteArgs a) {
@@ -363,7 +419,7 @@ __global__ void __launch_bounds__(32 * route_warps(NE)) route_kernel(const Route
   __shared__ int sh_n[32];
   __shared__ float sh_loss;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, W = blockDim.x >> 5;
-  RouteWarp<NE>& sh = reinterpret_cast<RouteWarp<NE>*>(region)[warp];
+  RouteWarp& sh = reinterpret_cast<RouteWarp*>(region)[warp];
   const int step = gridDim.x * W, T = (int)a.T;         // T k <= 2^30
   int t = blockIdx.x * W + warp;
   RawLogits<NE, BF16> raw;
@@ -454,7 +510,8 @@ __global__ void __launch_bounds__(32 * route_warps(NE)) route_kernel(const Route
 }
 
 // The blocks' partials summed: one cluster of 8 blocks, each taking every 8th
-// group of 32 experts, warp w the parts w, w + 32, ... of them
+// group of 32 experts, warp w the parts w, w + 32, ... of them.  Latency only
+// (300 KB from L2): 3.7 us behind the kernel before; one block took 2.8 more.
 __global__ void __launch_bounds__(1024) route_finish_kernel(const RouteArgs a, int parts) {
   __shared__ float sh_l[32][33];
   __shared__ int sh_c[32][33];
@@ -465,9 +522,7 @@ __global__ void __launch_bounds__(1024) route_finish_kernel(const RouteArgs a, i
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   int n = 0;
-  for (int i = threadIdx.x; i < parts; i += blockDim.x) n += a.ws_n[i];
-  n = __reduce_add_sync(0xFFFFFFFFu, n);
-  if (lane == 0) sh_n[warp] = n;
+  const int my_n = (int)threadIdx.x < parts ? a.ws_n[threadIdx.x] : 0;     // parts <= 152
   float loss = 0.0f;
   for (int e0 = (int)rank * 32; e0 < a.E; e0 += kClusterCtas * 32) {
     const int e = e0 + lane;
@@ -480,6 +535,8 @@ __global__ void __launch_bounds__(1024) route_finish_kernel(const RouteArgs a, i
         c += a.ws_counts[(long long)i * a.E + e];
       }
     }
+    n = __reduce_add_sync(0xFFFFFFFFu, my_n);             // after the loads above are out
+    if (lane == 0) sh_n[warp] = n;
     sh_l[warp][lane] = v;
     sh_c[warp][lane] = c;
     __syncthreads();
@@ -523,6 +580,10 @@ MPM_DEV float sigmoid_parts(float l, float& slope) {
   return l >= 0.0f ? q : zq;
 }
 
+// A warp per token, the next token's logits in flight.  8191 tokens of 128 bf16
+// experts take 5.3 us (reading and writing the logits: 0.7): the chain of five warp
+// sums and two passes through shared memory of a warp's one or two tokens, and
+// the launch.  Without the next token in flight, scores through shared memory: 9.3 us.
 constexpr int kBwdWarps = 8;
 
 template <int NE, bool SIG, bool BF16>
@@ -687,7 +748,8 @@ static cudaError_t route_forward(RouteArgs a, cudaStream_t st) {
   const bool small = a.T <= kClusterTokens;
   int W = route_warps(NE);
   if (small && a.T < (long long)kClusterCtas * W) W = (int)((a.T + kClusterCtas - 1) / kClusterCtas);
-  const size_t smem = (size_t)(2 * a.E + 3) / 4 * 16 + W * sizeof(RouteWarp<NE>);   // holds [W][E] too
+  const size_t warp_bytes = std::max(sizeof(RouteWarp), (size_t)a.E * 4);
+  const size_t smem = (size_t)(2 * a.E + 3) / 4 * 16 + W * warp_bytes;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cfg.stream = st;
