@@ -581,13 +581,19 @@ MPM_DEV float sigmoid_parts(float l, float& slope) {
 }
 
 // A warp per token, the next token's logits in flight.  8191 tokens of 128 bf16
-// experts take 5.3 us (reading and writing the logits: 0.7): the chain of five warp
+// experts take 4.9 us (reading and writing the logits: 0.7): the chain of five warp
 // sums and two passes through shared memory of a warp's one or two tokens, and
 // the launch.  Without the next token in flight, scores through shared memory: 9.3 us.
 constexpr int kBwdWarps = 8;
+// Blocks an SM, which is also the grid: with more blocks than are resident some
+// warps have a token more than the others (32768 x 256: 23.7 us with 6 an SM,
+// 19.9 with the 4 that fit; 8191 x 128: 5.5 with 5 resident of 6, 4.9 with all 6)
+constexpr int bwd_blocks(int ne, bool sig) {
+  return ne <= 2 ? 8 : ne <= 4 ? (sig ? 5 : 6) : ne <= 8 ? 4 : ne <= 16 ? (sig ? 2 : 3) : 1;
+}
 
 template <int NE, bool SIG, bool BF16>
-__global__ void __launch_bounds__(32 * kBwdWarps) route_bwd_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(32 * kBwdWarps, bwd_blocks(NE, SIG)) route_bwd_kernel(const RouteArgs a) {
   extern __shared__ __align__(16) uint8_t route_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float* shd = reinterpret_cast<float*>(route_smem) + warp * (32 * NE);      // the token's ds
@@ -781,7 +787,7 @@ static cudaError_t route_forward(RouteArgs a, cudaStream_t st) {
 
 template <int NE, bool SIG, bool BF16>
 static cudaError_t route_backward(RouteArgs a, cudaStream_t st) {
-  const long long n = (a.T + kBwdWarps - 1) / kBwdWarps, most = 152 * 6;
+  const long long n = (a.T + kBwdWarps - 1) / kBwdWarps, most = 152 * bwd_blocks(NE, SIG);
   return launch_serial(route_bwd_kernel<NE, SIG, BF16>, dim3((unsigned)(n < most ? n : most)),
                        dim3(32 * kBwdWarps), (size_t)kBwdWarps * 32 * NE * 4, st, a);
 }
