@@ -530,11 +530,11 @@ __global__ void __launch_bounds__(1024 / C) add_rmsnorm_bwd_ring_kernel(const No
   }
 }
 
-// What the ring does not take (rows of up to 256 columns, of more than 8192, and
+// What the ring does not take (few short rows, rows of more than 8192 columns and
 // operands that start at different places of a word) has two kernels: dx from
 // one row a block (short rows: one a warp), held in registers with all its loads
 // in flight, and dw's partials from blocks of columns.  They read dy and h
-// twice; short rows are bound by latency there (19074 x 176: 16.3 us), single
+// twice; short rows are bound by latency there (2000 x 256: 6.9 us), single
 // elements by instructions (3000 x 4161 at different offsets: 72 us, where a
 // register form that kept dw beside one row at a time took 216 and the ring, at
 // equal offsets, takes 30).  WIDE rows (32 values a thread) would not fit in
@@ -793,16 +793,16 @@ static cudaError_t norm_bwd_words(const NormBwd& p, cudaStream_t st) {
 cudaError_t launch_add_rmsnorm_backward(const NormBwd& p, cudaStream_t st) {
   const bool v = p.K % 8 == 0 && vec8(p.dy, p.lddy) && vec8(p.dy2, p.lddy2) && vec8(p.h, p.ldh) &&
                  vec8(p.dh, p.lddh) && vec8(p.dx, p.lddx) && vec8(p.w, 0);
+  // few short rows are quicker in two kernels (2000 x 256: 6.9 against 7.6 us;
+  // 32768 x 256: 32.8 against 19.9; 2000 x 143: 6.9 and 8.3; 18434 x 143: 30.1 and
+  // 16.0), and the shortest at any number (30000 x 64: 15.9 and 16.6)
+  const bool ring = p.K > 256 || (p.K > 128 && p.M >= 4096);
   if (v) {
-    if (p.K <= 256) return norm_bwd_two<8, 1, true>(p, st);
-    if (p.K > 8192) return norm_bwd_two<8, 4, false>(p, st);
-    return norm_bwd_words<false>(p, st);
+    if (ring && p.K <= 8192) return norm_bwd_words<false>(p, st);
+    return p.K <= 256 ? norm_bwd_two<8, 1, true>(p, st) : norm_bwd_two<8, 4, false>(p, st);
   }
-  // The same for rows that start anywhere; few short ones are quicker in two
-  // kernels (2000 x 143: 6.9 against 8.3 us; 18434 x 143: 30.1 against 16.0)
-  if ((p.K > 256 || (p.K > 128 && p.M >= 4096)) && p.K + 7 <= 8192 && same_words(p.dy, p.lddy, p.dy2, p.lddy2) &&
-      same_words(p.dy, p.lddy, p.h, p.ldh) && same_words(p.dy, p.lddy, p.dh, p.lddh) &&
-      same_words(p.dy, p.lddy, p.dx, p.lddx))
+  if (ring && p.K + 7 <= 8192 && same_words(p.dy, p.lddy, p.dy2, p.lddy2) && same_words(p.dy, p.lddy, p.h, p.ldh) &&
+      same_words(p.dy, p.lddy, p.dh, p.lddh) && same_words(p.dy, p.lddy, p.dx, p.lddx))
     return norm_bwd_words<true>(p, st);
   if (p.K <= 128) return norm_bwd_two<1, 4, true>(p, st);
   if (p.K <= 4 * kNormMaxThreads) return norm_bwd_two<1, 4, false>(p, st);
