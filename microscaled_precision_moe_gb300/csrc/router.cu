@@ -40,8 +40,8 @@ namespace mpm {
 constexpr int kRouteMaxParts = 152;                     // one block of up to 32 warps on each SM
 constexpr int kClusterCtas = 8;
 // One cluster routes up to this many tokens: no second kernel, but 8 SMs (256
-// experts, sigmoid: 7.2 against 7.9 us at 160 tokens, 8.5 and 7.7 at 256)
-constexpr long long kClusterTokens = 192;
+// experts, sigmoid: 6.4 us at 100 tokens, 7.1 at 160; else 6.5 at 200)
+constexpr long long kClusterTokens = 128;
 constexpr float kDeadLogit = -3.3895313892515355e38f;   // bf16's lowest finite value
 constexpr float kLargest = 3.4028234663852886e38f;
 constexpr float kLog2e = 1.44269504088896341f;
@@ -737,8 +737,16 @@ static int route_ne(int E) {
   while (ne * 32 < E) ne *= 2;
   return ne;
 }
+// Warps of a block outside the cluster: as many as its registers allow, but few
+// tokens are spread over the SMs, down to 8 a block (512 tokens of 256 experts,
+// sigmoid: 7.9 us by 32 warps, 6.7 by 8, 7.2 by 4 and twice the partials)
+static int route_block_warps(long long T, int E) {
+  const int most = route_warps(route_ne(E));
+  const long long w = (T + kRouteMaxParts - 1) / kRouteMaxParts;
+  return (int)std::min<long long>(most, std::max<long long>(w, 8));
+}
 static int route_parts(long long T, int E) {
-  const int w = route_warps(route_ne(E));
+  const int w = route_block_warps(T, E);
   const long long n = (T + w - 1) / w;
   return (int)(n < kRouteMaxParts ? n : kRouteMaxParts);
 }
@@ -754,7 +762,7 @@ static bool route_vec(const void* p, long long ld, int bf16, int E) {
 template <int NE, bool SIG, bool BF16>
 static cudaError_t route_forward(RouteArgs a, cudaStream_t st) {
   const bool small = a.T <= kClusterTokens;
-  int W = route_warps(NE);
+  int W = small ? route_warps(NE) : route_block_warps(a.T, a.E);
   if (small && a.T < (long long)kClusterCtas * W) W = (int)std::max<long long>((a.T + kClusterCtas - 1) / kClusterCtas, 4);   // four for the sums
   const size_t warp_bytes = std::max(sizeof(RouteWarp), (size_t)a.E * 4);
   const size_t smem = (size_t)(2 * a.E + 3) / 4 * 16 + W * warp_bytes;
