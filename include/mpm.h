@@ -454,9 +454,9 @@ mpm_status mpm_add_rmsnorm_backward(const void* dy_dev, int64_t lddy,
  * mpm_moe_build_segments.  The workload routings of the pages are softmax,
  * top-k with ties to the lower expert and renormalised weights.
  * ws_dev: at least mpm_moe_route_workspace_bytes(T, E) bytes, 4-byte aligned,
- * uninitialised; NULL where that is 0 (few tokens).  Requirements: T >= 1, 1 <= E <= 1024, 1 <= k <= min(E, 64),
- * T * k <= 2^30, ld >= E, scale finite, bias_dev only with sigmoid scores;
- * pointers aligned to their element.
+ * uninitialised; NULL where that is 0 (few tokens).  Requirements: T >= 1,
+ * 1 <= E <= 1024, 1 <= k <= min(E, 64), T * k <= 2^30, ld >= E, scale finite,
+ * bias_dev only with sigmoid scores; pointers aligned to their element.
  */
 size_t mpm_moe_route_workspace_bytes(int64_t T, int64_t E);
 mpm_status mpm_moe_route(const void* logits_dev, int logits_dtype, int64_t T, int64_t E, int64_t ld,

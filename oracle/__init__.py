@@ -28,5 +28,8 @@ Modules:
   moe      - expert segments and permutation, fp64 grouped GEMMs, SwiGLU,
              combine, the MXFP8 and BF16 backward, the single-pass FC2 with
              online amax compensation (report section 5.6)
+  norm     - residual RMSNorm and its gradient (fp64)
+  router   - top-k router, balance loss, their gradient, the gradient of the
+             routing weights (fp64)
   metrics  - relative L2, SNR, MAE, relative Frobenius error
 """
