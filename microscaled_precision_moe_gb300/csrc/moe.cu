@@ -398,9 +398,10 @@ __global__ void __launch_bounds__(256) gather_nvfp4_kernel(const uint4* __restri
 // of 128 rows, one word (a row's four scales of a tile) per thread and tile.
 // Bound by the bytes, K (1 + 1/32) written a row and a token's row read once from
 // DRAM (its k copies come from L2): 8192 tokens x 8 x 2048 take 33.5 us, 5.7 TB/s
-// and 0.84 of the measured copy; 64 x 8 x 7168, 26 MB written in 16-row
-// segments (mostly padding), 5.4 us, 4 by its bytes.  Codes and scales of 128 rows in one block
-// took 39.2 and 24 us: too few loads in flight, too few blocks for 64 tokens.
+// and 0.84 of the measured copy; 64 x 8 x 7168, 26 MB written in 16-row segments
+// (mostly padding), 5.4 us, 4 by its bytes.  Codes and scales of 128 rows in one
+// block took 39.2 and 24 us: too few loads in flight, too few blocks for 64
+// tokens.  Bulk copies through shared memory, a row a lane: 35.9 and 5.3 us.
 constexpr int kGatherRows = 16, kGatherTiles = 8, kGatherChunk = 128;   // 16-byte words
 
 __global__ void __launch_bounds__(256) gather_mxfp8_kernel(const uint4* __restrict__ src_q,
