@@ -397,13 +397,16 @@ __global__ void __launch_bounds__(256) gather_nvfp4_kernel(const uint4* __restri
 // a lane in flight together); the others write whole runs of up to 8 scale tiles
 // of 128 rows, one word (a row's four scales of a tile) per thread and tile.
 // Bound by the bytes, K (1 + 1/32) written a row and a token's row read once from
-// DRAM (its k copies come from L2): 8192 tokens x 8 x 2048 take 33.5 us, 5.7 TB/s
-// and 0.84 of the measured copy; 64 x 8 x 7168, 26 MB written in 16-row segments
-// (mostly padding), 5.4 us, 4 by its bytes.  Codes and scales of 128 rows in one
+// DRAM (its k copies come from L2): 8192 tokens x 8 x 2048 take 31.0 us, 6.2 TB/s
+// and 0.91 of the measured copy; 64 x 8 x 7168, 26 MB written in 16-row segments
+// (mostly padding), 5.4 us, 4 by its bytes.  STREAM, for outputs that L2 cannot
+// hold: codes stored to leave it first, so that the tokens' rows stay (33.5 us
+// without; a smaller output is left there for the GEMM that reads it next).  Codes and scales of 128 rows in one
 // block took 39.2 and 24 us: too few loads in flight, too few blocks for 64
 // tokens.  Bulk copies through shared memory, a row a lane: 35.9 and 5.3 us.
 constexpr int kGatherRows = 16, kGatherTiles = 8, kGatherChunk = 128;   // 16-byte words
 
+template <bool STREAM>
 __global__ void __launch_bounds__(256) gather_mxfp8_kernel(const uint4* __restrict__ src_q,
                                                           const uint8_t* __restrict__ src_s,
                                                           int T, long long K, int k,
@@ -445,7 +448,10 @@ __global__ void __launch_bounds__(256) gather_mxfp8_kernel(const uint4* __restri
       uint4* d = dst_q + (r0 + i) * q16;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (r0 + i < rend && c0 + 32 * j < q16) d[c0 + 32 * j] = v[i][j];
+        if (r0 + i < rend && c0 + 32 * j < q16) {
+          if (STREAM) __stcs(d + c0 + 32 * j, v[i][j]);
+          else d[c0 + 32 * j] = v[i][j];
+        }
     }
     return;
   }
@@ -676,7 +682,8 @@ cudaError_t launch_gather_mxfp8(const uint8_t* q, const uint8_t* sc, long long T
   const long long ntiles = (K / 32 + 3) / 4, groups = (ntiles + kGatherTiles - 1) / kGatherTiles;
   const long long blocks = code_blocks + (cap + 127) / 128 * groups;
   if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  return launch_serial(gather_mxfp8_kernel, dim3((unsigned)blocks), dim3(256), 0, s,
+  const auto kernel = cap * K > (96ll << 20) ? gather_mxfp8_kernel<true> : gather_mxfp8_kernel<false>;
+  return launch_serial(kernel, dim3((unsigned)blocks), dim3(256), 0, s,
                        reinterpret_cast<const uint4*>(q), sc, (int)T, K, k, perm, seg_end, cap,
                        code_blocks, reinterpret_cast<uint4*>(dst_q), dst_s, status);
 }
