@@ -59,7 +59,6 @@ struct RawBf16 {
 };
 
 MPM_DEV float bf16_f(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-MPM_DEV uint16_t f_bf16(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
 // What a vector is computed in: pairs of fp32 (VEC = 8), or one
 template <int VEC>
