@@ -118,6 +118,27 @@ def test_softmax_pitch_ties_masks(normalize, scale):
     assert o["ids"][7].tolist() == [0, 1, 2, 3, 4, 5] and not o["prob"][7].any()
 
 
+@pytest.mark.parametrize("T,E,k", [(300, 256, 8), (700, 60, 4), (90, 700, 20), (40, 40, 40)])
+@pytest.mark.parametrize("std,shift", [(1.0, 0.0), (0.01, 0.0), (12.0, 0.0), (1.0, -15.0), (1.0, 9.0), (30.0, -70.0)])
+@pytest.mark.parametrize("bias", [None, 0.1, 300.0, float("inf")])
+def test_sigmoid_choice_is_by_the_fp32_keys(T, E, k, std, shift, bias):
+    """Saturated, vanishing and nearly equal scores: the choice is that of the
+    scores and sums rounded to fp32, ties to the lower expert."""
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    l = torch.randn(T, E, device="cuda", generator=g) * std + shift
+    b = None
+    if bias is not None:
+        b = torch.randn(E, device="cuda", generator=g) * (bias if bias < 1e3 else 1.0)
+        if bias > 1e3:
+            b[::7] = bias
+    key = 1.0 / (1.0 + torch.exp(-l))
+    if b is not None:
+        key = key + b
+    want = torch.sort(key, dim=1, descending=True, stable=True)[1][:, :k]
+    o = _ops().moe_route(l, k, score="sigmoid", bias=b)
+    assert torch.equal(o["ids"].long(), want)
+
+
 def test_lowest_fp32_value_is_a_mask_too():
     l = _logits(2, 40, 16)
     l[:, 5] = torch.finfo(torch.float32).min
