@@ -11,6 +11,7 @@
 //
 // A row is held in the registers of the threads of one block, or of one warp, so
 // every operand is read once.
+#include <algorithm>
 #include <atomic>
 #include "norm.cuh"
 #include "launch.cuh"
@@ -670,14 +671,16 @@ static unsigned norm_threads(int K, int per_thread) {
 // The ring form: blocks an SM, and the stages that fit beside one another
 struct NormRing { unsigned threads; int blocks, stages, smem; };
 // 512 threads an SM, 16 columns each (8 columns and 1024 threads: 15.8 against
-// 15.1 us at 4093 x 1544, the same at 8192 x 2048)
-static int ring_blocks(int K) {          // K: columns of the words that a row touches
-  const int n = 512 / (int)norm_threads(K, 8 * kRingWords);
-  return n < 1 ? 1 : n;
+// 15.1 us at 4093 x 1544, the same at 8192 x 2048); but two blocks of up to 320
+// where their registers fit beside one another and there are rows for them (4000
+// x 4480: 27.4 against 31.3 us, 4000 x 5120: 30.6 and 32.9; 200 x 4480: 7.7 and 6.7)
+constexpr int kRingPair = 320;
+static int ring_blocks(long long M, int K, int pair) {    // K: columns of the words that a row touches
+  const int threads = (int)norm_threads(K, 8 * kRingWords), n = 512 / threads;
+  return n <= 1 && threads <= pair && M >= 1024 ? 2 : (n < 1 ? 1 : n);
 }
-static NormRing norm_ring(int K, int per_thread, int stage) {
-  NormRing r{norm_threads(K, per_thread), 0, 0, 0};
-  r.blocks = ring_blocks(K);
+static NormRing norm_ring(int blocks, int K, int per_thread, int stage) {
+  NormRing r{norm_threads(K, per_thread), blocks, 0, 0};
   r.stages = (222 * 1024 / r.blocks - 1024) / stage;
   if (r.stages > kRingStages) r.stages = kRingStages;
   r.smem = r.stages * stage;
@@ -734,7 +737,7 @@ cudaError_t launch_add_rmsnorm(const NormFwd& p, cudaStream_t st) {
 // Blocks of the backward's ring, each with its own partial dw (the two-kernel
 // form makes no more)
 long long rmsnorm_backward_parts(long long M, int K) {
-  const long long most = 152ll * ring_blocks(K);
+  const long long most = 152ll * ring_blocks(M, K, kRingPair);
   return M < most ? M : most;
 }
 
@@ -754,8 +757,10 @@ static cudaError_t norm_dw(const NormBwd& p, long long parts, cudaStream_t st) {
 template <auto kernel, bool OFF>
 static cudaError_t norm_bwd_ring(const NormBwd& p, int operands, cudaStream_t st) {
   const int n = OFF ? (p.K + 14) / 8 * 8 : p.K;      // columns of the words that a row touches, at most
-  const NormRing r = norm_ring(n, 8 * kRingWords, 2 * n * operands);
-  const long long blocks = rmsnorm_backward_parts(p.M, n);       // no more than of K
+  // 128 registers by words, 97 with two operands, 84 with more
+  const int pair = OFF ? 0 : (operands == 2 ? 288 : kRingPair);
+  const NormRing r = norm_ring(ring_blocks(p.M, n, pair), n, 8 * kRingWords, 2 * n * operands);
+  const long long blocks = std::min(p.M, 152ll * r.blocks);      // no more than the workspace has parts
   const cudaError_t err = launch_ring<kernel>(r, blocks, p, st);
   return err != cudaSuccess ? err : norm_dw(p, blocks, st);
 }
