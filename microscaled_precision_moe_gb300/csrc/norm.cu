@@ -342,6 +342,11 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) add_
 // its row of the workspace, which a second kernel sums in a fixed order (no
 // atomics: the same bytes every time).
 
+// What bounds a thread's registers: 512 threads, but with two operands alone the
+// compiler then takes 97, one too many for two blocks of 320 (4000 x 4480: 33.8
+// against 22.9 us, 8192 x 2048: 22.3 against 21.2)
+constexpr int ring_most_threads(int c, bool more) { return more ? 1024 / c : 640; }
+
 // Rows of 16-byte aligned operands stream through a ring of S stages in shared
 // memory, one row's operands each, by bulk copies that thread 0 issues: S - 1
 // rows are in flight whatever the threads are doing.  A thread takes C words of
@@ -359,7 +364,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) add_
 // elements of the rows beside it, which are masked; at the ends of the operand,
 // where there may be nothing beside it, it takes the row's own elements.
 template <int C, bool TWO, bool RES, bool OFF>
-__global__ void __launch_bounds__(1024 / C) add_rmsnorm_bwd_ring_kernel(const NormBwd p, int S) {
+__global__ void __launch_bounds__(ring_most_threads(C, TWO || RES || OFF)) add_rmsnorm_bwd_ring_kernel(const NormBwd p, int S) {
   constexpr int NT = 2 + (TWO ? 1 : 0) + (RES ? 1 : 0);
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float sh[2][32];
@@ -757,9 +762,8 @@ static cudaError_t norm_dw(const NormBwd& p, long long parts, cudaStream_t st) {
 template <auto kernel, bool OFF>
 static cudaError_t norm_bwd_ring(const NormBwd& p, int operands, cudaStream_t st) {
   const int n = OFF ? (p.K + 14) / 8 * 8 : p.K;      // columns of the words that a row touches, at most
-  // 128 registers by words, 97 with two operands, 84 with more
-  const int pair = OFF ? 0 : (operands == 2 ? 288 : kRingPair);
-  const NormRing r = norm_ring(ring_blocks(p.M, n, pair), n, 8 * kRingWords, 2 * n * operands);
+  // by words a thread has 128 registers: no room for a second block
+  const NormRing r = norm_ring(ring_blocks(p.M, n, OFF ? 0 : kRingPair), n, 8 * kRingWords, 2 * n * operands);
   const long long blocks = std::min(p.M, 152ll * r.blocks);      // no more than the workspace has parts
   const cudaError_t err = launch_ring<kernel>(r, blocks, p, st);
   return err != cudaSuccess ? err : norm_dw(p, blocks, st);
