@@ -337,10 +337,10 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) add_
 //   dx = rstd (g - xh mean_K(g xh)) + dh,   dw = sum over rows of dy xh,
 // computed from u = dy rstd as t = u w, c = sum_K t h,
 //   dx = t - h (rstd^2 c / K) + dh,         dw += u h.
-// Blocks walk rows blockIdx.x, blockIdx.x + gridDim.x, ... (or groups of R of
-// them); each keeps its columns' share of dw in fp32 registers and writes it to
-// its row of the workspace, which a second kernel sums in a fixed order (no
-// atomics: the same bytes every time).
+// Blocks walk rows blockIdx.x, blockIdx.x + gridDim.x, ...; each keeps its
+// columns' share of dw in fp32 registers and writes it to its row of the
+// workspace, which a second kernel sums in a fixed order (no atomics: the same
+// bytes every time).
 
 // What bounds a thread's registers: 512 threads, but with two operands alone the
 // compiler then takes 97, one too many for two blocks of 320 (4000 x 4480: 33.8
@@ -360,7 +360,8 @@ constexpr int ring_most_threads(int c, bool more) { return more ? 1024 / c : 640
 //
 // OFF: rows that start anywhere, by their words.  A block's rows start at one
 // place of a word (the blocks are a multiple of 8, or have one row each), so its
-// threads keep their columns (8000 x 1003 takes 19.4 us, 43 by single elements).  A copy takes whole words, and with them a few
+// threads keep their columns (8000 x 1003 takes 19.4 us, 43 by single elements).
+// A copy takes whole words, and with them a few
 // elements of the rows beside it, which are masked; at the ends of the operand,
 // where there may be nothing beside it, it takes the row's own elements.
 template <int C, bool TWO, bool RES, bool OFF>
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) rmsn
 
 // Partials of dw = sum over rows of dy h rstd: one column a thread, the rows
 // blockIdx.y, blockIdx.y + gridDim.y, ..., eight of them in flight, which is
-// what its time goes by: 95 of the 256 us at 12000 x 4161
+// what its time goes by: 95 of the 256 us at 12000 x 4161 by single elements
 __global__ void __launch_bounds__(256) rmsnorm_dw_rows_kernel(const NormBwd p) {
   pdl_wait();
   pdl_launch_dependents();
