@@ -120,6 +120,18 @@ def test_nothing_outside_the_outputs_is_written(K, pad):
         assert (b[0] == 7).all() and (b[-1] == 7).all() and (b[:, K:] == 7).all()
 
 
+def test_outputs_made_together_do_not_overlap():
+    x, r, w = _rows(63, 3, 96), _rows(64, 3, 96), _weight(65, 96, True)
+    o = _ops().add_rmsnorm(x, w, residual=r, quantize=True)
+    o["dx"], o["dw"] = _ops().add_rmsnorm_backward(x, o["h"], o["rstd"], w)
+    want = {n: t.clone() for n, t in o.items()}
+    assert all(t.is_contiguous() for t in o.values())
+    for n in o:
+        o[n].zero_()
+        want[n].zero_()
+        assert all(torch.equal(o[m], want[m]) for m in o)
+
+
 @pytest.mark.parametrize("K", [2048, 7168, 1001])
 def test_in_place_residual(K):
     ops = _ops()
