@@ -438,7 +438,8 @@ mpm_status mpm_add_rmsnorm_backward(const void* dy_dev, int64_t lddy,
  * token are those with the largest logit (softmax) or score + bias (sigmoid;
  * bias_dev, nullable, fp32 [E], sways the choice only), in descending order,
  * ties to the lower expert.  prob = the chosen scores, divided by their sum if
- * `normalize` (a sum of 0 gives 0), times `scale`.
+ * `normalize` (a sum of 0 gives 0), times `scale`.  A score is an fp32 number: the
+ * sigmoid of a logit below -88.7 is 0, and passes no gradient.
  * An expert is out of reach of a token where its logit or bias is NaN or at
  * most bf16's lowest finite value (so -inf and either type's lowest value):
  * its score is 0 and it is chosen, lowest expert first and with weight 0, only

@@ -30,8 +30,9 @@
 // depends on the last bit of 1 / (1 + expf(-l)), with the IEEE reciprocal, and of
 // its sum with the bias: tau is found among keys by the hardware functions and
 // lowered by a bound on what separates the two, and only the candidates, one a
-// lane, get the exact ones (32768 x 256: 28.0 -> 24.7 us; 20000 x 400: 38.0 ->
-// 28.7; 64 x 256: 5.6 -> 5.2).
+// lane, get the exact ones (32768 x 256: 28.0 -> 25.2 us; 20000 x 400: 38.0 ->
+// 29.3; 64 x 256: 5.6 -> 5.4).  Weights are of the exact scores; load and loss, sums
+// over many, of the approximate ones.
 // Sums over tokens go through per-block partials added in a fixed order (no
 // floating-point atomics).
 #include <algorithm>
@@ -49,6 +50,13 @@ constexpr long long kClusterTokens = 128;
 constexpr float kDeadLogit = -3.3895313892515355e38f;   // bf16's lowest finite value
 constexpr float kLargest = 3.4028234663852886e38f;
 constexpr float kLog2e = 1.44269504088896341f;
+// Sigmoid scores may be fp32 subnormals (logits of -88.7 to -87.3), which the
+// hardware's approximations flush to 0.  Where a sum of scores is below kVanishing
+// (all of its logits below -13.8) a flushed one would matter, and exact scores times
+// kVanishingScale take the place of the approximate ones: the factor leaves their
+// ratios as they are.  Elsewhere a flushed score is less than 2^-106 of the sum.
+constexpr float kVanishing = 9.5367431640625e-7f;           // 2^-20
+constexpr float kVanishingScale = 1.8446744073709552e19f;   // 2^64
 
 // warps of a block: as many as its registers allow
 constexpr int route_warps(int ne) { return ne <= 8 ? 32 : (ne <= 16 ? 16 : 8); }
@@ -179,10 +187,17 @@ MPM_DEV void route_one_by_one(const RouteArgs& a, int t, int lane, const float (
       if (on && top > 1u) atomicAdd(&sh_counts[e], 1);
     }
   }
-  const float f = !a.normalize ? unit : (d > 0.0f ? __fdiv_rn(1.0f, d) : 0.0f);
-  const float sc = on ? __fmul_rn(f, a.scale) : 0.0f;
-  if (lane < a.k) a.prob[t * a.k + lane] = __fmul_rn(w0, sc);
-  if (lane + 32 < a.k) a.prob[t * a.k + 32 + lane] = __fmul_rn(w1, sc);
+  float f = unit;
+  if (a.normalize) {
+    if (d < kVanishing) {                               // sigmoid scores only, or none in reach
+      w0 = __fmul_rn(w0, kVanishingScale);
+      w1 = __fmul_rn(w1, kVanishingScale);
+      d = __fmul_rn(d, kVanishingScale);
+    }
+    f = d > 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
+  }
+  if (lane < a.k) a.prob[t * a.k + lane] = on ? __fmul_rn(__fmul_rn(w0, f), a.scale) : 0.0f;
+  if (lane + 32 < a.k) a.prob[t * a.k + 32 + lane] = on ? __fmul_rn(__fmul_rn(w1, f), a.scale) : 0.0f;
 }
 
 // a warp's shared memory in the token loop: the candidates' keys and experts
@@ -310,8 +325,9 @@ MPM_DEV void route_token(const RouteArgs& a, int t, int next, int lane, RawLogit
     }
   } else {
     sum = warp_sum(lane_sum(s));
+    quick = quick && sum >= kVanishing;  // else the shares are taken below
   }
-  const float share = on && sum > 0.0f ? rcp_ftz(sum) : 0.0f;
+  const float share = on && sum >= kVanishing ? rcp_ftz(sum) : 0.0f;      // (softmax: 0, or 1 and more)
   const uint64_t share2 = f32x2(share, share);
 #pragma unroll
   for (int i = 0; i < NE; i += 2)
@@ -390,7 +406,11 @@ MPM_DEV void route_token(const RouteArgs& a, int t, int next, int lane, RawLogit
       else w = chosen ? exp2_ftz(__fmaf_rn(own, kLog2e, -m2)) : 0.0f;
       float f = unit;
       if (a.normalize) {
-        const float d = warp_sum(w);
+        float d = warp_sum(w);
+        if (SIG && d < kVanishing) {
+          w = __fmul_rn(w, kVanishingScale);
+          d = __fmul_rn(d, kVanishingScale);
+        }
         f = d > 0.0f ? rcp_ftz(d) : 0.0f;
       }
       if (chosen) {
@@ -410,6 +430,12 @@ MPM_DEV void route_token(const RouteArgs& a, int t, int next, int lane, RawLogit
     for (int i = 0; i < NE; ++i) {
       s[i] = sigmoid_exact(l[i]);
       sig_key[i] = l[i] > -INFINITY ? __fadd_rn(s[i], bias[i]) : -INFINITY;
+    }
+    if (on && sum < kVanishing) {
+      sum = __fmul_rn(warp_sum(lane_sum(s)), kVanishingScale);
+      const float f = sum > 0.0f ? rcp_ftz(sum) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) load[i] = __fmaf_rn(__fmul_rn(s[i], kVanishingScale), f, load[i]);
     }
   }
   route_one_by_one<NE, BF16>(a, t, lane, key, s, unit, on, sh_counts);

@@ -1,0 +1,114 @@
+"""Sigmoid routing on the GPU where scores vanish, saturate or are swayed by a
+bias, in every type and width of the kernels.
+
+The choice is by the scores and sums rounded to fp32, which elementary torch
+operations give; weights, loads, loss and gradient are those of the choice, in
+fp64.  A score is an fp32 number: the sigmoid of a logit below about -88.7 is 0.
+
+Bounds as for the router's other tests: weights within 1e-5 of themselves (a
+score that is an fp32 subnormal is off by at most 2^-150 / 2^-128 = 2.4e-7
+more), loads within 2e-5, gradients within 2e-5 of the sum of their terms'
+magnitudes, a bf16 result by 2^-8 of itself more.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import router as R
+from tests.gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+
+PROB, LOAD, GRAD, BF16 = 1e-5, 2e-5, 2e-5, 2.0 ** -8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def _close(got, want, tol, what):
+    got = got.float().cpu().numpy().astype(np.float64)
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size}, first {np.argwhere(bad)[0]}: " \
+                          f"{got[bad][0]} for {np.broadcast_to(want, got.shape)[bad][0]}"
+
+
+def _route(l, k, normalize, scale, bias, mask):
+    """The call, and its outputs checked: (outputs, logits in fp64 with -inf
+    where the score is 0, ids)."""
+    from microscaled_precision_moe_gb300 import ops
+    T, E = l.shape
+    o = ops.moe_route(l, k, score="sigmoid", normalize=normalize, scale=scale, bias=bias, token_mask=mask)
+    f = l.float()
+    live = f > R.LOWEST
+    if bias is not None:
+        live &= (bias > R.LOWEST)[None]
+    s32 = 1.0 / (1.0 + torch.exp(-f.clamp(max=R.FLT_MAX)))
+    key = torch.where(live, s32 if bias is None else s32 + bias, torch.full_like(f, -torch.inf))
+    ids = torch.sort(key, dim=1, descending=True, stable=True)[1][:, :k]
+    assert torch.equal(o["ids"].long(), ids)
+    keep = np.ones(T, bool) if mask is None else mask.cpu().numpy()
+    picked = torch.gather(live, 1, ids).cpu().numpy() & keep[:, None]
+    ids = ids.cpu().numpy()
+    counts = np.bincount(ids[picked], minlength=E)
+    assert np.array_equal(o["counts"].cpu().numpy(), counts) and int(o["n_tokens"]) == keep.sum()
+    ref = torch.where(live & (s32 > 0), f.double(), torch.full_like(f, -torch.inf).double()).cpu().numpy()
+    s, _, _ = R.scores(ref, "sigmoid")
+    prob = R.weights(s, ids, normalize, scale) * keep[:, None]
+    total = s.sum(1, keepdims=True)
+    load = (s / np.where(total > 0, total, 1.0) * keep[:, None]).sum(0) / max(keep.sum(), 1)
+    loss = E / (k * max(keep.sum(), 1)) * np.dot(counts, load)
+    _close(o["prob"], prob, PROB * np.abs(prob) + 1e-30, "prob")
+    _close(o["load"], load, LOAD * load + 1e-12, "load")
+    _close(o["loss"], loss, LOAD * loss + 1e-12, "loss")
+    assert ops.get_device_status() == 0
+    return o, ref, ids
+
+
+def _bias(E, g):
+    """Distinct sways, one infinite, some experts out of reach."""
+    b = 0.3 * torch.randn(E, device="cuda", generator=g)
+    b[E // 3], b[E // 2], b[-1] = float("-inf"), float("nan"), torch.finfo(torch.bfloat16).min
+    return b
+
+
+def _logits(T, E, std, shift, bf16, g):
+    l = torch.randn(T, E, device="cuda", generator=g) * std + shift
+    return l.to(torch.bfloat16) if bf16 else l
+
+
+CASES = [(40, 33, 5, 1.0, 0.0), (300, 60, 4, 12.0, -40.0), (130, 128, 8, 30.0, -70.0), (257, 256, 8, 1.0, -15.0),
+         (70, 300, 16, 1.0, 9.0), (150, 700, 20, 4.0, -87.0), (9, 1024, 40, 2.0, 0.0)]
+
+
+@pytest.mark.parametrize("T,E,k,std,shift", CASES)
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_forward(T, E, k, std, shift, bf16, biased, normalize):
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    l = _logits(T, E, std, shift, bf16, g)
+    mask = torch.arange(T, device="cuda") % 6 != 4
+    _route(l, k, normalize, 2.5, _bias(E, g) if biased else None, mask)
+
+
+@pytest.mark.parametrize("k", [1, 2, 4])
+@pytest.mark.parametrize("E,equal", [(8, False), (64, False), (64, True), (256, True)])
+@pytest.mark.parametrize("biased", [True, False])
+def test_weights_of_subnormal_scores(k, E, equal, biased):
+    """Every score of a row below fp32's normal range (logits of -88.7 to -85):
+    normalised weights are finite shares of one.  With masses of equal keys the
+    choice is made one expert after the other."""
+    g = torch.Generator(device="cuda").manual_seed(k + E)
+    l = -88.7 + 3.7 * torch.rand(200, E, device="cuda", generator=g)
+    if equal:
+        l = l[:, :1].expand(200, E).contiguous()
+    b = 0.01 * torch.randn(E, device="cuda", generator=g) if biased and not equal else None
+    if biased and equal:
+        b = torch.zeros(E, device="cuda")
+    o, _, _ = _route(l, k, True, 2.5, b, None)
+    total = o["prob"].double().sum(1)
+    assert (total - 2.5).abs().max() < 2.5 * PROB
+    # the shares of a token whose scores are all that small count as any other's
+    assert abs(float(o["load"].double().sum()) - 1.0) < LOAD
