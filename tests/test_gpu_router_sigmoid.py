@@ -112,3 +112,68 @@ def test_weights_of_subnormal_scores(k, E, equal, biased):
     assert (total - 2.5).abs().max() < 2.5 * PROB
     # the shares of a token whose scores are all that small count as any other's
     assert abs(float(o["load"].double().sum()) - 1.0) < LOAD
+
+
+def _gradient(l, k, normalize, scale, bias, mask, size, seed):
+    """The gradient of weights and loss, apart and together, where a score of 0
+    passes nothing on."""
+    from microscaled_precision_moe_gb300 import ops
+    o, ref, ids = _route(l, k, normalize, scale, bias, mask)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    dprob = torch.randn(ids.shape, device="cuda", generator=g) * size
+    dloss = torch.full((1,), size, device="cuda")
+    for dp, dl in ((dprob, dloss), (dprob, None), (None, dloss)):
+        got = ops.moe_route_backward(l, o["ids"], o["counts"], o["n_tokens"], dprob=dp, dloss=dl, score="sigmoid",
+                                     normalize=normalize, scale=scale, bias=bias, token_mask=mask)
+        want, mag = R.route_backward(ref, ids, o["counts"].cpu().numpy(),
+                                     np.zeros(ids.shape) if dp is None else dp.cpu().numpy(),
+                                     0.0 if dl is None else size, "sigmoid", normalize, scale, None,
+                                     None if mask is None else mask.cpu().numpy())
+        _close(got, want, GRAD * mag + 1e-30 * max(size, 1.0) + (BF16 * np.abs(want) if l.dtype == torch.bfloat16 else 0),
+               "dlogits")
+    assert ops.get_device_status() == 0
+
+
+@pytest.mark.parametrize("T,E,k,std,shift", CASES)
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_gradient(T, E, k, std, shift, bf16, biased, normalize):
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    l = _logits(T, E, std, shift, bf16, g)
+    mask = torch.arange(T, device="cuda") % 6 != 4
+    _gradient(l, k, normalize, 2.5, _bias(E, g) if biased else None, mask, 1.0, E)
+
+
+@pytest.mark.parametrize("k", [1, 2, 4])
+@pytest.mark.parametrize("lo,hi", [(-88.7, -85.0), (-87.3, -86.5), (-88.7, -20.0), (-110.0, -80.0)])
+@pytest.mark.parametrize("biased", [True, False])
+@pytest.mark.parametrize("size", [0.01, 30.0, 1e4])
+def test_gradient_of_subnormal_scores(k, lo, hi, biased, size):
+    """Normalised weights of scores near and below fp32's normal range: their
+    gradient is of the order of dprob, and so is the kernel's, whatever the sum
+    of the scores."""
+    g = torch.Generator(device="cuda").manual_seed(k)
+    l = lo + (hi - lo) * torch.rand(120, 64, device="cuda", generator=g)
+    b = 0.01 * torch.randn(64, device="cuda", generator=g) if biased else None
+    _gradient(l, k, True, 2.5, b, None, size, 7)
+
+
+def test_extreme_rows_have_finite_gradients():
+    """Saturated, vanishing and huge logits, every row of the gradient."""
+    from microscaled_precision_moe_gb300 import ops
+    g = torch.Generator(device="cuda").manual_seed(10)
+    l = torch.randn(30, 24, device="cuda", generator=g) * 2
+    l[1] *= 1e4
+    l[2] = -90.0 - torch.arange(24, device="cuda")      # sigmoids that are 0 in fp32
+    l[3] = 3e38
+    l[3, :4] = -3e38
+    l[4] = -88.0
+    l[5] = -87.3
+    for normalize in (True, False):
+        o = ops.moe_route(l, 4, score="sigmoid", normalize=normalize)
+        d = ops.moe_route_backward(l, o["ids"], o["counts"], o["n_tokens"], score="sigmoid", normalize=normalize,
+                                   dprob=30.0 * torch.randn(30, 4, device="cuda", generator=g),
+                                   dloss=torch.full((1,), 30.0, device="cuda"))
+        assert torch.isfinite(o["prob"]).all() and torch.isfinite(o["loss"]).all() and torch.isfinite(d).all()
+        assert not d[2].any() and not o["prob"][2].any()
