@@ -53,6 +53,7 @@ class MoEBlock:
         e = lambda *s, dtype=bf: torch.empty(*s, dtype=dtype, device=dev)
         self.norm = {"y": e(T, H), "h": e(T, H), "rstd": e(T, dtype=f32)}
         self._h = None                               # what the last norm was taken of
+        self._kept = False                           # whether the buffers are those of a whole forward
         self.logits_p = e(T, self.Ep, dtype=f32)
         self.logits = self.logits_p[:, :E]
         self.route = None
@@ -79,6 +80,7 @@ class MoEBlock:
                              self.norm["y"], self.wr, None, 0, None, 0, self.logits_p, tile_m=256)
 
     def _norm_and_route(self, x, residual, token_mask, quantize):
+        self._kept = False
         ops.add_rmsnorm(x, self.norm_weight, residual=residual, eps=self.eps, quantize=quantize,
                         out=self.norm)
         self._h = x if residual is None else self.norm["h"]
@@ -90,15 +92,18 @@ class MoEBlock:
     def forward(self, x, residual=None, token_mask=None):
         """(out [T, H], h [T, H]) bf16: the expert layer's output and the
         residual stream h = x + residual (x itself without one).  The balance
-        loss and the expert counts are in self.route."""
+        loss and the expert counts are in self.route.  The backward reads x or
+        h and the mask again: they stay as they are until then."""
         self._norm_and_route(x, residual, token_mask, quantize=False)
         r = self.route
         out = self.experts.forward(self.norm["y"], r["ids"], r["prob"])
+        self._kept = True
         return out, self._h
 
     def infer(self, x, residual=None, token_mask=None):
         """forward without what the gradient needs, on the norm's own MXFP8
-        copy: the same bytes."""
+        copy: the same bytes.  It overwrites what an earlier forward kept, and
+        a backward after it is refused."""
         self._norm_and_route(x, residual, token_mask, quantize=True)
         r, n = self.route, self.norm
         out = self.experts.forward_quantized(n["row_q"], n["row_s"], r["ids"], r["prob"])
@@ -111,6 +116,9 @@ class MoEBlock:
 
         Returns a dict: dx [T, H] bf16 (of x and of the residual), dw_norm [H],
         dw_router [E, H], dw1, dw2 fp32."""
+        if not self._kept:
+            raise RuntimeError("backward needs a forward: infer keeps nothing for it and overwrites "
+                               "what an earlier forward kept")
         T, H, E = self.T, self.H, self.E
         r, n = self.route, self.norm
         dy, dw1, dw2 = self.experts.backward(dout)

@@ -366,6 +366,7 @@ class MXFP8MoE:
         self.dx = e(T, H, dtype=bf)
         self.dw1 = e(E, 2 * I, H, dtype=f32)
         self.dw2 = e(E, H, I, dtype=f32)
+        self._kept = False               # whether the last forward kept the backward's operands
 
     # stages of one training step, for CUDA-event marks (see forward / backward)
     # (quant_x and quant_dy quantise the routed rows straight from the token
@@ -384,6 +385,7 @@ class MXFP8MoE:
         T, H, I, E, k, cap = self.T, self.H, self.I, self.E, self.k, self.cap
         mark = mark or (lambda i: None)
         seg, perm, inv, rp = self.seg
+        self._kept = False
         mark(1)
         ops.moe_build_segments(topk_ids, topk_prob, E, out=self.seg, ws=self.seg_ws,
                                pad=self.tile_m)
@@ -404,16 +406,19 @@ class MXFP8MoE:
                              tile_m=self.tile_m)
         mark(6)
         ops.moe_combine(self.y, inv, T, k, out=self.out)
+        self._kept = True
         return self.out
 
     def forward_quantized(self, x_q, x_s, topk_ids, topk_prob):
         """The forward for rollout, on tokens that are MXFP8 already: row-wise
         codes x_q [T, H] and tiled scales x_s, as ops.add_rmsnorm or
         ops.mxfp8_quantize write them.  Their bytes are gathered into the
-        expert order and no operand of the backward is kept: the same out as
-        forward gives for the bf16 rows they were quantised from."""
+        expert order and no operand of the backward is kept (a backward after
+        it is refused): the same out as forward gives for the bf16 rows they
+        were quantised from."""
         T, H, I, E, k, cap = self.T, self.H, self.I, self.E, self.k, self.cap
         seg, perm, inv, rp = self.seg
+        self._kept = False
         ops.moe_build_segments(topk_ids, topk_prob, E, out=self.seg, ws=self.seg_ws,
                                pad=self.tile_m)
         xq, xs, dq = self.xq["row_q"], self.xq["row_s"], self.dq
@@ -434,9 +439,16 @@ class MXFP8MoE:
         [T, H] bf16: <dout, y> / prob of the rows it combined."""
         return ops.moe_combine_dprob(dout, self.y, self.seg[2], topk_prob, out=out)
 
+    def _need_forward(self):
+        if not self._kept:
+            raise RuntimeError("backward needs a forward: forward_quantized keeps no operands of it "
+                               "and overwrites those of an earlier forward")
+
     def backward(self, dy, mark=None):
-        """``mark(i)`` (optional) before STEP_STAGES[i] for i = 7..13 and once
-        more (14) at the end."""
+        """dX [T, H] bf16, dW1 [E, 2I, H] fp32, dW2 [E, H, I] fp32 after a
+        forward.  ``mark(i)`` (optional) before STEP_STAGES[i] for i = 7..13
+        and once more (14) at the end."""
+        self._need_forward()
         T, H, I, E, k, cap = self.T, self.H, self.I, self.E, self.k, self.cap
         mark = mark or (lambda i: None)
         seg, perm, inv, rp = self.seg
@@ -503,6 +515,7 @@ class MXFP8MoE:
             raise RuntimeError(f"prepare_backward_weights({mode!r}) first")
         if self.tile_m != 256:
             raise ValueError("the BF16 backward runs its GEMMs on CTA pairs: tile_m=256")
+        self._need_forward()
         H, I, E, cap = self.H, self.I, self.E, self.cap
         seg = self.seg[0]
         mark = mark or (lambda i: None)

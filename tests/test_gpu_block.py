@@ -140,3 +140,46 @@ def test_refusals():
         MoEBlock(128, 256, 256, 8, 2, w, z(4, 256), z(8, 512, 256), z(8, 256, 256))
     with pytest.raises(ValueError, match="multiple"):
         MoEBlock(128, 256, 128, 8, 2, w, z(8, 256), z(8, 256, 256), z(8, 256, 128))
+
+
+def test_backward_needs_the_forward_it_belongs_to():
+    """A rollout overwrites what the forward kept: no gradient of a mixture."""
+    b, x, res, *_ = _block(T=128, H=256, I=256, E=8, k=2)
+    dout = synth.moe_grad_out(synth.scaled(synth.MOE_30B, T=128, H=256), device="cuda")
+    b.infer(x, res)
+    with pytest.raises(RuntimeError, match="forward"):
+        b.backward(dout)
+    b.forward(x, res)
+    want = {n: t.clone() for n, t in b.backward(dout).items()}
+    b.forward(x, res)
+    b.infer(res, x)
+    with pytest.raises(RuntimeError, match="forward"):
+        b.backward(dout)
+    b.forward(x, res)
+    assert all(torch.equal(t, want[n]) for n, t in b.backward(dout).items())
+    # a rollout that is refused halfway has overwritten the norm's rows
+    with pytest.raises((TypeError, ValueError)):
+        b.infer(res, x, token_mask=torch.ones(5, dtype=torch.bool, device="cuda"))
+    with pytest.raises(RuntimeError, match="forward"):
+        b.backward(dout)
+
+
+@pytest.mark.parametrize("mode", ["mxfp8", "high_precision", "dequantized"])
+def test_expert_layer_backward_after_a_quantised_forward(mode):
+    from microscaled_precision_moe_gb300 import ops
+    from microscaled_precision_moe_gb300.moe import MXFP8MoE
+    shape = synth.scaled(synth.MOE_30B, T=128, H=256, I=256, E=8, k=2)
+    w1, w2 = synth.moe_weights(shape, device="cuda")
+    ids, prob = (t.cuda() for t in synth.routing(shape))
+    x, dout = synth.moe_activations(shape, device="cuda"), synth.moe_grad_out(shape, device="cuda")
+    layer = MXFP8MoE(128, 256, 256, 8, 2)
+    layer.quantize_weights(w1, w2)
+    if mode != "mxfp8":
+        layer.prepare_backward_weights(mode, w1, w2)
+    back = (lambda: layer.backward(dout)) if mode == "mxfp8" else (lambda: layer.backward_bf16(dout, mode))
+    layer.forward(x, ids, prob)
+    back()
+    q = ops.mxfp8_quantize(x, colwise=False)
+    layer.forward_quantized(q["row_q"], q["row_s"], ids, prob)
+    with pytest.raises(RuntimeError, match="forward"):
+        back()
