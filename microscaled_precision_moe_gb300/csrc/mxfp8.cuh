@@ -38,15 +38,27 @@ MPM_DEV int mx_exponent(uint32_t bits) {
 
 MPM_DEV float pow2_neg(int e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
 
-// max |x| over bf16 pairs with packed bf16 abs / max (finite inputs), as the
-// 16-bit pattern of the larger magnitude in the low half
+// max of two pairs of bf16 magnitudes, half by half; of a number and a NaN the
+// number
+MPM_DEV uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+// max |x| of the low and of the high halves of bf16 pairs, with packed bf16 abs / max
 template <int N>
-MPM_DEV uint32_t absmax_bf16x2_packed(const uint32_t (&w)[N]) {
+MPM_DEV uint32_t absmax_bf16x2_halves(const uint32_t (&w)[N]) {
   __nv_bfloat162 acc = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
 #pragma unroll
   for (int j = 1; j < N; ++j) acc = __hmax2(acc, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[j])));
-  const uint32_t m = *reinterpret_cast<uint32_t*>(&acc);
-  return max(m & 0xFFFFu, m >> 16);
+  return *reinterpret_cast<uint32_t*>(&acc);
 }
+// the larger half, by its bits: of a number and a NaN (a half that held nothing
+// else) the NaN
+MPM_DEV uint32_t larger_half(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
+// max |x| over bf16 pairs, as the 16-bit pattern of the larger magnitude in the
+// low half
+template <int N>
+MPM_DEV uint32_t absmax_bf16x2_packed(const uint32_t (&w)[N]) { return larger_half(absmax_bf16x2_halves(w)); }
 
 }  // namespace mpm

@@ -305,10 +305,22 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) add_
       if (p.h && live) store_columns<VEC, OFF>(oh, p.h + row * p.ldh, k, p.K);
       if (p.y && live) store_columns<VEC, OFF>(o, p.y + row * p.ldy, k, p.K);
       if (OFF || !p.q) continue;
-      // K % 32 == 0: a block of 32 lies in 32 / VEC neighbouring lanes
-      uint32_t m = VEC == 8 ? absmax_bf16x2_packed(o.w) : o.w[0] & 0x7FFFu;
+      // K % 32 == 0: a block of 32 lies in 32 / VEC neighbouring lanes.  The
+      // quantiser's maximum, also of NaN: over the even columns and over the odd
+      // ones, where a number passes over a NaN, then of the two by their bits.
+      uint32_t m;
+      if constexpr (VEC == 8) {
+        m = absmax_bf16x2_halves(o.w);
 #pragma unroll
-      for (int d = 16 / VEC; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        for (int d = 2; d > 0; d >>= 1) m = max_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        m = larger_half(m);
+      } else {
+        constexpr uint32_t kEven = 0x55555555u;
+        m = o.w[0] & 0x7FFFu;
+        const uint32_t nan = __ballot_sync(0xFFFFFFFFu, m > 0x7F80u);
+        m = __reduce_max_sync(0xFFFFFFFFu, m > 0x7F80u ? 0u : m);
+        if ((nan & kEven) == kEven || (nan & ~kEven) == ~kEven) m = 0x7FFFu;
+      }
       const int e = mx_exponent(m << 16);
       if (!live) continue;
       const uint64_t sc = f32x2_splat(pow2_neg(e));

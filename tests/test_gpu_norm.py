@@ -306,3 +306,32 @@ def test_offsets_past_32_bits():
     dx, _ = ops.add_rmsnorm_backward(x, x, o["rstd"], w)
     dref, _ = ops.add_rmsnorm_backward(tail, tail, ref["rstd"], w)
     assert torch.equal(dx[-130:], dref)
+
+
+@pytest.mark.parametrize("pad", [0, 5])
+@pytest.mark.parametrize("f32", [True, False])
+def test_the_quantisers_bytes_of_nan_and_infinities(pad, f32):
+    """The 8-bit copy is the quantiser's whatever the rows hold: one infinity
+    (rstd 0: a NaN among zeros), runs of them, whole blocks, NaN weights."""
+    ops = _ops()
+    inf, nan = float("inf"), float("nan")
+    x, w = _rows(70, 12, 256, pad), _weight(71, 256, f32)
+    x[1, 5] = inf
+    x[2, 8:16] = inf
+    x[3, 32:64] = inf
+    x[4, 64:96:2] = inf
+    x[5, 65:96:2] = -inf
+    x[6, 100] = nan
+    x[7, 0:32:2] = inf
+    x[8, 3], x[8, 4] = inf, -inf
+    for clear in (False, True):
+        if clear:                                      # NaN weights in one column, a run, and a whole block
+            w = w.clone()
+            w[7] = w[40:48] = w[128:160] = w[161:192:2] = nan
+            w[200] = inf
+        o = ops.add_rmsnorm(x, w, quantize=True)
+        ref = ops.mxfp8_quantize(o["y"], colwise=False)
+        assert_bytes_equal(u8(o["row_q"]), u8(ref["row_q"]), "codes")
+        assert_bytes_equal(u8(o["row_s"]), u8(ref["row_s"]), "tiled scales")
+        alone = ops.add_rmsnorm(x, w, want_y=False, quantize=True)
+        assert torch.equal(alone["row_q"], o["row_q"]) and torch.equal(alone["row_s"], o["row_s"])
