@@ -10,6 +10,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -111,8 +112,9 @@ int weight_type(const Tensor& w, int64_t K) {
     fail(PyExc_ValueError, "weight: expected a contiguous [%lld], got shape %s", (long long)K, shape_of(w).c_str());
   return w.scalar_type() == ScalarType::Float ? MPM_DTYPE_F32 : MPM_DTYPE_BF16;
 }
-// all given tensors on the first one's CUDA device
-void need_cuda(std::initializer_list<const Tensor*> ts) {
+// all given tensors on the first one's CUDA device, which is the current one while
+// the result lives: the library launches on the current device
+[[nodiscard]] c10::cuda::CUDAGuard need_cuda(std::initializer_list<const Tensor*> ts) {
   c10::DeviceIndex dev = -1;
   for (const Tensor* t : ts) {
     if (!t) continue;
@@ -120,6 +122,7 @@ void need_cuda(std::initializer_list<const Tensor*> ts) {
     if (dev < 0) dev = t->device().index();
     if (t->device().index() != dev) fail(PyExc_ValueError, "the tensors are on different CUDA devices");
   }
+  return c10::cuda::CUDAGuard(dev);
 }
 
 Tensor make(at::IntArrayRef size, ScalarType type, const Tensor& like) {
@@ -244,7 +247,7 @@ PyObject* add_rmsnorm(PyObject* const* a, Py_ssize_t n) {
   if (res && (h = item(d.o, kH, "h"))) ldh = matrix(*h, "h", ScalarType::BFloat16, M, K);
   if (quantize && (q = item(d.o, kRowQ, "row_q"))) need_buffer(*q, "row_q", ScalarType::Byte, M * K);
   if (quantize && (s = item(d.o, kRowS, "row_s"))) need_buffer(*s, "row_s", ScalarType::Byte, sb);
-  need_cuda({&x, &w, res, y, h, rstd, q, s});
+  const auto device = need_cuda({&x, &w, res, y, h, rstd, q, s});
   Tensor ny, nh, nr, nq, ns;
   Outputs made(x);
   if (want_y && !y) { made.add(ny, {M, K}, ScalarType::BFloat16); y = &ny; }
@@ -293,7 +296,7 @@ PyObject* add_rmsnorm_backward(PyObject* const* a, Py_ssize_t n) {
   const size_t wsb = want_dw ? mpm_add_rmsnorm_backward_workspace_bytes(M, K) : 0;
   if (!want_dw) ws = nullptr;
   if (ws) need_buffer(*ws, "ws", ScalarType::Byte, (int64_t)wsb);
-  need_cuda({&dy, &h, &rstd, &w, dy2, dh, dx, dw, ws});
+  const auto device = need_cuda({&dy, &h, &rstd, &w, dy2, dh, dx, dw, ws});
   Tensor nx, nw, nws;
   Outputs made(dy);
   if (!dx) { made.add(nx, {M, K}, bf); dx = &nx; }
@@ -376,7 +379,7 @@ PyObject* moe_route(PyObject* const* a, Py_ssize_t n) {
   const Tensor* ws = tensor(a[8], "ws", true);
   const size_t wsb = mpm_moe_route_workspace_bytes(r.T, r.E);
   if (ws) need_buffer(*ws, "ws", ScalarType::Byte, (int64_t)wsb);
-  need_cuda({r.logits, r.bias, r.mask, ws, t[0], t[1], t[2], t[3], t[4], t[5]});
+  const auto device = need_cuda({r.logits, r.bias, r.mask, ws, t[0], t[1], t[2], t[3], t[4], t[5]});
   if (fresh) {
     Outputs all(*r.logits);
     for (int i = 0; i < 6; ++i) {
@@ -429,7 +432,7 @@ PyObject* moe_route_backward(PyObject* const* a, Py_ssize_t n) {
     out_type = t == ScalarType::Float ? MPM_DTYPE_F32 : MPM_DTYPE_BF16;
     ldd = matrix(*out, "out", t, r.T, r.E);
   }
-  need_cuda({r.logits, &ids, &counts, &nt, dprob, dloss, r.bias, r.mask, out});
+  const auto device = need_cuda({r.logits, &ids, &counts, &nt, dprob, dloss, r.bias, r.mask, out});
   Tensor made;
   if (!out) { made = make({r.T, r.E}, r.logits->scalar_type(), *r.logits); out = &made; }
   check(mpm_moe_route_backward(r.logits->data_ptr(), r.type, r.T, r.E, r.ld, (int)k, r.score, normalize,
@@ -460,7 +463,7 @@ PyObject* moe_combine_dprob(PyObject* const* a, Py_ssize_t n) {
   const int64_t T = prob.size(0), k = prob.size(1);
   need_buffer(inv, "inv_perm", ScalarType::Int, T * k);
   if (out) need_buffer(*out, "out", ScalarType::Float, T * k);
-  need_cuda({&dout, &y, &inv, &prob, out});
+  const auto device = need_cuda({&dout, &y, &inv, &prob, out});
   Tensor made;
   if (!out) { made = make({T, k}, ScalarType::Float, dout); out = &made; }
   check(mpm_moe_combine_dprob(dout.data_ptr(), y.data_ptr(), static_cast<int32_t*>(inv.data_ptr()),
@@ -499,7 +502,7 @@ PyObject* moe_gather_mxfp8(PyObject* const* a, Py_ssize_t n) {
     need_buffer(*dq, "out codes", u8, cap * K);
     need_buffer(*ds, "out scales", u8, sb);
   }
-  need_cuda({&q, &s, &perm, &seg, dq, ds});
+  const auto device = need_cuda({&q, &s, &perm, &seg, dq, ds});
   Tensor nq, ns;
   if (!dq) {
     nq = make({cap, K}, u8, q);
