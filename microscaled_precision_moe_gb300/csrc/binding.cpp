@@ -65,8 +65,7 @@ bool truth(PyObject* o) {
   if (v < 0) throw PyError();
   return v != 0;
 }
-int small_int(PyObject* o, const char* name) {
-  const long long v = integer(o);
+int small_int(long long v, const char* name) {
   if (v < INT32_MIN || v > INT32_MAX) fail(PyExc_ValueError, "%s = %lld does not fit 32 bits", name, v);
   return (int)v;
 }
@@ -359,7 +358,7 @@ struct Router {
 PyObject* moe_route(PyObject* const* a, Py_ssize_t n) {
   need_args(n, 9);
   const Router r(a[0], a[2], a[5], a[6]);
-  const int k = small_int(a[1], "k");
+  const int k = small_int(integer(a[1]), "k");
   const bool normalize = truth(a[3]);
   const double scale = real(a[4]);
   if (k < 1) fail(PyExc_ValueError, "k = %d: at least one expert a token", k);
@@ -413,7 +412,7 @@ PyObject* moe_route_backward(PyObject* const* a, Py_ssize_t n) {
   if (ids.dim() != 2 || ids.size(0) != r.T)
     fail(PyExc_ValueError, "ids: expected [%lld, k], got shape %s", (long long)r.T, shape_of(ids).c_str());
   need_buffer(ids, "ids", ScalarType::Int, 0);
-  const int64_t k = ids.size(1);
+  const int k = small_int(ids.size(1), "k");
   need_buffer(counts, "counts", ScalarType::Int, r.E);
   need_buffer(nt, "n_tokens", ScalarType::Int, 1);
   if (dprob) {
@@ -435,7 +434,7 @@ PyObject* moe_route_backward(PyObject* const* a, Py_ssize_t n) {
   const auto device = need_cuda({r.logits, &ids, &counts, &nt, dprob, dloss, r.bias, r.mask, out});
   Tensor made;
   if (!out) { made = make({r.T, r.E}, r.logits->scalar_type(), *r.logits); out = &made; }
-  check(mpm_moe_route_backward(r.logits->data_ptr(), r.type, r.T, r.E, r.ld, (int)k, r.score, normalize,
+  check(mpm_moe_route_backward(r.logits->data_ptr(), r.type, r.T, r.E, r.ld, k, r.score, normalize,
                                (float)scale, static_cast<float*>(ptr(r.bias)), static_cast<uint8_t*>(ptr(r.mask)),
                                static_cast<int32_t*>(ids.data_ptr()), static_cast<int32_t*>(counts.data_ptr()),
                                static_cast<int32_t*>(nt.data_ptr()), static_cast<float*>(ptr(dprob)),
@@ -460,14 +459,15 @@ PyObject* moe_combine_dprob(PyObject* const* a, Py_ssize_t n) {
   if (dout.dim() != 2 || y.dim() != 2 || prob.dim() != 2 || dout.size(0) != prob.size(0) || y.size(1) != dout.size(1))
     fail(PyExc_ValueError, "dout %s and y_perm %s do not match prob %s", shape_of(dout).c_str(), shape_of(y).c_str(),
          shape_of(prob).c_str());
-  const int64_t T = prob.size(0), k = prob.size(1);
+  const int64_t T = prob.size(0);
+  const int k = small_int(prob.size(1), "k");
   need_buffer(inv, "inv_perm", ScalarType::Int, T * k);
   if (out) need_buffer(*out, "out", ScalarType::Float, T * k);
   const auto device = need_cuda({&dout, &y, &inv, &prob, out});
   Tensor made;
   if (!out) { made = make({T, k}, ScalarType::Float, dout); out = &made; }
   check(mpm_moe_combine_dprob(dout.data_ptr(), y.data_ptr(), static_cast<int32_t*>(inv.data_ptr()),
-                              static_cast<float*>(prob.data_ptr()), T, (int)k, dout.size(1), y.size(0),
+                              static_cast<float*>(prob.data_ptr()), T, k, dout.size(1), y.size(0),
                               static_cast<float*>(out->data_ptr()), stream_of(dout)),
         "mpm_moe_combine_dprob");
   if (a[4] != Py_None) { Py_INCREF(a[4]); return a[4]; }
@@ -483,7 +483,8 @@ PyObject* moe_gather_mxfp8(PyObject* const* a, Py_ssize_t n) {
   const Tensor &q = *tensor(a[0], "q"), &s = *tensor(a[1], "s"), &perm = *tensor(a[2], "perm"),
                &seg = *tensor(a[3], "seg_offsets");
   const int64_t E = integer(a[4]), cap = integer(a[6]);
-  const int k = small_int(a[5], "k");
+  const int k = small_int(integer(a[5]), "k");
+  if (E < 1 || cap < 1) fail(PyExc_ValueError, "E = %lld and cap = %lld: both at least 1", (long long)E, (long long)cap);
   need_buffer(q, "q", u8, 0);
   if (q.dim() != 2) fail(PyExc_ValueError, "q: expected a 2-d tensor, got shape %s", shape_of(q).c_str());
   const int64_t T = q.size(0), K = q.size(1);
@@ -491,7 +492,10 @@ PyObject* moe_gather_mxfp8(PyObject* const* a, Py_ssize_t n) {
     fail(PyExc_ValueError, "q: K = %lld is not a multiple of the 32-value MXFP8 block", (long long)K);
   need_buffer(s, "s", u8, (int64_t)mpm_scale_bytes(T, K / 32));
   need_buffer(perm, "perm", ScalarType::Int, cap);
-  need_buffer(seg, "seg_offsets", ScalarType::Int, E + 1);
+  need_buffer(seg, "seg_offsets", ScalarType::Int, 0);
+  if (E >= seg.numel())
+    fail(PyExc_ValueError, "seg_offsets: holds %lld elements, E = %lld experts need one more than that",
+         (long long)seg.numel(), (long long)E);
   const int64_t sb = (int64_t)mpm_scale_bytes(cap, K / 32);
   const Tensor *dq = nullptr, *ds = nullptr;
   if (a[7] != Py_None) {

@@ -246,3 +246,23 @@ def test_binding_refusals(lib):
         ops.moe_gather_mxfp8(q, s, perm, seg, 4, 2, cap, out=(torch.zeros(cap, 64, dtype=u8), s[:4]))
     with pytest.raises(ValueError, match="CUDA"):
         ops.moe_gather_mxfp8(q, s, perm, seg, 4, 2, cap)
+
+
+def test_sizes_past_their_range_are_refused(lib):
+    """Sizes that would wrap in the checks, or in the library's 32-bit arguments,
+    are refused for what they are."""
+    import torch
+    from microscaled_precision_moe_gb300 import ops
+    bf, i32, u8 = torch.bfloat16, torch.int32, torch.uint8
+    q, s = torch.zeros(4, 32, dtype=u8), torch.zeros(512, dtype=u8)
+    perm, seg = torch.zeros(128, dtype=i32), torch.zeros(5, dtype=i32)
+    for E, cap, what in ((2 ** 63 - 1, 128, "seg_offsets"), (5, 128, "seg_offsets"), (0, 128, "at least 1"),
+                         (-2 ** 63, 128, "at least 1"), (4, 0, "at least 1"), (4, -2 ** 62, "at least 1")):
+        with pytest.raises(ValueError, match=what):
+            ops.moe_gather_mxfp8(q, s, perm, seg, E, 2, cap)
+    none = lambda dtype: torch.zeros(0, 2 ** 32 + 1, dtype=dtype)  # noqa: E731
+    with pytest.raises(ValueError, match="k = 4294967297"):
+        ops.moe_combine_dprob(torch.zeros(0, 64, dtype=bf), torch.zeros(4, 64, dtype=bf), torch.zeros(0, dtype=i32),
+                              none(torch.float32))
+    with pytest.raises(ValueError, match="k = 4294967297"):
+        ops.moe_route_backward(torch.zeros(0, 8), none(i32), torch.zeros(8, dtype=i32), torch.zeros(1, dtype=i32))
