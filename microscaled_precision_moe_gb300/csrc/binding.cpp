@@ -9,7 +9,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -124,53 +124,21 @@ int weight_type(const Tensor& w, int64_t K) {
   return c10::cuda::CUDAGuard(dev);
 }
 
-Tensor make(at::IntArrayRef size, ScalarType type, const Tensor& like) {
-  return at::detail::empty_cuda(size, type, std::nullopt, like.device(), std::nullopt, std::nullopt);
+// A new tensor on the current device, with memory of its own: straight from the
+// caching allocator, in 0.5 us where the generic factory takes 0.8 (outputs that
+// share one allocation are 0.3 each, but a resize of one reaches the others)
+Tensor make(at::IntArrayRef size, ScalarType type) {
+  c10::Allocator* memory = c10::cuda::CUDACachingAllocator::get();
+  int64_t bytes = (int64_t)c10::elementSize(type);
+  for (const int64_t n : size) bytes *= n;
+  auto storage = c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), (size_t)bytes,
+                                                       memory->allocate((size_t)bytes), memory, /*resizable=*/true);
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(std::move(storage), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                      c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(size);
+  return t;
 }
 
-// The outputs that a call makes.  Small ones share one allocation, each from a
-// 256-byte boundary of it on: allocating and freeing one takes 0.9 us on the host,
-// and a small batch's outputs are kept and dropped together.
-class Outputs {
- public:
-  explicit Outputs(const Tensor& like) : like_(like) {}
-  void add(Tensor& t, at::IntArrayRef size, ScalarType type) {
-    Item& i = items_[n_++];
-    i = {&t, {size[0], size.size() > 1 ? size[1] : 1}, size.size(), type, bytes_};
-    bytes_ += (i.size[0] * i.size[1] * (int64_t)c10::elementSize(type) + 255) / 256 * 256;
-  }
-  void make_all() {
-    if (n_ < 2 || bytes_ > kShared) {
-      for (int j = 0; j < n_; ++j) *items_[j].t = make(items_[j].sizes(), items_[j].type, like_);
-      return;
-    }
-    const Tensor base = make({bytes_}, ScalarType::Byte, like_);
-    for (int j = 0; j < n_; ++j) {
-      const Item& i = items_[j];
-      Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()),
-                                                          c10::DispatchKeySet(c10::DispatchKey::CUDA),
-                                                          c10::scalarTypeToTypeMeta(i.type));
-      t.unsafeGetTensorImpl()->set_storage_offset(i.at / (int64_t)c10::elementSize(i.type));
-      t.unsafeGetTensorImpl()->set_sizes_contiguous(i.sizes());
-      *i.t = std::move(t);
-    }
-  }
-
- private:
-  static constexpr int64_t kShared = 1 << 20;
-  struct Item {
-    Tensor* t;
-    int64_t size[2];
-    size_t dims;
-    ScalarType type;
-    int64_t at;
-    at::IntArrayRef sizes() const { return at::IntArrayRef(size, dims); }
-  };
-  const Tensor& like_;
-  Item items_[6];
-  int n_ = 0;
-  int64_t bytes_ = 0;
-};
 void* ptr(const Tensor* t) { return t ? t->data_ptr() : nullptr; }
 cudaStream_t stream_of(const Tensor& t) { return c10::cuda::getCurrentCUDAStream(t.device().index()).stream(); }
 
@@ -248,13 +216,11 @@ PyObject* add_rmsnorm(PyObject* const* a, Py_ssize_t n) {
   if (quantize && (s = item(d.o, kRowS, "row_s"))) need_buffer(*s, "row_s", ScalarType::Byte, sb);
   const auto device = need_cuda({&x, &w, res, y, h, rstd, q, s});
   Tensor ny, nh, nr, nq, ns;
-  Outputs made(x);
-  if (want_y && !y) { made.add(ny, {M, K}, ScalarType::BFloat16); y = &ny; }
-  if (res && !h) { made.add(nh, {M, K}, ScalarType::BFloat16); h = &nh; }
-  if (!rstd) { made.add(nr, {M}, ScalarType::Float); rstd = &nr; }
-  if (quantize && !q) { made.add(nq, {M, K}, ScalarType::Byte); q = &nq; }
-  if (quantize && !s) { made.add(ns, {sb}, ScalarType::Byte); s = &ns; }
-  made.make_all();
+  if (want_y && !y) { ny = make({M, K}, ScalarType::BFloat16); y = &ny; }
+  if (res && !h) { nh = make({M, K}, ScalarType::BFloat16); h = &nh; }
+  if (!rstd) { nr = make({M}, ScalarType::Float); rstd = &nr; }
+  if (quantize && !q) { nq = make({M, K}, ScalarType::Byte); q = &nq; }
+  if (quantize && !s) { ns = make({sb}, ScalarType::Byte); s = &ns; }
   if (y == &ny) put(d.o, kY, ny);
   if (h == &nh) put(d.o, kH, nh);
   if (rstd == &nr) put(d.o, kRstd, nr);
@@ -297,11 +263,9 @@ PyObject* add_rmsnorm_backward(PyObject* const* a, Py_ssize_t n) {
   if (ws) need_buffer(*ws, "ws", ScalarType::Byte, (int64_t)wsb);
   const auto device = need_cuda({&dy, &h, &rstd, &w, dy2, dh, dx, dw, ws});
   Tensor nx, nw, nws;
-  Outputs made(dy);
-  if (!dx) { made.add(nx, {M, K}, bf); dx = &nx; }
-  if (want_dw && !dw) { made.add(nw, {K}, ScalarType::Float); dw = &nw; }
-  made.make_all();
-  if (want_dw && !ws) { nws = make({(int64_t)wsb}, ScalarType::Byte, dy); ws = &nws; }
+  if (!dx) { nx = make({M, K}, bf); dx = &nx; }
+  if (want_dw && !dw) { nw = make({K}, ScalarType::Float); dw = &nw; }
+  if (want_dw && !ws) { nws = make({(int64_t)wsb}, ScalarType::Byte); ws = &nws; }
   check(mpm_add_rmsnorm_backward(dy.data_ptr(), lddy, ptr(dy2), lddy2, h.data_ptr(), ldh,
                                  static_cast<float*>(rstd.data_ptr()), w.data_ptr(), wt, ptr(dh), lddh, M, K,
                                  dx->data_ptr(), lddx, static_cast<float*>(ptr(dw)), ptr(ws), wsb, stream_of(dy)),
@@ -379,18 +343,14 @@ PyObject* moe_route(PyObject* const* a, Py_ssize_t n) {
   const size_t wsb = mpm_moe_route_workspace_bytes(r.T, r.E);
   if (ws) need_buffer(*ws, "ws", ScalarType::Byte, (int64_t)wsb);
   const auto device = need_cuda({r.logits, r.bias, r.mask, ws, t[0], t[1], t[2], t[3], t[4], t[5]});
-  if (fresh) {
-    Outputs all(*r.logits);
-    for (int i = 0; i < 6; ++i) {
-      const int64_t size[2] = {o[i].rows, o[i].cols};
-      all.add(made[i], at::IntArrayRef(size, o[i].cols ? 2 : 1), o[i].type);
-      t[i] = &made[i];
-    }
-    all.make_all();
-    for (int i = 0; i < 6; ++i) put(d.o, o[i].key, made[i]);
+  for (int i = 0; i < 6 && fresh; ++i) {
+    const int64_t size[2] = {o[i].rows, o[i].cols};
+    made[i] = make(at::IntArrayRef(size, o[i].cols ? 2 : 1), o[i].type);
+    t[i] = &made[i];
+    put(d.o, o[i].key, made[i]);
   }
   Tensor nws;
-  if (!ws && wsb) { nws = make({(int64_t)wsb}, ScalarType::Byte, *r.logits); ws = &nws; }
+  if (!ws && wsb) { nws = make({(int64_t)wsb}, ScalarType::Byte); ws = &nws; }
   check(mpm_moe_route(r.logits->data_ptr(), r.type, r.T, r.E, r.ld, k, r.score, normalize, (float)scale,
                       static_cast<float*>(ptr(r.bias)), static_cast<uint8_t*>(ptr(r.mask)),
                       static_cast<int32_t*>(ptr(t[0])), static_cast<float*>(ptr(t[1])),
@@ -433,7 +393,7 @@ PyObject* moe_route_backward(PyObject* const* a, Py_ssize_t n) {
   }
   const auto device = need_cuda({r.logits, &ids, &counts, &nt, dprob, dloss, r.bias, r.mask, out});
   Tensor made;
-  if (!out) { made = make({r.T, r.E}, r.logits->scalar_type(), *r.logits); out = &made; }
+  if (!out) { made = make({r.T, r.E}, r.logits->scalar_type()); out = &made; }
   check(mpm_moe_route_backward(r.logits->data_ptr(), r.type, r.T, r.E, r.ld, k, r.score, normalize,
                                (float)scale, static_cast<float*>(ptr(r.bias)), static_cast<uint8_t*>(ptr(r.mask)),
                                static_cast<int32_t*>(ids.data_ptr()), static_cast<int32_t*>(counts.data_ptr()),
@@ -465,7 +425,7 @@ PyObject* moe_combine_dprob(PyObject* const* a, Py_ssize_t n) {
   if (out) need_buffer(*out, "out", ScalarType::Float, T * k);
   const auto device = need_cuda({&dout, &y, &inv, &prob, out});
   Tensor made;
-  if (!out) { made = make({T, k}, ScalarType::Float, dout); out = &made; }
+  if (!out) { made = make({T, k}, ScalarType::Float); out = &made; }
   check(mpm_moe_combine_dprob(dout.data_ptr(), y.data_ptr(), static_cast<int32_t*>(inv.data_ptr()),
                               static_cast<float*>(prob.data_ptr()), T, k, dout.size(1), y.size(0),
                               static_cast<float*>(out->data_ptr()), stream_of(dout)),
@@ -509,8 +469,8 @@ PyObject* moe_gather_mxfp8(PyObject* const* a, Py_ssize_t n) {
   const auto device = need_cuda({&q, &s, &perm, &seg, dq, ds});
   Tensor nq, ns;
   if (!dq) {
-    nq = make({cap, K}, u8, q);
-    ns = make({sb}, u8, q);
+    nq = make({cap, K}, u8);
+    ns = make({sb}, u8);
     dq = &nq;
     ds = &ns;
   }

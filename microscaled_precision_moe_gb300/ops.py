@@ -395,8 +395,7 @@ def add_rmsnorm(x, weight, residual=None, eps=1e-6, want_y=True, quantize=False,
     (unless want_y is False), h bf16 [M, K] (with a residual), rstd fp32 [M],
     and with ``quantize`` row_q u8 [M, K], row_s (tiled [M, K/32]): the bytes
     mxfp8_quantize(y, colwise=False) gives.  Entries of ``out`` that the call
-    does not make stay as they are.  weight: bf16 or fp32 [K].  New outputs of
-    up to 1 MiB together share one allocation (as do the router's)."""
+    does not make stay as they are.  weight: bf16 or fp32 [K]."""
     return (_native_module or _native()).add_rmsnorm(x, weight, residual, eps, want_y, quantize, out)
 
 

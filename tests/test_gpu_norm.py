@@ -335,3 +335,18 @@ def test_the_quantisers_bytes_of_nan_and_infinities(pad, f32):
         assert_bytes_equal(u8(o["row_s"]), u8(ref["row_s"]), "tiled scales")
         alone = ops.add_rmsnorm(x, w, want_y=False, quantize=True)
         assert torch.equal(alone["row_q"], o["row_q"]) and torch.equal(alone["row_s"], o["row_s"])
+
+
+def test_outputs_own_their_memory():
+    """Growing one output in place leaves the others as they are."""
+    ops = _ops()
+    x, r, w = _rows(66, 3, 96), _rows(67, 3, 96), _weight(68, 96, True)
+    o = ops.add_rmsnorm(x, w, residual=r, quantize=True)
+    o["dx"], o["dw"] = ops.add_rmsnorm_backward(x, o["h"], o["rstd"], w)
+    l = torch.randn(40, 16, device="cuda", generator=torch.Generator(device="cuda").manual_seed(69))
+    for outs in (o, ops.moe_route(l, 2)):
+        want = {n: t.clone() for n, t in outs.items()}
+        for n in list(outs):
+            grown = outs.pop(n)
+            grown.resize_(4096).zero_()
+            assert all(torch.equal(t, want[m]) for m, t in outs.items()), n
