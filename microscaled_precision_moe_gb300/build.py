@@ -2,10 +2,11 @@
 cmake).
 
 Each .cu file compiles to an object in parallel; the objects link into
-``microscaled_precision_moe_gb300/libmpm.so``.  ``csrc/binding.cpp``, which
-marshals torch tensors into some of the library's calls, compiles beside them
-against the headers of the running torch and links into ``_binding.so``.
-Rebuilds only when a source or header is newer than either.
+``microscaled_precision_moe_gb300/libmpm.so``, for which nvcc is enough.
+``csrc/binding.cpp``, which marshals torch tensors into some of the library's
+calls, compiles beside them against the headers of the running torch and links
+into ``_binding.so``; without torch there is none, and where its build fails the
+library is still there.  Rebuilds what a source or header is newer than.
 
     python -m microscaled_precision_moe_gb300.build [--force] [--verbose]
 """
@@ -14,6 +15,7 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -49,11 +51,24 @@ def _headers():
     return sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(ROOT, "include", "*.h")))
 
 
+def _older(target: str, files) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(f) > os.path.getmtime(target) for f in files)
+
+
+def has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
+def library_needs_build() -> bool:
+    return _older(LIB, _sources() + _headers() + [__file__])
+
+
+def binding_needs_build() -> bool:
+    return has_torch() and _older(BINDING, _headers() + [BINDING_SRC, __file__])
+
+
 def needs_build() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return any(os.path.getmtime(f) > t for f in _sources() + _headers() + [BINDING_SRC, __file__])
+    return library_needs_build() or binding_needs_build()
 
 
 def _run(cmd, what: str, verbose: bool = False):
@@ -85,24 +100,33 @@ def _compile_binding(verbose: bool) -> str:
     return obj
 
 
-def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    if not force and not needs_build():
-        return LIB
+def _link_binding(obj: str) -> None:
     from torch.utils.cpp_extension import library_paths
-    os.makedirs(BUILD, exist_ok=True)
-    srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(_compile_binding, verbose)
-        objs = list(ex.map(lambda s: _compile(s, verbose, list(extra)), srcs))
-        binding = binding.result()
-    tmp = LIB + ".tmp"
-    _run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], "link of libmpm.so")
-    os.replace(tmp, LIB)
     tmp = BINDING + ".tmp"
-    _run(["g++", "-shared", "-o", tmp, binding, "-L", PKG, "-l:libmpm.so",
+    _run(["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libmpm.so",
           *[f for p in library_paths() for f in ("-L", p)], "-lc10", "-lc10_cuda", "-ltorch_cpu",
           "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "link of _binding.so")
     os.replace(tmp, BINDING)
+
+
+def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    """Build what is out of date, or everything: the library's path.  An error
+    of the binding is raised after the library is in place."""
+    library = force or library_needs_build()
+    binding = has_torch() and (force or binding_needs_build())
+    if not library and not binding:
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    srcs = _sources() if library else []
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding_obj = ex.submit(_compile_binding, verbose) if binding else None
+        objs = list(ex.map(lambda s: _compile(s, verbose, list(extra)), srcs))
+        if library:
+            tmp = LIB + ".tmp"
+            _run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], "link of libmpm.so")
+            os.replace(tmp, LIB)
+        if binding:
+            _link_binding(binding_obj.result())
     return LIB
 
 
