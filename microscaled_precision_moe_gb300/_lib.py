@@ -122,6 +122,14 @@ def load(path: str = LIB_PATH):
     return lib
 
 
+def binding_abi() -> str:
+    """What _binding.so is compiled for and may only be loaded with: it inlines
+    torch's own tensor layout."""
+    import sys
+    import torch
+    return f"torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
 def check(status: int, what: str = ""):
     if status != MPM_OK:
         raise MpmError(f"{what}: {STATUS_NAMES.get(status, status)}")

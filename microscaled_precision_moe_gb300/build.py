@@ -6,7 +6,8 @@ Each .cu file compiles to an object in parallel; the objects link into
 ``csrc/binding.cpp``, which marshals torch tensors into some of the library's
 calls, compiles beside them against the headers of the running torch and links
 into ``_binding.so``; without torch there is none, and where its build fails the
-library is still there.  Rebuilds what a source or header is newer than.
+library is still there.  Rebuilds what a source or header is newer than, and the
+binding for another torch or Python.
 
     python -m microscaled_precision_moe_gb300.build [--force] [--verbose]
 """
@@ -22,6 +23,8 @@ import subprocess
 import sys
 import sysconfig
 
+from ._lib import binding_abi
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
@@ -29,6 +32,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmpm.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_FOR = os.path.join(BUILD, "binding_for.txt")     # the torch and Python it was built for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -63,8 +67,16 @@ def library_needs_build() -> bool:
     return _older(LIB, _sources() + _headers() + [__file__])
 
 
+def _built_for() -> str:
+    try:
+        with open(BINDING_FOR) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def binding_needs_build() -> bool:
-    return has_torch() and _older(BINDING, _headers() + [BINDING_SRC, __file__])
+    return has_torch() and (_older(BINDING, _headers() + [BINDING_SRC, __file__]) or _built_for() != binding_abi())
 
 
 def needs_build() -> bool:
@@ -93,7 +105,7 @@ def _compile_binding(verbose: bool) -> str:
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     inc = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     obj = os.path.join(BUILD, "binding.cpp.o")
-    _run(["g++", "-O2", "-std=c++17", "-fPIC",
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", f'-DMPM_BINDING_FOR="{binding_abi()}"',
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
           "-I", os.path.join(ROOT, "include"), *[f for p in inc for f in ("-isystem", p)],
           "-c", BINDING_SRC, "-o", obj], f"g++ {BINDING_SRC}", verbose)
@@ -107,6 +119,8 @@ def _link_binding(obj: str) -> None:
           *[f for p in library_paths() for f in ("-L", p)], "-lc10", "-lc10_cuda", "-ltorch_cpu",
           "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "link of _binding.so")
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR, "w") as f:
+        f.write(binding_abi())
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:

@@ -524,5 +524,7 @@ PyMODINIT_FUNC PyInit__binding() {
       {&kProb, "prob"}, {&kCounts, "counts"}, {&kLoad, "load"}, {&kTokens, "n_tokens"}, {&kLoss, "loss"}};
   for (auto& k : keys)
     if (!(*k.key = PyUnicode_InternFromString(k.name))) return nullptr;
-  return PyModule_Create(&module);
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", MPM_BINDING_FOR) < 0) Py_CLEAR(m);
+  return m;
 }

@@ -36,6 +36,9 @@ def _native():
         except ImportError as e:
             raise L.MpmError(f"_binding.so not usable ({e}); build it with "
                              f"`python -m microscaled_precision_moe_gb300.build`") from e
+        if _binding.built_for != L.binding_abi():
+            raise L.MpmError(f"_binding.so is built for {_binding.built_for}, this is {L.binding_abi()}; build it "
+                             f"again with `python -m microscaled_precision_moe_gb300.build`")
         _native_module = _binding
     return _native_module
 

@@ -20,7 +20,8 @@ def made(tmp_path, monkeypatch):
 
     monkeypatch.setattr(B, "_run", run)
     monkeypatch.setattr(B, "nvcc", lambda: "nvcc")
-    for name, path in (("BUILD", "_build"), ("LIB", "libmpm.so"), ("BINDING", "_binding.so")):
+    for name, path in (("BUILD", "_build"), ("LIB", "libmpm.so"), ("BINDING", "_binding.so"),
+                       ("BINDING_FOR", "_build/binding_for.txt")):
         monkeypatch.setattr(B, name, str(tmp_path / path))
     monkeypatch.setattr(B, "PKG", str(tmp_path))
     return ran
@@ -73,3 +74,26 @@ def test_only_what_is_out_of_date(made, tmp_path, monkeypatch):
     monkeypatch.setattr(B, "BINDING_SRC", str(source))
     B.build()
     assert {cmd[0] for _, cmd in made} == {"g++"}
+
+
+def test_another_torch_rebuilds_the_binding(made, monkeypatch):
+    import torch
+    B.build()
+    made.clear()
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    assert B.needs_build()
+    B.build()
+    assert {cmd[0] for _, cmd in made} == {"g++"} and not B.needs_build()
+    assert any("torch 9.9.9" in arg for _, cmd in made for arg in cmd)
+
+
+def test_a_binding_of_another_torch_is_refused(monkeypatch):
+    import torch
+    from microscaled_precision_moe_gb300 import _lib, ops
+    B.build()
+    monkeypatch.setattr(ops, "_native_module", None)
+    assert ops._native().built_for == _lib.binding_abi()
+    monkeypatch.setattr(ops, "_native_module", None)
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    with pytest.raises(_lib.MpmError, match="built for torch .* this is torch 9.9.9"):
+        ops._native()
