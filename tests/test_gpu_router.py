@@ -355,3 +355,34 @@ def test_gather_mxfp8_bad_token_sets_status():
     torch.cuda.synchronize()
     assert ops.get_device_status() == 7
     assert not dq[row].any() and torch.equal(dq[int(inv[8])], q["row_q"][4])
+
+
+@pytest.mark.parametrize("T,H,I,E,k,kw", [(256, 512, 256, 8, 4, {}), (100, 256, 256, 12, 3, {"tile_m": 128}),
+                                          (256, 512, 256, 8, 2, {"fc2": "online"})])
+def test_nvfp4_layer_prob_grad(T, H, I, E, k, kw):
+    """The NVFP4 layer's gradient of the routing weights is that of its own
+    combined rows, and doubling a weight moves the output by that much."""
+    from microscaled_precision_moe_gb300.moe import NVFP4MoE, NVFP4Weights
+    ops = _ops()
+    shape = synth.scaled(synth.MOE_30B, T=T, H=H, I=I, E=E, k=k)
+    ids, prob = (t.cuda() for t in synth.routing(shape))
+    w = NVFP4Weights.quantize(*synth.moe_weights(shape, device="cuda"))
+    x = synth.moe_activations(shape, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(T)
+    dout = torch.randn(T, H, device="cuda", generator=g).to(torch.bfloat16)
+    prob[3, 1] = 0.0
+    layer = NVFP4MoE(T, H, I, E, k, **kw)
+    out = layer.forward(x, ids, prob, w).float().clone()
+    y, inv = layer.y.clone(), layer.seg[2].clone()
+    got = layer.prob_grad(dout, prob)
+    want, mag = R.combine_dprob(np_bf16(dout), np_bf16(y), inv.cpu().numpy(), prob.cpu().numpy())
+    _close(got.cpu().numpy(), want, (H / 32 + 40) * 2.0 ** -24 * mag + 1e-30, "dprob")
+    assert float(got[3, 1]) == 0.0
+    # D and so its scales double with the weight, exactly; out is rounded to bf16 twice
+    twice = prob.clone()
+    twice[:, 0] *= 2
+    moved = layer.forward(x, ids, twice, w).float() - out
+    change = (moved.double() * dout.double()).sum(1)
+    size = (out.abs().double() + moved.abs().double()) * dout.double().abs()
+    assert ((change - (got[:, 0] * prob[:, 0]).double()).abs() <= 2 * BF16 * size.sum(1)).all()
+    assert ops.get_device_status() == 0
