@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(ring_most_threads(C, TWO || RES || OFF)) add_r
       const long long ahead = row + (long long)(S - 1) * step;
       if (ahead < p.M) issue(ahead, cur.s == 0 ? S - 1 : cur.s - 1);
     }
-    const float f = -__fmul_rn(__fmul_rn(rstd, rstd), __fmul_rn(c, rk));
+    const float f = -__fmul_rn(rstd, __fmul_rn(rstd, __fmul_rn(c, rk)));      // rstd^2 may leave fp32
     const uint64_t f2 = f32x2(f, f);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormTeams : kNormMaxThreads) rmsn
     }
   }
   row_sums<WARP, 1>(c, sh);
-  const float f = -__fmul_rn(__fmul_rn(rstd, rstd), __fdiv_rn(c[0], (float)p.K));
+  const float f = -__fmul_rn(rstd, __fmul_rn(rstd, __fdiv_rn(c[0], (float)p.K)));      // rstd^2 may leave fp32
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     const int k = (i * nt + t) * VEC, iw = WIDE ? 0 : i;

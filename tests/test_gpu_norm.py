@@ -350,3 +350,19 @@ def test_outputs_own_their_memory():
             grown = outs.pop(n)
             grown.resize_(4096).zero_()
             assert all(torch.equal(t, want[m]) for m, t in outs.items()), n
+
+
+@pytest.mark.parametrize("M,K", [(40, 64), (40, 1024), (40, 1001), (9, 9000)])
+def test_gradient_where_the_square_of_rstd_leaves_fp32(M, K):
+    """A zero row under an eps of 1e-39 (rstd 3e19), and rows near 1e17."""
+    ops = _ops()
+    h, dy, w = _rows(80, M, K), _rows(81, M, K, std=1e-2), _weight(82, K, True)
+    h[3] = 0
+    h[5] = (h[5].float() * 1e17).to(torch.bfloat16)
+    h[6] = (h[6].float() * 1e-20).to(torch.bfloat16)
+    rstd = ops.add_rmsnorm(h, w, eps=1e-39)["rstd"]
+    dx, dw = ops.add_rmsnorm_backward(dy, h, rstd, w)
+    rx, rw, mx, mw = N.add_rmsnorm_backward(np_bf16(dy), np_bf16(h), rstd.cpu().numpy(), w.cpu().numpy())
+    _within(np_bf16(dx), rx, BF16 * np.abs(rx) + DX * mx + 1e-38, "dx")
+    _within(dw.cpu().numpy(), rw, DW * mw + 1e-38, "dw")
+    assert float(rstd[3]) > 1e19 and torch.isfinite(dx).all()
