@@ -69,8 +69,13 @@ class MoEBlock:
         self.one_segment = torch.tensor([0, T], dtype=torch.int32, device=dev)
 
     def set_weights(self, router_weight=None, w1=None, w2=None):
-        """New router and / or expert weights (quantised here)."""
+        """New router and / or expert weights (quantised here; w1 and w2
+        together)."""
+        if (w1 is None) != (w2 is None):
+            raise ValueError("w1 and w2 are set together")
         if router_weight is not None:
+            if tuple(router_weight.shape) != (self.E, self.H):
+                raise ValueError(f"router_weight: expected {(self.E, self.H)}, got {tuple(router_weight.shape)}")
             self.wr[:self.E] = router_weight
         if w1 is not None:
             self.experts.quantize_weights(w1, w2)

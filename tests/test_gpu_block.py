@@ -183,3 +183,14 @@ def test_expert_layer_backward_after_a_quantised_forward(mode):
     layer.forward_quantized(q["row_q"], q["row_s"], ids, prob)
     with pytest.raises(RuntimeError, match="forward"):
         back()
+
+
+def test_set_weights_takes_both_experts_weights_and_the_routers_shape():
+    b, x, res, wr, wn, w1, w2 = _block(T=128, H=256, I=256, E=8, k=2)
+    out = b.forward(x, res)[0].clone()
+    for kw in (dict(w2=w2), dict(w1=w1), dict(router_weight=wr[:1]), dict(router_weight=wr[0]),
+               dict(router_weight=wr.t())):
+        with pytest.raises(ValueError, match="router_weight|together"):
+            b.set_weights(**kw)
+    b.set_weights(w1=w1, w2=2 * w2)
+    assert torch.equal(b.forward(x, res)[0], 2 * out)
