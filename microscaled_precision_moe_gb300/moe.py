@@ -417,6 +417,8 @@ class MXFP8MoE:
         it is refused): the same out as forward gives for the bf16 rows they
         were quantised from."""
         T, H, I, E, k, cap = self.T, self.H, self.I, self.E, self.k, self.cap
+        if tuple(x_q.shape) != (T, H):
+            raise ValueError(f"x_q: expected {(T, H)}, got {tuple(x_q.shape)}")
         seg, perm, inv, rp = self.seg
         self._kept = False
         ops.moe_build_segments(topk_ids, topk_prob, E, out=self.seg, ws=self.seg_ws,

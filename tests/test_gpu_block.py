@@ -194,3 +194,14 @@ def test_set_weights_takes_both_experts_weights_and_the_routers_shape():
             b.set_weights(**kw)
     b.set_weights(w1=w1, w2=2 * w2)
     assert torch.equal(b.forward(x, res)[0], 2 * out)
+
+
+def test_quantised_rows_of_another_shape_are_refused():
+    from microscaled_precision_moe_gb300 import ops
+    b, x, *_ = _block(T=128, H=512, I=256, E=8, k=2)
+    ids = torch.arange(256, dtype=torch.int32, device="cuda").view(128, 2) % 8
+    prob = torch.full((128, 2), 0.5, device="cuda")
+    for rows in (x[:, :256].contiguous(), x[:64]):
+        q = ops.mxfp8_quantize(rows, colwise=False)
+        with pytest.raises(ValueError, match="x_q"):
+            b.experts.forward_quantized(q["row_q"], q["row_s"], ids, prob)
