@@ -56,7 +56,7 @@ constexpr float kLog2e = 1.44269504088896341f;
 // kVanishingScale take the place of the approximate ones: the factor leaves their
 // ratios as they are.  Elsewhere a flushed score is less than 2^-106 of the sum.
 constexpr float kVanishing = 9.5367431640625e-7f;           // 2^-20
-constexpr float kVanishingScale = 1.8446744073709552e19f;   // 2^64
+constexpr float kVanishingScale = 1.099511627776e12f;        // 2^40
 constexpr float kLeastLogit = -88.72283f;                   // below it expf(-l) is infinite: the score is 0
 
 // warps of a block: as many as its registers allow
@@ -636,10 +636,11 @@ __global__ void __launch_bounds__(1024) route_finish_kernel(const RouteArgs a, i
 // cancellation at either end.  The choices' scores are recomputed from their
 // logits (one lane each), and their ds join the others through shared memory.
 // The sigmoid's dl is a product of s, as small as fp32 goes, and 1 / S or 1 / W, as
-// large: s and s (1 - s) are held times 2^64, which keeps each factor in fp32's range
-// and cancels in s / S and s / W (a branch for vanishing sums instead: 23.7 against
-// 24.3 us at 32768 x 256, 21.5 and 21.2 with bf16 logits).  exp(-|l|), which may be a
-// subnormal, is the square of the hardware's exp(-|l| / 2), which is not.
+// large: s and s (1 - s) are held times 2^40, which keeps each factor in fp32's range
+// (for gradients up to 10^12 where the sums are smallest, down to 10^-33 where they
+// are not) and cancels in s / S and s / W.  A branch for vanishing sums instead: 23.7
+// against 24.6 us at 32768 x 256, 21.5 and 21.2 with bf16 logits.  exp(-|l|), which
+// may be a subnormal, is the square of the hardware's exp(-|l| / 2), which is not.
 MPM_DEV float sigmoid_parts(float l, float& slope) {
   const float e = exp2_ftz(__fmul_rn(-fabsf(l), 0.5f * kLog2e));
   const float z = l >= kLeastLogit ? __fmul_rn(e, e) : 0.0f;
@@ -737,7 +738,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_blocks(NE, SIG)) route_bwd
           w[c] = SIG ? sigmoid_parts(cl[c], slope) : __fmul_rn(exp_neg(__fsub_rn(cl[c], m)), r);
         const float wsum = warp_sum(__fadd_rn(w[0], w[1]));
         const float rw = wsum > 0.0f ? __fdiv_rn(1.0f, wsum) : 1.0f;
-        const float dot = __fmul_rn(warp_sum(__fmaf_rn(w[0], d[0], __fmul_rn(w[1], d[1]))), rw);
+        const float dot = warp_sum(__fmaf_rn(__fmul_rn(w[0], rw), d[0], __fmul_rn(__fmul_rn(w[1], rw), d[1])));
 #pragma unroll
         for (int c = 0; c < 2; ++c) d[c] = __fmul_rn(__fsub_rn(d[c], dot), rw);
       } else if (SIG) {

@@ -177,3 +177,17 @@ def test_extreme_rows_have_finite_gradients():
                                    dloss=torch.full((1,), 30.0, device="cuda"))
         assert torch.isfinite(o["prob"]).all() and torch.isfinite(o["loss"]).all() and torch.isfinite(d).all()
         assert not d[2].any() and not o["prob"][2].any()
+
+
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("scale", [1e-3, 1e6])
+def test_gradient_of_swayed_choices_among_large_scores(normalize, scale):
+    """A bias that picks vanishing scores among ordinary ones: the gradient that
+    the others get through the load is as small, and the weights' gradient times
+    a large scale stays finite."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    l = torch.randn(200, 96, device="cuda", generator=g) * 3
+    l[:, :8] = -40.0 - 45.0 * torch.rand(200, 8, device="cuda", generator=g)
+    b = torch.zeros(96, device="cuda")
+    b[:8] = 5.0 + torch.arange(8, device="cuda")
+    _gradient(l, 3, normalize, scale, b, None, 1e3, 5)
