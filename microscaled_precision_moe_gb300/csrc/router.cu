@@ -24,8 +24,9 @@
 //      ballots, the keys through shared memory), and each lane counts the keys
 //      above its own, its place among the choices; only where places collide are
 //      equal keys told apart by expert.
-// With k > 32, more than 32 such keys (masses of ties) or fewer than k lanes with
-// an expert in reach, the warp takes k maxima one after the other instead.
+// With k > 32, more than 32 such keys (masses of ties), fewer than k lanes with an
+// expert in reach or sigmoid scores that all vanish, the warp takes k maxima one after
+// the other instead.
 // Softmax scores use the hardware exponential (a few ulp).  A sigmoid choice
 // depends on the last bit of 1 / (1 + expf(-l)), with the IEEE reciprocal, and of
 // its sum with the bias: tau is found among keys by the hardware functions and
