@@ -15,8 +15,9 @@ import torch
 
 own = False
 
-#: logits at or below this (-inf and the types' lowest values) mark a token out of reach
-LOWEST = -2.0 ** 100
+#: logits at or below bf16's lowest finite value mark a token out of reach
+LOWEST = -3.3895313892515355e38
+FLT_MAX = 3.4028234663852886e38
 FLOOR = 2.0 ** -116
 
 
@@ -245,14 +246,14 @@ def _scaled(s):
     """(scaled logits with -inf for tokens out of reach, that mask, scored rows)"""
     l = s["logits"].float()
     live = l > LOWEST
-    z = torch.where(live, l / s["temperature"], torch.full_like(l, -math.inf))
+    z = torch.where(live, (l.clamp(max=FLT_MAX) / s["temperature"]).clamp(max=FLT_MAX), torch.full_like(l, -math.inf))
     return z, live, s["targets"] >= 0
 
 
 def _plain_logprob(s):
     z, live, scored = _scaled(s)
     m, first = z.max(1, keepdim=True)
-    m = m.clamp(min=2.0 * LOWEST)
+    m = m.clamp(min=-FLT_MAX)
     some = live.any(1)
     # the sum without one of its largest terms, which is 1: where that token is nearly certain the others are what counts
     e = torch.exp(z - m).scatter(1, first, 0.0)
@@ -333,7 +334,8 @@ def exact(case, seed):
         return _exact_few(s)
     l = s["logits"].double()
     out = ~(l > LOWEST)
-    x = (l / s["temperature"]).masked_fill(out, -math.inf)
+    x = torch.minimum(l, torch.full((), FLT_MAX, dtype=torch.float64, device="cuda")) / s["temperature"]
+    x = torch.minimum(x, torch.full((), FLT_MAX, dtype=torch.float64, device="cuda")).masked_fill(out, -math.inf)
     t = s["targets"]
     rows = torch.nonzero(t >= 0)[:, 0]
     T = t.numel()
