@@ -272,7 +272,8 @@ MPM_DEV Stats block_stats(const Shared::Half& h, const Row<F32>& r, int q0, int 
   const float own = lane < NW ? h.own[lane] : 0.0f, other = lane < NW ? h.other[lane] : 0.0f;
   const int ow = __ffs(__ballot_sync(0xffffffffu, lane < NW && m == M)) - 1;
   const float s_all = warp_sum((other + own) * sc);
-  const float w = warp_sum(lane < NW ? sc * fmaf(d, other + own, h.w[lane]) : 0.0f);
+  // a part of weight 0 (nothing in reach, among others) adds 0: its distance times its number of elements may overflow
+  const float w = warp_sum(sc > 0.0f ? sc * fmaf(d, other + own, h.w[lane]) : 0.0f);
   float rest = s_all - 1.0f;
   if (s_all < 1.5f && M > LOW) {
     const int owner = ow * 32 + h.lane[ow];
@@ -429,7 +430,10 @@ MPM_DEV void write_row(const LogprobFwd& p, long long row, const Stats& st, floa
   if (lane == 0) {
     p.lse[row] = some ? fmaf(st.m, p.inv_t, lr) : -INFINITY;
     if (p.logp) p.logp[row] = some ? (zt <= LOW ? (lr == lr ? -INFINITY : lr) : fmaf(zt - st.m, p.inv_t, -lr)) : -INFINITY;
-    if (p.entropy) p.entropy[row] = some ? fmaxf(0.0f, lr - kLn2 * st.w / (1.0f + st.rest)) + 0.0f * lr : 0.0f;
+    if (p.entropy) {
+      const float h = lr - kLn2 * st.w / (1.0f + st.rest);
+      p.entropy[row] = some ? (h < 0.0f ? 0.0f : h) : 0.0f;       // a NaN passes
+    }
   }
   if (lane < p.top) {
     p.top_ids[row * p.top + lane] = key ? (int)(0xFFFFFFFFu - (uint32_t)key) : -1;
@@ -600,7 +604,7 @@ __global__ void __launch_bounds__(NT + 64, 2) token_logprob_kernel(const Logprob
           const int first = __ffs(__ballot_sync(0xffffffffu, lane < cs && o.x == M)) - 1;
           const float d = (o.x - M) * c, sc = lane < cs ? ex2(d) : 0.0f;
           const float rest = warp_sum(sc * (lane == first ? o.y : 1.0f + o.y));
-          const float w_all = warp_sum(sc * fmaf(d, 1.0f + o.y, o.z));
+          const float w_all = warp_sum(sc > 0.0f ? sc * fmaf(d, 1.0f + o.y, o.z) : 0.0f);
           st = Stats{M, rest, w_all};
           if (TOP) {
             // the blocks' alternatives, each in descending order
@@ -731,7 +735,7 @@ __global__ void __launch_bounds__(NT + 64, 2) token_logprob_kernel(const Logprob
         const float mw = warp_max(bm);
         if (mw > m) {
           // 2^((z - m) c) -> 2^((z - mw) c): s 2^-D and (w - D s) 2^-D
-          const float D = (mw - m) * c, f = ex2(-D);
+          const float D = fminf((mw - m) * c, 0x1p90f), f = ex2(-D);       // f is 0 there, and D s finite
           const uint64_t f2 = f32x2(f, f), nD2 = f32x2(-D, -D);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {

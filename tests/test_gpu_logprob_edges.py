@@ -1,0 +1,49 @@
+"""Token log probabilities and their gradient at the ends of what they take: masks of most of a large vocabulary at
+the lowest temperature, against values known in closed form.
+
+u = 2^-24; an exponential is off by 4 u, a logarithm by 4 u of its result at most.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests.gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+
+UNIT = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def _ops():
+    from microscaled_precision_moe_gb300 import ops
+    return ops
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T,V,temperature", [(1, 2_000_000, 1e-3), (100, 400_000, 1e-3), (160, 1_600_000, 1e-3), (400, 7000, 1e-3),
+                                             (400, 900, 1e-3), (1, 1 << 20, 0.0025)])
+def test_entropy_beside_a_mask_of_most_of_the_row(bf16, T, V, temperature):
+    """Two equal tokens in reach among masked ones, which a part of the row (a block, a warp) holds alone: ln 2.
+    Terms that are 0 add 0, however many and however far they are."""
+    l = torch.full((T, V), -torch.inf, dtype=torch.bfloat16 if bf16 else torch.float32, device="cuda")
+    l[:, :2] = 1.5
+    t = torch.zeros(T, dtype=torch.int64, device="cuda")
+    o = _ops().token_logprob(l, t, temperature=temperature, entropy=True, top=3)
+    tol = 8 * UNIT
+    assert (o["entropy"] - math.log(2)).abs().max() <= tol
+    assert (o["logp"] + math.log(2)).abs().max() <= tol
+    assert (o["top_ids"] == torch.tensor([0, 1, -1], device="cuda")).all()
+    # and with the tokens in reach at the row's end
+    l[:, :2] = torch.finfo(l.dtype).min
+    l[:, V - 2:] = 1.5
+    t += V - 1
+    o = _ops().token_logprob(l, t, temperature=temperature, entropy=True)
+    assert (o["entropy"] - math.log(2)).abs().max() <= tol and (o["logp"] + math.log(2)).abs().max() <= tol
+    assert _ops().get_device_status() == 0
