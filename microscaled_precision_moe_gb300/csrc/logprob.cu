@@ -1141,7 +1141,7 @@ __global__ void __launch_bounds__(NT, PARTS ? 3 : 4) token_logprob_backward_kern
           for (int j = 0; j < VE; ++j)
             if (x.t == e + j) {
               const float z = element<F32>(v[u], j), lp = __fsub_rn(__fmul_rn(z, p.inv_t), x.lse);
-              d[j] = z <= LOW ? 0.0f : -p.inv_t * (x.gl * expm1f(lp) + x.gh * expf(lp) * (lp + x.H));
+              d[j] = z <= LOW && x.lse == x.lse ? 0.0f : -p.inv_t * (x.gl * expm1f(lp) + x.gh * expf(lp) * (lp + x.H));
             }
         }
       }

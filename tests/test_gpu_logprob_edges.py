@@ -47,3 +47,17 @@ def test_entropy_beside_a_mask_of_most_of_the_row(bf16, T, V, temperature):
     o = _ops().token_logprob(l, t, temperature=temperature, entropy=True)
     assert (o["entropy"] - math.log(2)).abs().max() <= tol and (o["logp"] + math.log(2)).abs().max() <= tol
     assert _ops().get_device_status() == 0
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T,V", [(4, 300), (4, 40000), (2000, 300)])
+def test_gradient_of_a_row_with_nan_and_a_masked_target(bf16, T, V):
+    l = torch.randn(T, V, device="cuda").to(torch.bfloat16 if bf16 else torch.float32)
+    t = torch.full((T,), 3, device="cuda")
+    l[1:3, 3] = -torch.inf
+    l[1, 5], l[2, 6] = torch.nan, torch.inf
+    o = _ops().token_logprob(l, t, entropy=True)
+    one = torch.ones(T, device="cuda")
+    for a, b in ((one, None), (None, one), (one, one)):
+        got = _ops().token_logprob_backward(l, t, o["lse"], dlogp=a, entropy=o["entropy"] if b is not None else None, dentropy=b)
+        assert got[1:3].isnan().all() and got[0].isfinite().all() and got[3:].isfinite().all()
