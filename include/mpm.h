@@ -590,7 +590,8 @@ mpm_status mpm_moe_few_tokens(const mpm_moe_few_tokens_desc* desc, cudaStream_t 
  * probability 0, never an alternative, logp -inf as a target.  A row with
  * nothing in reach gives lse and logp -inf and entropy 0; alternatives that do
  * not exist are (-1, -inf).  A NaN, +inf or a logit above 2^100 makes lse, logp,
- * entropy and top_logp of its row NaN.
+ * entropy and all of top_logp of its row NaN; beside a NaN, top_ids are some tokens of
+ * the row, or -1, not necessarily the largest.
  * Sums and statistics are fp32; the sum is kept without its largest term, so
  * that logp and the entropy of nearly certain tokens keep their relative
  * precision.

@@ -437,7 +437,7 @@ MPM_DEV void write_row(const LogprobFwd& p, long long row, const Stats& st, floa
   }
   if (lane < p.top) {
     p.top_ids[row * p.top + lane] = key ? (int)(0xFFFFFFFFu - (uint32_t)key) : -1;
-    p.top_logp[row * p.top + lane] = key ? fmaf(key_value(key) - st.m, p.inv_t, -lr) : -INFINITY;
+    p.top_logp[row * p.top + lane] = key ? fmaf(key_value(key) - st.m, p.inv_t, -lr) : lr == lr ? -INFINITY : lr;
   }
 }
 

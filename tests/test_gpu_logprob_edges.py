@@ -61,3 +61,23 @@ def test_gradient_of_a_row_with_nan_and_a_masked_target(bf16, T, V):
     for a, b in ((one, None), (None, one), (one, one)):
         got = _ops().token_logprob_backward(l, t, o["lse"], dlogp=a, entropy=o["entropy"] if b is not None else None, dentropy=b)
         assert got[1:3].isnan().all() and got[0].isfinite().all() and got[3:].isfinite().all()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T,V", [(6, 300), (6, 50001), (400, 300), (400, 4000), (400, 7000), (400, 15000)])
+def test_alternatives_of_a_row_with_nan(bf16, T, V):
+    """Every log probability of such a row is NaN, those of places that no token takes among them."""
+    l = torch.randn(6, V, device="cuda").to(torch.bfloat16 if bf16 else torch.float32)
+    l[1] = torch.nan
+    l[2] = -torch.inf
+    l[2, 7] = torch.nan
+    l[3, 1::2] = torch.nan
+    l[3, ::2] = -torch.inf
+    l[4, 5] = torch.inf
+    l[5, V - 1] = torch.nan
+    l = l.repeat((T + 5) // 6, 1)[:T].contiguous()
+    o = _ops().token_logprob(l, None, top=4)
+    row = torch.arange(T, device="cuda") % 6
+    assert (o["lse"].isnan() == (row > 0)).all()
+    assert (o["top_logp"].isnan() == (row > 0)[:, None]).all()
+    assert ((o["top_ids"] >= -1) & (o["top_ids"] < V)).all()
