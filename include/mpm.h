@@ -586,11 +586,11 @@ mpm_status mpm_moe_few_tokens(const mpm_moe_few_tokens_desc* desc, cudaStream_t 
  * entropy 0, alternatives (-1, -inf).  A target at or past V sets
  * MPM_ERR_DEVICE_BOUNDS and counts as not scored.  Without targets every row is
  * scored and logp_dev is NULL.
- * Logits at or below -2^100 (-inf, the types' lowest values) are out of reach:
+ * Logits at or below bf16's lowest finite value (-inf, the types' lowest values) are out of reach:
  * probability 0, never an alternative, logp -inf as a target.  A row with
  * nothing in reach gives lse and logp -inf and entropy 0; alternatives that do
- * not exist are (-1, -inf).  A NaN, +inf or a logit above 2^100 makes lse, logp,
- * entropy and all of top_logp of its row NaN; beside a NaN, top_ids are some tokens of
+ * not exist are (-1, -inf).  A NaN, +inf or a largest quotient by the temperature
+ * above 2^128 (1 - 2^-9) in magnitude makes lse, logp, entropy and all of top_logp of its row NaN; beside a NaN, top_ids are some tokens of
  * the row, or -1, not necessarily the largest.
  * Sums and statistics are fp32; the sum is kept without its largest term, so
  * that logp and the entropy of nearly certain tokens keep their relative

@@ -4,13 +4,15 @@
 //
 // With z = logits / temperature, M the largest z of a row and
 //   rest = sum over all tokens but one with z = M of e^(z - M)
-//   w    = sum of e^(z - M) (z - M)
+//   w    = sum of e^(z - M) (l - L), l the logits and L their largest
 // a row's results are
 //   lse = M + log1p(rest),  logp_t = (z_t - M) - log1p(rest),
-//   H   = log1p(rest) - w / (1 + rest).
+//   H   = log1p(rest) - w / temperature / (1 + rest).
 // The sum is kept without its largest term, which is 1: where a token is
 // nearly certain (most positions of a rollout) log p is as small as rest, and
-// 1 + rest in fp32 would lose it.
+// 1 + rest in fp32 would lose it.  w is of differences that are finite wherever they weigh anything (masked tokens
+// stand at the lowest value, and their quotient by a temperature may overflow): above 2^100 the next logit is more than
+// 2^76 away, only tokens equal to L weigh anything and w is 0.
 //
 // Forward: one pass over the logits, bound by reading them (8192 x 32768 bf16 81 us, 0.99 of a plain copy's rate; 64 x
 // 131072 with 8 alternatives 9.6 us and 1 x 131072 with 20 7.6, latency).  Batches of 32 KB come by bulk copies through a
@@ -41,8 +43,10 @@ constexpr int FEW = 128;             // candidates that the closing warp ranks b
 constexpr int SHORT = 64;            // longer lists are first reduced by the row's own bound (k = 20 at 2047 x 50001: 65.7 -> 61.7 us)
 constexpr int MAX_CLUSTER = 8;
 constexpr int QUEUE = 4;              // rows handed on ahead
-constexpr float LOW = -0x1p100f;     // logits at or below it are out of reach
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float LOW = -0x1.FEp127f;  // bf16's lowest finite value: logits at or below it are out of reach
+constexpr float FAR = -0x1p100f;     // no probability is left there, unless all logits are as low (lse is -2^90 or less then)
+constexpr float MOST = 0x1.FFp127f;  // a row whose largest logit's quotient by the temperature is larger is NaN
+constexpr float kLog2e = 1.4426950408889634f;
 
 MPM_DEV float ex2(float t) {
   float r;
@@ -142,17 +146,17 @@ MPM_DEV float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// the words of a vector raised to LOW (a NaN stays), and their largest
-template <bool F32>
+// the words of a vector raised to LOW (a NaN stays), or to FAR, and their largest
+template <bool F32, bool TO_FAR = false>
 MPM_DEV float clamp_max(uint4& v) {
   if (F32) {
     float f[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = max_nan(f[i], LOW);
+    for (int i = 0; i < 4; ++i) f[i] = max_nan(f[i], TO_FAR ? FAR : LOW);
     v = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
     return fmaxf(max3(f[0], f[1], f[2]), f[3]);
   }
-  const uint32_t low2 = 0xF180F180u;           // -2^100 twice
+  const uint32_t low2 = TO_FAR ? 0xF180F180u : 0xFF7FFF7Fu;           // the bound twice
   v = make_uint4(max_nan2(v.x, low2), max_nan2(v.y, low2), max_nan2(v.z, low2), max_nan2(v.w, low2));
   const uint32_t a = max_nan2(max_nan2(v.x, v.y), max_nan2(v.z, v.w));
   return fmaxf(bf16lo(a), bf16hi(a));
@@ -215,7 +219,7 @@ MPM_DEV float logit(const void* logits, long long at) {
              : __uint_as_float((uint32_t)static_cast<const uint16_t*>(logits)[at] << 16);
 }
 
-struct Stats { float m, rest, w; };            // of a row or of a part of it, w in units of log2
+struct Stats { float m, rest, w; };            // of a row or of a part of it
 
 struct Shared {
   // of the row (by its parity among the block's) that the closing warp works on while the next one is read
@@ -267,8 +271,8 @@ template <bool F32>
 MPM_DEV Stats block_stats(const Shared::Half& h, const Row<F32>& r, int q0, int q1, float c, int lane) {
   const float m = lane < NW ? h.m[lane] : LOW;
   const float M = warp_max(m);
-  const float d = (m - M) * c;
-  const float sc = lane < NW ? ex2(d) : 0.0f;
+  const float d = m - M;
+  const float sc = lane < NW ? ex2(d * c) : 0.0f;
   const float own = lane < NW ? h.own[lane] : 0.0f, other = lane < NW ? h.other[lane] : 0.0f;
   const int ow = __ffs(__ballot_sync(0xffffffffu, lane < NW && m == M)) - 1;
   const float s_all = warp_sum((other + own) * sc);
@@ -425,19 +429,21 @@ __device__ __noinline__ void select_by_rounds(uint64_t* best_of, const uint64_t*
 // A row's results, by one warp; key: lane i's the i-th alternative
 MPM_DEV void write_row(const LogprobFwd& p, long long row, const Stats& st, float zt, uint64_t key, int lane) {
   const bool some = st.m > LOW || st.rest != st.rest;
-  // NaN and +inf make every result of the row NaN
-  const float lr = st.m <= -LOW ? log1pf(st.rest) : NAN;
+  // NaN, +inf and quotients past MOST make every result of the row NaN
+  const float lr = !some || fabsf(st.m * p.inv_t) <= MOST ? log1pf(st.rest) : NAN;
+  // (of halves: the difference of two logits may overflow where its quotient by the temperature does not)
+  auto logp = [&](float z) { return fmaf(0.5f * z - 0.5f * st.m, 2.0f * p.inv_t, -lr); };
   if (lane == 0) {
     p.lse[row] = some ? fmaf(st.m, p.inv_t, lr) : -INFINITY;
-    if (p.logp) p.logp[row] = some ? (zt <= LOW ? (lr == lr ? -INFINITY : lr) : fmaf(zt - st.m, p.inv_t, -lr)) : -INFINITY;
+    if (p.logp) p.logp[row] = some ? (zt <= LOW ? (lr == lr ? -INFINITY : lr) : logp(zt)) : -INFINITY;
     if (p.entropy) {
-      const float h = lr - kLn2 * st.w / (1.0f + st.rest);
+      const float h = lr - (st.m > -FAR ? 0.0f : st.w * p.inv_t / (1.0f + st.rest));
       p.entropy[row] = some ? (h < 0.0f ? 0.0f : h) : 0.0f;       // a NaN passes
     }
   }
   if (lane < p.top) {
     p.top_ids[row * p.top + lane] = key ? (int)(0xFFFFFFFFu - (uint32_t)key) : -1;
-    p.top_logp[row * p.top + lane] = key ? fmaf(key_value(key) - st.m, p.inv_t, -lr) : lr == lr ? -INFINITY : lr;
+    p.top_logp[row * p.top + lane] = key ? logp(key_value(key)) : lr == lr ? -INFINITY : lr;
   }
 }
 
@@ -602,7 +608,7 @@ __global__ void __launch_bounds__(NT + 64, 2) token_logprob_kernel(const Logprob
           if (lane && lane < cs) o = sh.stats[lane];
           const float M = warp_max(o.x);
           const int first = __ffs(__ballot_sync(0xffffffffu, lane < cs && o.x == M)) - 1;
-          const float d = (o.x - M) * c, sc = lane < cs ? ex2(d) : 0.0f;
+          const float d = o.x - M, sc = lane < cs ? ex2(d * c) : 0.0f;
           const float rest = warp_sum(sc * (lane == first ? o.y : 1.0f + o.y));
           const float w_all = warp_sum(sc > 0.0f ? sc * fmaf(d, 1.0f + o.y, o.z) : 0.0f);
           st = Stats{M, rest, w_all};
@@ -734,8 +740,8 @@ __global__ void __launch_bounds__(NT + 64, 2) token_logprob_kernel(const Logprob
         tmax = fmaxf(tmax, bm);
         const float mw = warp_max(bm);
         if (mw > m) {
-          // 2^((z - m) c) -> 2^((z - mw) c): s 2^-D and (w - D s) 2^-D
-          const float D = fminf((mw - m) * c, 0x1p90f), f = ex2(-D);       // f is 0 there, and D s finite
+          // 2^((z - m) c) -> 2^((z - mw) c): s f and (w - D s) f, f = 2^(-D c)
+          const float D = fminf(mw - m, 0x1p90f), f = ex2(-D * c);         // f is 0 there, and D s finite
           const uint64_t f2 = f32x2(f, f), nD2 = f32x2(-D, -D);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -796,12 +802,12 @@ __global__ void __launch_bounds__(NT + 64, 2) token_logprob_kernel(const Logprob
         auto add = [&](const uint4& x) {
 #pragma unroll
           for (int i = 0; i < VE / 2; ++i) {
-            const uint64_t t2 = mul_f32x2(add2(pair<F32>(x, i), nm2), c2);
+            const uint64_t d2 = add2(pair<F32>(x, i), nm2);
             float lo, hi;
-            f32x2_split(t2, lo, hi);
+            f32x2_split(mul_f32x2(d2, c2), lo, hi);
             const uint64_t e2 = f32x2(ex2(lo), ex2(hi));
-            s2[i & 1] = add2(s2[i & 1], e2);
-            w2[i & 1] = fma2(e2, t2, w2[i & 1]);
+            w2[i & 1] = fma2(d2, e2, w2[i & 1]);
+            s2[i & 1] = add2(e2, s2[i & 1]);
           }
         };
 #pragma unroll
@@ -857,7 +863,7 @@ MPM_DEV void leave_out(uint4& v, float m) {
   for (int i = 0; i < 8; ++i) {
     if (!found && element<false>(v, i) == m) {
       found = true;
-      w[i >> 1] = (i & 1) ? (w[i >> 1] & 0xFFFFu) | 0xF1800000u : (w[i >> 1] & 0xFFFF0000u) | 0xF180u;
+      w[i >> 1] = (i & 1) ? (w[i >> 1] & 0xFFFFu) | 0xFF7F0000u : (w[i >> 1] & 0xFFFF0000u) | 0xFF7Fu;
     }
   }
   v = make_uint4(w[0], w[1], w[2], w[3]);
@@ -994,12 +1000,12 @@ __global__ void __launch_bounds__(SHORT_WARPS * 32, VL > 4 ? 4 : 8) token_logpro
     if (u * TEAM < r.nv) {
 #pragma unroll
       for (int i = 0; i < VE / 2; ++i) {
-        const uint64_t t2 = mul_f32x2(add2(pair<F32>(v[u], i), nm2), c2);
+        const uint64_t d2 = add2(pair<F32>(v[u], i), nm2);
         float lo, hi;
-        f32x2_split(t2, lo, hi);
+        f32x2_split(mul_f32x2(d2, c2), lo, hi);
         const uint64_t e2 = f32x2(ex2(lo), ex2(hi));
         s2[i & 1] = add2(s2[i & 1], e2);
-        w2[i & 1] = fma2(e2, t2, w2[i & 1]);
+        w2[i & 1] = fma2(e2, d2, w2[i & 1]);
       }
     }
   }
@@ -1060,6 +1066,20 @@ __global__ void __launch_bounds__(SHORT_WARPS * 32, VL > 4 ? 4 : 8) token_logpro
 // 2^lt U vectors, goes to a team of 2^lt threads: a block, or, where rows are short, down to a warp.
 // (A team of the whole block is known as such, so that what is the same for the block stays out of the threads'
 // registers: with the team's size as an argument alone 8192 x 32768 bf16 took 269 us instead of 163.)
+// A vector of a row whose lse is -2^90 or less: the scaled logits next to it are 2^66 away or more, so p is 1 at lse and 0
+// elsewhere, as it is of 0, FAR and (out of reach) -inf with an lse of 0.
+template <bool F32>
+MPM_DEV uint4 at_lse(const uint4& v, float inv_t, float lse) {
+  uint32_t w[4];
+  auto bits = [&](int i) {
+    const float z = element<F32>(v, i);
+    return z * inv_t == lse ? 0u : (F32 ? 0x10000u : 1u) * (z > LOW ? 0xF180u : 0xFF80u);
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = F32 ? bits(i) : bits(2 * i) | (bits(2 * i + 1) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 template <bool F32, bool OUT32, bool PARTS>
 __global__ void __launch_bounds__(NT, PARTS ? 3 : 4) token_logprob_backward_kernel(const LogprobBwd p, const int chunks, const int lt) {
   constexpr int VE = Row<F32>::VE, OS = OUT32 ? 4 : 2;
@@ -1106,8 +1126,13 @@ __global__ void __launch_bounds__(NT, PARTS ? 3 : 4) token_logprob_backward_kern
     if (i + step < items) load(nx, nv);
     const Row<F32> r(p.logits, x.row, p.ld, p.V);
     const bool zero = x.t < 0 || x.lse == -INFINITY;
+    if (__builtin_expect(!zero && x.lse <= -0x1p90f, 0)) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = at_lse<F32>(v[u], p.inv_t, x.lse);
+      x.lse = 0.0f;
+    }
     // -p (g_l + g_h (log p + H)) / temperature = p (A log p + B)
-    const float A = -x.gh * p.inv_t, B = -(x.gl + x.gh * x.H) * p.inv_t;
+    const float A = -x.gh * p.inv_t, G = x.gl * p.inv_t, K = x.gh * x.H * p.inv_t, B = -(G + K);
     const uint64_t it2 = f32x2(p.inv_t, p.inv_t), zero2 = f32x2(p.zero, p.zero), nl2 = f32x2(-x.lse, -x.lse), k2 = f32x2(kLog2e, kLog2e);
     const uint64_t A2 = f32x2(A, A), B2 = f32x2(B, B);
     uint8_t* out = static_cast<uint8_t*>(p.out) + x.row * p.ldo * OS;
@@ -1124,13 +1149,14 @@ __global__ void __launch_bounds__(NT, PARTS ? 3 : 4) token_logprob_backward_kern
 #pragma unroll
         for (int j = 0; j < VE; ++j) d[j] = 0.0f;
       } else {
-        clamp_max<F32>(v[u]);
+        uint4 near = v[u];
+        clamp_max<F32, true>(near);
 #pragma unroll
         for (int j = 0; j < VE / 2; ++j) {
           // The scaled logit is rounded before lse is taken off, as lse was: so no p comes out above 1 (at logits of 1e9
           // lse's rounding is 32), and where a token is nearly certain the difference is 0 rather than what that left.
           // (A zero that the compiler does not know: a product would be drawn into the sum.)
-          const uint64_t lp2 = add2(fma2(pair<F32>(v[u], j), it2, zero2), nl2);
+          const uint64_t lp2 = add2(fma2(pair<F32>(near, j), it2, zero2), nl2);
           float lo, hi;
           f32x2_split(mul_f32x2(lp2, k2), lo, hi);
           const uint64_t e2 = f32x2(ex2(lo), ex2(hi));         // p log p first: 0 where p is
@@ -1140,8 +1166,8 @@ __global__ void __launch_bounds__(NT, PARTS ? 3 : 4) token_logprob_backward_kern
 #pragma unroll
           for (int j = 0; j < VE; ++j)
             if (x.t == e + j) {
-              const float z = element<F32>(v[u], j), lp = __fsub_rn(__fmul_rn(z, p.inv_t), x.lse);
-              d[j] = z <= LOW && x.lse == x.lse ? 0.0f : -p.inv_t * (x.gl * expm1f(lp) + x.gh * expf(lp) * (lp + x.H));
+              const float z = element<F32>(v[u], j), lp = max_nan(__fsub_rn(__fmul_rn(z, p.inv_t), x.lse), FAR);
+              d[j] = z <= LOW && x.lse == x.lse ? 0.0f : -fmaf(G, expm1f(lp), expf(lp) * fmaf(-A, lp, K));
             }
         }
       }

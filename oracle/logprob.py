@@ -1,7 +1,7 @@
 """Log probabilities of tokens, their entropy and alternatives, and the
 gradient, in fp64 numpy.
 
-    z = logits / temperature, over the tokens in reach (logit above -2^100)
+    z = logits / temperature, over the tokens in reach (logit above bf16's lowest finite value)
     lse = log sum e^z,  logp = z[target] - lse,  H = -sum p log p
     dz_i = g_l ([i = target] - p_i) - g_h p_i (log p_i + H)
 
@@ -9,7 +9,7 @@ A negative target leaves its row out.  A row with NaN or +inf is NaN.
 """
 import numpy as np
 
-LOW = -2.0 ** 100
+LOW = -(2.0 - 2.0 ** -7) * 2.0 ** 127          # bf16's lowest finite value
 
 
 def _row(l, temperature):

@@ -9,7 +9,9 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import logprob as O
 from tests.gpu_util import need_gpu
+from tests.test_gpu_logprob import _close
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +83,146 @@ def test_alternatives_of_a_row_with_nan(bf16, T, V):
     assert (o["lse"].isnan() == (row > 0)).all()
     assert (o["top_logp"].isnan() == (row > 0)[:, None]).all()
     assert ((o["top_ids"] >= -1) & (o["top_ids"] < V)).all()
+
+
+def _in_range(v, what):
+    """Log probabilities past fp32's numbers are -inf."""
+    return v if what == "lse" else np.where(v < -float(np.finfo(np.float32).max), -np.inf, v)
+
+
+def _forward(l, targets, temperature, top, distinct):
+    """token_logprob of rows that repeat the first `distinct` ones, each against fp64.  What moves a result: a term
+    e^(z - M) by 4 u of the exponential and by its argument's five roundings (1 / temperature, its product with
+    log2 e and that constant, the difference, the product with it), 5 u |z - M|; the sum of V terms by (40 + V / 1024) u; w's
+    terms by theirs times |z - M|."""
+    ops = _ops()
+    V = l.shape[1]
+    n, nt = l[:distinct].float().cpu().numpy().astype(np.float64), targets[:distinct].cpu().numpy()
+    want = O.token_logprob(n, nt, temperature, top)
+    o = ops.token_logprob(l, targets, temperature=temperature, entropy=True, top=top)
+    live = n > O.LOW
+    d = np.where(live, (want["M"][:, None] - np.where(live, n, 0) / temperature), np.inf)
+    e = np.exp(-d)
+    far = np.where(d < 1e3, d, 0)                  # e is 0 beyond
+    some = live.any(1)
+    near = lambda f: np.where(some, (e * f).sum(1), 0)
+    rest, w, s2 = want["rest"], near(far), near(far * far)
+    rel = (44 + V / 1024) * UNIT
+    d_rest = rel * rest + 5 * UNIT * w
+    lr = np.log1p(rest)
+    d_lr = d_rest / (1 + rest) + 4 * UNIT * lr
+    w1 = w / (1 + rest)
+    tol = {"lse": d_lr + 4 * UNIT * (np.abs(want["M"]) + lr),
+           "entropy": d_lr + (rel * w + 5 * UNIT * s2) / (1 + rest) + w1 * (d_rest / (1 + rest) + 6 * UNIT) + 2 * UNIT * (lr + w1)}
+    gap = lambda x, r: np.where(np.isfinite(x), np.abs(np.where(np.isfinite(x), x, 0) + r), 0)
+    tol["logp"] = d_lr + 4 * UNIT * (gap(want["logp"], lr) + lr)
+    tol["top_logp"] = d_lr[:, None] + 4 * UNIT * (gap(want["top_logp"], lr[:, None]) + lr[:, None])
+    T = l.shape[0]
+    of = np.arange(T) % distinct
+    for k in tol:
+        if k in o:
+            _close(o[k].cpu().numpy(), _in_range(want[k], k)[of], tol[k][of], k)
+    if top:
+        assert np.array_equal(o["top_ids"].cpu().numpy(), want["top_ids"][of]), "alternatives"
+    assert ops.get_device_status() == 0
+    return o
+
+
+def _odd_rows(T, V, dtype, temperature, seed=0):
+    """Rows whose logits reach the ends of the type's range, repeated; (logits, targets)."""
+    rng = np.random.default_rng(seed)
+    low = float(torch.finfo(torch.bfloat16).min)
+    r = rng.normal(size=(8, V)) * 2
+    t = np.zeros(8, np.int64)
+    hit = rng.permutation(V)
+    r[0, hit[:V // 3]] = -1e35                     # far down, in reach all the same: no weight, but a log probability
+    t[0] = hit[0]
+    r[1] = -1e31 * (1 + rng.integers(0, 8, V) / 8)  # nothing above -2^100
+    t[1] = r[1].argmax()
+    r[2] = -np.inf                                 # alternatives from both ends
+    r[2, hit[:5]] = 1.0, 0.5, -2e30, -1e33, -3e38
+    t[2] = hit[3]
+    r[3, hit[:3]] = 1e31                           # three equal ones above 2^100
+    t[3] = hit[1]
+    r[4] = np.where(rng.random(V) < 0.5, -2e38, -np.inf)
+    r[4, hit[0]] = 2e38
+    t[4] = hit[0]
+    r[5] = low                                     # the lowest value is a mask, the next one is not (its quotient in range)
+    r[5, hit[0]] = -2e38 if temperature < 1 else np.nextafter(np.float32(low), np.float32(0)) if dtype == torch.float32 else -3.3762318e38
+    t[5] = hit[0]
+    r[6, hit[0]] = 2.3e38
+    t[6] = hit[2]
+    t[7] = r[7].argmax()
+    l = torch.from_numpy(r.astype(np.float32)).to(dtype)
+    n = (T + 7) // 8
+    return l.repeat(n, 1)[:T].contiguous().cuda(), torch.from_numpy(t).repeat(n)[:T].cuda()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T,V,top", [(8, 300, 5), (8, 50001, 20), (40, 131072, 32), (700, 777, 0), (400, 4000, 5), (400, 7000, 1), (400, 15000, 8)])
+@pytest.mark.parametrize("temperature", [1.0, 0.7, 1.3])
+def test_every_finite_logit_above_the_lowest_is_in_reach(bf16, T, V, top, temperature):
+    l, t = _odd_rows(T, V, torch.bfloat16 if bf16 else torch.float32, temperature)
+    o = _forward(l, t, temperature, top, 8)
+    assert o["logp"].isfinite().all() and o["lse"].isfinite().all()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T,V", [(8, 300), (8, 50001), (2000, 300), (1400, 1500)])
+@pytest.mark.parametrize("temperature", [1.0, 0.7, 1.3])
+def test_gradient_of_logits_at_the_ends_of_the_range(bf16, T, V, temperature):
+    """Where lse is huge p is 1 at the largest logits and 0 elsewhere; a target far below the others gets its dlogp."""
+    dtype = torch.bfloat16 if bf16 else torch.float32
+    l, t = _odd_rows(T, V, dtype, temperature)
+    o = _ops().token_logprob(l, t, temperature=temperature, entropy=True)
+    g = torch.Generator(device="cuda").manual_seed(V)
+    dl, dh = (torch.randn(8, device="cuda", generator=g).repeat((T + 7) // 8)[:T].contiguous() for _ in range(2))
+    n, nt = l[:8].float().cpu().numpy().astype(np.float64), t[:8].cpu().numpy()
+    lse, H = o["lse"][:8].cpu().numpy().astype(np.float64), o["entropy"][:8].cpu().numpy().astype(np.float64)
+    assert abs(H[3] - math.log(3)) <= 8 * UNIT and np.abs(H[[4, 5, 6]]).max() == 0
+    for a, b in ((dl, dh), (dl, None), (None, dh)):
+        na, nb = (np.zeros(8) if x is None else x[:8].cpu().numpy().astype(np.float64) for x in (a, b))
+        want, mag = O.token_logprob_backward(n[[0, 2, 7]], nt[[0, 2, 7]], lse[[0, 2, 7]], na[[0, 2, 7]], H[[0, 2, 7]], nb[[0, 2, 7]], temperature)
+        full, size = np.zeros((8, V)), np.zeros((8, V))
+        full[[0, 2, 7]], size[[0, 2, 7]] = want, mag
+        for r in (1, 3, 4, 5, 6):
+            top = n[r] == n[r].max()
+            full[r] = np.where(top, -(na[r] + nb[r] * H[r]), 0.0) / temperature
+            full[r, nt[r]] = (-nb[r] * H[r] if top[nt[r]] else na[r]) / temperature
+            size[r] = np.where(top, np.abs(na[r]) + np.abs(nb[r]) * H[r], 0.0) / temperature
+        live = np.where(n > -2.0 ** 100, n, 0.0)
+        arg = np.where((np.abs(lse) < 1e20)[:, None], np.abs(live) / temperature + np.abs(lse)[:, None], 0.0)
+        # a p below fp32's normal numbers is 0; a result of one product, dlogp / temperature, is off by the roundings of 1 /
+        # temperature and of itself
+        tol = 2 * UNIT * np.abs(full) + size * (16 * UNIT + 8 * UNIT * arg) + 8 * UNIT * arg * (np.abs(na) + np.abs(nb))[:, None] / temperature + 2.0 ** -120
+        for out in (None, torch.full((T, V), 7.0, dtype=torch.float32, device="cuda"), l.clone()):
+            src = out if out is not None and out.dtype == dtype and out.shape == l.shape and torch.equal(out, l) else l
+            got = _ops().token_logprob_backward(src, t, o["lse"], dlogp=a, entropy=None if b is None else o["entropy"],
+                                                dentropy=b, temperature=temperature, out=out)
+            extra = 2.0 ** -8 * np.abs(full) if got.dtype == torch.bfloat16 else 0.0
+            of = np.arange(T) % 8
+            _close(got.float().cpu().numpy(), full[of], (tol + extra)[of], "dlogits")
+    assert _ops().get_device_status() == 0
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T,V", [(4, 300), (4, 50001), (400, 300), (400, 4000), (400, 15000)])
+def test_quotients_past_the_range_are_nan(bf16, T, V):
+    """A largest logit whose quotient by the temperature no fp32 number holds makes its row NaN, as +inf does; logits far
+    below the largest may have such a quotient."""
+    l = torch.randn(4, V, device="cuda")
+    l[1, 5] = 3e38
+    l[2] = -3e38
+    l[3, ::3] = -3e38
+    l = l.to(torch.bfloat16 if bf16 else torch.float32).repeat((T + 3) // 4, 1)[:T].contiguous()
+    t = torch.full((T,), 5, device="cuda")
+    o = _ops().token_logprob(l, t, temperature=0.5, entropy=True, top=2)
+    row = torch.arange(T, device="cuda") % 4
+    bad = (row == 1) | (row == 2)
+    for k in ("logp", "lse", "entropy"):
+        assert torch.equal(o[k].isnan(), bad), k
+    assert torch.equal(o["top_logp"].isnan(), bad[:, None].expand(T, 2)) and o["logp"][~bad].isfinite().all()
+    one = torch.ones(T, device="cuda")
+    for a, b in ((one, None), (None, one)):
+        d = _ops().token_logprob_backward(l, t, o["lse"], dlogp=a, entropy=None if b is None else o["entropy"], dentropy=b, temperature=0.5)
+        assert d[bad].isnan().all() and d[~bad].isfinite().all()
