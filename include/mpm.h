@@ -621,6 +621,18 @@ mpm_status mpm_token_logprob_backward(const void* logits_dev, int logits_dtype, 
                                       float temperature, void* dlogits_dev, int dlogits_dtype, int64_t ldd,
                                       cudaStream_t stream);
 
+/*
+ * The same from the forward's logp_dev too (fp32 [T], nullable).  The target's own term is then taken from it: lse is rounded
+ * to fp32, by up to 2^-25 of its magnitude, and where a target is nearly certain that is as much as 1 - p itself (at lse = 25
+ * and 1 - p = 6e-8 the difference logit - lse is 0).  Every other token's term is p's, whose relative error is that rounding; of a
+ * nearly certain token that is not the target, log p + entropy keeps it.
+ */
+mpm_status mpm_token_logprob_backward_from(const void* logits_dev, int logits_dtype, int64_t T, int64_t V, int64_t ld,
+                                           const void* targets_dev, int targets_type, const float* logp_dev,
+                                           const float* lse_dev, const float* dlogp_dev, const float* entropy_dev,
+                                           const float* dentropy_dev, float temperature, void* dlogits_dev,
+                                           int dlogits_dtype, int64_t ldd, cudaStream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* Dequantisation and transpose: operands of the BF16 backward              */
 /* ------------------------------------------------------------------------ */

@@ -105,6 +105,8 @@ _SIGS = {
     "mpm_token_logprob": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _int, _f32, _int, _vp, _vp, _vp, _vp, _vp, _vp]),
     "mpm_token_logprob_backward": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _int, _vp, _vp, _vp, _vp, _f32, _vp, _int,
                                           _i64, _vp]),
+    "mpm_token_logprob_backward_from": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _int, _vp, _vp, _vp, _vp, _vp, _f32, _vp,
+                                               _int, _i64, _vp]),
     "mpm_moe_combine_dprob": (_int, [_vp, _vp, _vp, _vp, _i64, _int, _i64, _i64, _vp, _vp]),
     "mpm_moe_gather_mxfp8": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _vp, _i64, _i64, _vp, _vp, _vp]),
     "mpm_nvfp4_dequantize": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp]),

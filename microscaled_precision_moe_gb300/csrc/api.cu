@@ -498,7 +498,16 @@ mpm_status mpm_token_logprob_backward(const void* logits, int dtype, int64_t T, 
                                       const void* targets, int targets_type, const float* lse, const float* dlogp,
                                       const float* entropy, const float* dentropy, float temperature, void* out,
                                       int out_dtype, int64_t ldd, cudaStream_t stream) {
-  if (!logits || !lse || !out || (dentropy && !entropy) || (dlogp && !targets)) return MPM_ERR_NULL;
+  return mpm_token_logprob_backward_from(logits, dtype, T, V, ld, targets, targets_type, nullptr, lse, dlogp, entropy, dentropy,
+                                         temperature, out, out_dtype, ldd, stream);
+}
+
+mpm_status mpm_token_logprob_backward_from(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                                           const void* targets, int targets_type, const float* logp, const float* lse,
+                                           const float* dlogp, const float* entropy, const float* dentropy,
+                                           float temperature, void* out, int out_dtype, int64_t ldd,
+                                           cudaStream_t stream) {
+  if (!logits || !lse || !out || (dentropy && !entropy) || ((dlogp || logp) && !targets)) return MPM_ERR_NULL;
   if ((dtype != MPM_DTYPE_BF16 && dtype != MPM_DTYPE_F32) ||
       (out_dtype != MPM_DTYPE_BF16 && out_dtype != MPM_DTYPE_F32) ||
       (targets && targets_type != MPM_INDEX_I32 && targets_type != MPM_INDEX_I64))
@@ -506,13 +515,13 @@ mpm_status mpm_token_logprob_backward(const void* logits, int dtype, int64_t T, 
   if (T < 1 || T > (1ll << 31) - 1 || V < 1 || V > (1ll << 31) - 64 || ld < V || ldd < V) return MPM_ERR_SHAPE;
   if (!(temperature >= 1e-3f && temperature <= 1e3f)) return MPM_ERR_SHAPE;
   if (!aligned(logits, dtype == MPM_DTYPE_F32 ? 4 : 2) || !aligned(out, out_dtype == MPM_DTYPE_F32 ? 4 : 2) ||
-      !aligned(targets, targets_type == MPM_INDEX_I64 ? 8 : 4) || !aligned(lse, 4) || !aligned(dlogp, 4) ||
+      !aligned(targets, targets_type == MPM_INDEX_I64 ? 8 : 4) || !aligned(logp, 4) || !aligned(lse, 4) || !aligned(dlogp, 4) ||
       !aligned(entropy, 4) || !aligned(dentropy, 4))
     return MPM_ERR_ALIGN;
   mpm::LogprobBwd p{};
   p.logits = logits; p.f32 = dtype == MPM_DTYPE_F32; p.T = T; p.V = V; p.ld = ld;
   p.targets = targets; p.targets_i64 = targets_type == MPM_INDEX_I64;
-  p.lse = lse; p.dlogp = dlogp; p.entropy = entropy; p.dentropy = dentropy;
+  p.logp = logp; p.lse = lse; p.dlogp = dlogp; p.entropy = entropy; p.dentropy = dentropy;
   p.inv_t = 1.0f / temperature;
   p.out = out; p.out_f32 = out_dtype == MPM_DTYPE_F32; p.ldo = ldd;
   p.status = status_ptr();

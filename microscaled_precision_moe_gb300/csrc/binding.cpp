@@ -549,20 +549,23 @@ PyObject* token_logprob(PyObject* const* a, Py_ssize_t n) {
   return d.give();
 }
 
-// (logits, targets, lse, dlogp, entropy, dentropy, temperature, out)
+// (logits, targets, lse, dlogp, entropy, dentropy, temperature, out, logp)
 PyObject* token_logprob_backward(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 8);
+  need_args(n, 9);
   const Tensor &l = *tensor(a[0], "logits"), &lse = *tensor(a[2], "lse");
   const Tensor *targets = tensor(a[1], "targets", true), *dlogp = tensor(a[3], "dlogp", true),
-               *h = tensor(a[4], "entropy", true), *dh = tensor(a[5], "dentropy", true), *out = tensor(a[7], "out", true);
+               *h = tensor(a[4], "entropy", true), *dh = tensor(a[5], "dentropy", true), *out = tensor(a[7], "out", true),
+               *logp = tensor(a[8], "logp", true);
   const int type = float_type(l, "logits");
   const int64_t ld = row_pitch(l, "logits"), T = l.size(0), V = l.size(1);
   const int it = index_type(targets, T);
   const ScalarType f32 = ScalarType::Float;
   need_rows(&lse, "lse", f32, T);
+  need_rows(logp, "logp", f32, T);
   need_rows(dlogp, "dlogp", f32, T);
   need_rows(h, "entropy", f32, T);
   need_rows(dh, "dentropy", f32, T);
+  if (logp && !targets) fail(PyExc_ValueError, "logp: log probabilities of targets need targets");
   if (dlogp && !targets) fail(PyExc_ValueError, "dlogp: a gradient of logp needs targets");
   if (dh && !h) fail(PyExc_ValueError, "dentropy: a gradient of the entropy needs the forward's entropy");
   const double temperature = real(a[6]);
@@ -572,13 +575,13 @@ PyObject* token_logprob_backward(PyObject* const* a, Py_ssize_t n) {
     out_type = float_type(*out, "out");
     ldd = matrix(*out, "out", out->scalar_type(), T, V);
   }
-  const auto device = need_cuda({&l, targets, &lse, dlogp, h, dh, out});
+  const auto device = need_cuda({&l, targets, logp, &lse, dlogp, h, dh, out});
   Tensor made;
   if (!out) { made = make({T, V}, l.scalar_type()); out = &made; }
-  check(mpm_token_logprob_backward(l.data_ptr(), type, T, V, ld, ptr(targets), it, static_cast<float*>(lse.data_ptr()),
-                                   static_cast<float*>(ptr(dlogp)), static_cast<float*>(ptr(h)),
-                                   static_cast<float*>(ptr(dh)), (float)temperature, out->data_ptr(), out_type, ldd,
-                                   stream_of(l)),
+  check(mpm_token_logprob_backward_from(l.data_ptr(), type, T, V, ld, ptr(targets), it, static_cast<float*>(ptr(logp)),
+                                        static_cast<float*>(lse.data_ptr()), static_cast<float*>(ptr(dlogp)),
+                                        static_cast<float*>(ptr(h)), static_cast<float*>(ptr(dh)), (float)temperature,
+                                        out->data_ptr(), out_type, ldd, stream_of(l)),
         "mpm_token_logprob_backward");
   if (a[7] != Py_None) { Py_INCREF(a[7]); return a[7]; }
   PyObject* p = THPVariable_Wrap(made);

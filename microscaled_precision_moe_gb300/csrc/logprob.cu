@@ -1062,7 +1062,8 @@ __global__ void __launch_bounds__(SHORT_WARPS * 32, VL > 4 ? 4 : 8) token_logpro
 
 // ---------------------------------------------------------------- gradient
 //   dz_i = g_l ([i = t] - p_i) - g_h p_i (log p_i + H),  p_i = e^(z_i - lse)
-// in one read and one write; the given token's own 1 - p is -expm1(log p).  An item, a row's chunk of
+// in one read and one write; the given token's own 1 - p is -expm1(log p), of the forward's log p where that is given: lse
+// rounded to fp32 holds no 1 - p of a nearly certain token.  An item, a row's chunk of
 // 2^lt U vectors, goes to a team of 2^lt threads: a block, or, where rows are short, down to a warp.
 // (A team of the whole block is known as such, so that what is the same for the block stays out of the threads'
 // registers: with the team's size as an argument alone 8192 x 32768 bf16 took 269 us instead of 163.)
@@ -1079,6 +1080,10 @@ MPM_DEV uint4 at_lse(const uint4& v, float inv_t, float lse) {
   for (int i = 0; i < 4; ++i) w[i] = F32 ? bits(i) : bits(2 * i) | (bits(2 * i + 1) << 16);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+
+// The same as a call: where registers are short (teams; 8192 x 1000 bf16 13.5 us, 14.0 in line, whose code spills)
+template <bool F32>
+__device__ __noinline__ uint4 at_lse_called(const uint4 v, float inv_t, float lse) { return at_lse<F32>(v, inv_t, lse); }
 
 template <bool F32, bool OUT32, bool PARTS>
 __global__ void __launch_bounds__(NT, PARTS ? 3 : 4) token_logprob_backward_kernel(const LogprobBwd p, const int chunks, const int lt) {
@@ -1128,7 +1133,7 @@ __global__ void __launch_bounds__(NT, PARTS ? 3 : 4) token_logprob_backward_kern
     const bool zero = x.t < 0 || x.lse == -INFINITY;
     if (__builtin_expect(!zero && x.lse <= -0x1p90f, 0)) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = at_lse<F32>(v[u], p.inv_t, x.lse);
+      for (int u = 0; u < U; ++u) v[u] = PARTS ? at_lse_called<F32>(v[u], p.inv_t, x.lse) : at_lse<F32>(v[u], p.inv_t, x.lse);
       x.lse = 0.0f;
     }
     // -p (g_l + g_h (log p + H)) / temperature = p (A log p + B)
@@ -1166,7 +1171,8 @@ __global__ void __launch_bounds__(NT, PARTS ? 3 : 4) token_logprob_backward_kern
 #pragma unroll
           for (int j = 0; j < VE; ++j)
             if (x.t == e + j) {
-              const float z = element<F32>(v[u], j), lp = max_nan(__fsub_rn(__fmul_rn(z, p.inv_t), x.lse), FAR);
+              const float z = element<F32>(v[u], j), own = p.logp ? p.logp[x.row] : __fsub_rn(__fmul_rn(z, p.inv_t), x.lse);
+              const float lp = max_nan(own, FAR);
               d[j] = z <= LOW && x.lse == x.lse ? 0.0f : -fmaf(G, expm1f(lp), expf(lp) * fmaf(-A, lp, K));
             }
         }

@@ -21,6 +21,7 @@ struct LogprobBwd {
   const void* logits; int f32; long long T, V, ld;
   const void* targets; int targets_i64;    // [T] (nullable)
   const float* lse;                        // [T]
+  const float* logp;                       // [T] (nullable: log p of the targets from lse)
   const float* dlogp;                      // [T] (nullable)
   const float* entropy; const float* dentropy;   // [T] (nullable, both or none)
   float inv_t; float zero;                 // 1 / temperature; 0

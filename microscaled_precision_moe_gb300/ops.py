@@ -492,13 +492,15 @@ def token_logprob(logits, targets=None, temperature=1.0, entropy=False, top=0, o
 
 
 def token_logprob_backward(logits, targets, lse, dlogp=None, entropy=None, dentropy=None,
-                           temperature=1.0, out=None):
+                           temperature=1.0, out=None, logp=None):
     """dlogits [T, V] (the logits' type, or that of ``out``, bf16 or fp32) of
     token_logprob with the same arguments, from dlogp and / or dentropy fp32 [T]
-    and the forward's lse (and entropy, with dentropy).  ``out`` may be the
-    logits themselves.  Rows with a NaN lse get NaN."""
+    and the forward's lse (and entropy, with dentropy).  With the forward's ``logp``
+    the gradient of nearly certain targets keeps its relative precision; lse alone
+    leaves it a rounding of lse.  ``out`` may be the logits themselves.  Rows with
+    a NaN lse get NaN."""
     return (_native_module or _native()).token_logprob_backward(logits, targets, lse, dlogp, entropy,
-                                                                dentropy, temperature, out)
+                                                                dentropy, temperature, out, logp)
 
 
 # ------------------------------------------------------------------ GEMM

@@ -58,9 +58,10 @@ def token_logprob(logits, targets=None, temperature=1.0, top=0):
     return o
 
 
-def token_logprob_backward(logits, targets, lse, dlogp=None, entropy=None, dentropy=None, temperature=1.0):
-    """(dlogits, mag): the gradient from the given lse (and entropy), and the sum of
-    the magnitudes of the terms each element is made of."""
+def token_logprob_backward(logits, targets, lse, dlogp=None, entropy=None, dentropy=None, temperature=1.0, logp=None):
+    """(dlogits, mag): the gradient from the given lse (and entropy; and log p of the
+    targets where it is given), and the sum of the magnitudes of the terms each
+    element is made of."""
     l = np.asarray(logits, np.float64)
     T, V = l.shape
     d, mag = np.zeros((T, V)), np.zeros((T, V))
@@ -69,6 +70,8 @@ def token_logprob_backward(logits, targets, lse, dlogp=None, entropy=None, dentr
             continue
         live = l[t] > LOW
         lp = np.where(live, l[t], 0.0) / temperature - lse[t]
+        if logp is not None and live[targets[t]]:
+            lp[targets[t]] = logp[t]
         p = np.where(live, np.exp(np.where(live, lp, -np.inf)), 0.0)
         g = 0.0 if dlogp is None else float(dlogp[t])
         gh = 0.0 if dentropy is None else float(dentropy[t])

@@ -91,3 +91,18 @@ def test_structure_mirrors_the_header(lib):
     from microscaled_precision_moe_gb300 import _lib as L
     # two ints, four sizes, two pitches, eleven pointers and the workspace's size, without padding
     assert C.sizeof(L.FewTokensDesc) == 2 * 4 + 4 * 8 + 2 * 8 + 11 * 8 + 8
+
+
+def _bwd_from(lib, logits=FAKE, dtype=0, T=4, V=100, ld=100, targets=FAKE, tt=0, logp=FAKE, lse=FAKE, dlogp=FAKE, H=FAKE, dH=FAKE,
+              temp=1.0, out=FAKE, odt=0, ldd=100):
+    v = lambda p: None if p is None else C.c_void_p(p)
+    return lib.mpm_token_logprob_backward_from(v(logits), dtype, T, V, ld, v(targets), tt, v(logp), v(lse), v(dlogp), v(H), v(dH),
+                                               temp, v(out), odt, ldd, None)
+
+
+@pytest.mark.parametrize("status,change", [
+    (1, dict(logits=None)), (1, dict(lse=None)), (1, dict(out=None)), (1, dict(H=None)), (1, dict(targets=None)),
+    (1, dict(targets=None, dlogp=None)), (4, dict(dtype=3)), (4, dict(tt=5)), (2, dict(T=0)), (2, dict(ldd=99)), (2, dict(temp=0.0)),
+    (3, dict(logp=FAKE + 2)), (3, dict(lse=FAKE + 2)), (3, dict(out=FAKE + 1))])
+def test_token_logprob_backward_from(lib, status, change):
+    assert _bwd_from(lib, **change) == status

@@ -226,3 +226,89 @@ def test_quotients_past_the_range_are_nan(bf16, T, V):
     for a, b in ((one, None), (None, one)):
         d = _ops().token_logprob_backward(l, t, o["lse"], dlogp=a, entropy=None if b is None else o["entropy"], dentropy=b, temperature=0.5)
         assert d[bad].isnan().all() and d[~bad].isfinite().all()
+
+
+def _certain_rows(T, V, dtype):
+    """Rows with one token far above the others, by 14 to 26, shifted so that lse is about 0, 20 and 40."""
+    gap = torch.arange(T) % 13 + 14.0
+    l = torch.zeros(T, V)
+    top = (torch.arange(T) * 613) % V
+    l[torch.arange(T), top] = gap
+    return (l + (torch.arange(T) % 3 * 20.0)[:, None]).to(dtype).cuda(), top.cuda(), gap.double().numpy()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T,V", [(39, 4096), (39, 50001), (1300, 1000)])
+def test_gradient_of_nearly_certain_targets(bf16, T, V):
+    """With the forward's logp the target's 1 - p is relatively exact, and the terms of a row cancel: against the closed
+    form, p = 1 / (1 + (V - 1) e^-gap).  logp is off by its own bound, (44 + V / 1024) u of it and 5 u gap of its argument's
+    rounding, and by 4 u; expm1, the products and the entropy's two terms add 16 u of the terms' magnitudes."""
+    ops = _ops()
+    l, t, gap = _certain_rows(T, V, torch.bfloat16 if bf16 else torch.float32)
+    o = ops.token_logprob(l, t, entropy=True)
+    rest = (V - 1) * np.exp(-gap)
+    p, lr = 1 / (1 + rest), np.log1p(rest)
+    H = lr + rest * gap / (1 + rest)
+    f32 = torch.zeros(T, V, device="cuda")
+    ones = torch.ones(T, device="cuda")
+    rel = (44 + V / 1024 + 5 * gap + 4) * UNIT
+    at = t.cpu().numpy()
+    # dlogp: the target's 1 - p
+    d = ops.token_logprob_backward(l, t, o["lse"], dlogp=ones, out=f32, logp=o["logp"]).cpu().numpy().astype(np.float64)
+    want = -np.expm1(-lr)
+    assert np.all(np.abs(d[np.arange(T), at] - want) <= want * (rel + 16 * UNIT))
+    # the rest of the row is -p of each other token, off by lse's rounding, which is 2^-24 of it, and as much of the scaled logit
+    lse = l.float().cpu().numpy().max(1) + lr
+    assert np.all(np.abs(d.sum(1)) <= want * (rel + (32 + 4 * lse) * UNIT))
+    # dentropy at the target: -p (log p + H), whose terms are lr and H
+    d = ops.token_logprob_backward(l, t, o["lse"], entropy=o["entropy"], dentropy=ones, out=f32, logp=o["logp"]).cpu().numpy()
+    want = -p * (H - lr)
+    s2 = rest * gap * gap / (1 + rest)
+    tol = (rel + 16 * UNIT) * (lr + H) + 5 * UNIT * s2
+    assert np.all(np.abs(d[np.arange(T), at] - want) <= tol)
+    assert ops.get_device_status() == 0
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_gradient_with_logp_is_the_same_elsewhere(bf16):
+    """Ordinary targets, unscored rows, masked targets, rows with nothing in reach, NaN: with logp within the rounding of
+    lse at the target, and the same bits everywhere else; in place and captured too."""
+    ops = _ops()
+    T, V = 61, 3001
+    l = torch.randn(T, V + 3, device="cuda").mul_(2).to(torch.bfloat16 if bf16 else torch.float32)[:, :V]
+    t = torch.randint(0, V, (T,), device="cuda")
+    l[3, ::2] = -torch.inf
+    l[4] = -torch.inf
+    l[5, t[5]] = -torch.inf
+    l[6, 9] = torch.nan
+    t[7:9] = -1
+    o = ops.token_logprob(l, t, entropy=True)
+    dl, dh = torch.randn(T, device="cuda"), torch.randn(T, device="cuda")
+    kw = dict(dlogp=dl, entropy=o["entropy"], dentropy=dh)
+    base = ops.token_logprob_backward(l, t, o["lse"], **kw)
+    got = ops.token_logprob_backward(l, t, o["lse"], logp=o["logp"], **kw)
+    hot = torch.zeros(T, V, dtype=torch.bool, device="cuda")
+    hot[t >= 0, t[t >= 0]] = True
+    same = lambda a, b: torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0))
+    assert same(torch.where(hot, 0, got), torch.where(hot, 0, base))
+    live = (t >= 0) & o["logp"].isfinite()
+    # log p by either way: off by 4 u of |z| + |lse| (below 30 here); the derivative of both terms by it is below |dl| + 3 |dh|
+    diff = (got.float() - base.float()).abs()[live, t[live]]
+    assert (diff <= 4 * UNIT * 30 * (dl.abs() + 16 * dh.abs())[live] + (2.0 ** -7 * base.float().abs()[live, t[live]] if bf16 else 1e-30)).all()
+    assert not got[4].any() and got[5, t[5]] == 0 and got[6].isnan().all() and not got[7:9].any()
+    want = got.clone()
+    torch.cuda.synchronize()
+    buf = l.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ops.token_logprob_backward(buf, t, o["lse"], out=buf, logp=o["logp"], **kw)
+    g.replay()
+    torch.cuda.synchronize()
+    assert same(buf, want)
+    for bad in (dict(logp=o["logp"][:5]), dict(logp=o["logp"][:, None])):
+        with pytest.raises(ValueError):
+            ops.token_logprob_backward(l, t, o["lse"], dlogp=dl, **bad)
+    with pytest.raises(TypeError):
+        ops.token_logprob_backward(l, t, o["lse"], dlogp=dl, logp=o["logp"].double())
+    with pytest.raises(ValueError):
+        ops.token_logprob_backward(l, None, o["lse"], entropy=o["entropy"], dentropy=dh, logp=o["logp"])

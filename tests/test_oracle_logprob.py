@@ -56,3 +56,16 @@ def test_gradient_against_differences(temperature):
             a[r, i] += 1e-5
             b[r, i] -= 1e-5
             assert abs((f(a) - f(b)) / 2e-5 - d[r, i]) < 1e-8
+
+
+def test_gradient_of_a_nearly_certain_target():
+    """From the target's own log p: the row's sum is 0 to its last bit; from an lse rounded to fp32 1 - p is lost."""
+    l = np.zeros((1, 9))
+    l[0, 4] = 25.0
+    t, one = np.array([4]), np.ones(1)
+    o = O.token_logprob(l, t)
+    rounded = np.float64(np.float32(o["lse"]))
+    exact, _ = O.token_logprob_backward(l, t, o["lse"], one)
+    d, _ = O.token_logprob_backward(l, t, rounded, one, logp=o["logp"])
+    assert np.isclose(d[0, 4], exact[0, 4], rtol=1e-12) and np.isclose(d[0, 4], 8 * np.exp(-25), rtol=1e-9)
+    assert O.token_logprob_backward(l, t, rounded, one)[0][0, 4] == 0
