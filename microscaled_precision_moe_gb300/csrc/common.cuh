@@ -202,6 +202,9 @@ MPM_DEV bool mbar_wait(uint32_t bar, uint32_t parity, int* st) {
   }
 }
 
+// Of a wait that every lane of a warp makes: it came for all of them, or the warp gives up as a whole.
+MPM_DEV bool warp_agrees(bool v) { return __all_sync(0xffffffffu, v); }
+
 // ---------------------------------------------------------------- TMA / bulk copies
 MPM_DEV void tma_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
   asm volatile(

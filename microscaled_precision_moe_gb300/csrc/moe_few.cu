@@ -37,6 +37,7 @@
 
 #include "moe_few.cuh"
 #include "nvfp4.cuh"
+#include "team_wait.cuh"
 
 namespace mpm {
 namespace few {
@@ -105,6 +106,26 @@ MPM_DEV bool wait_count(const int* p, int v, int* status) {
   }
   return true;
 }
+// Teams that wait as one: a warp, and the epilogue's four.
+struct WarpTeam {
+  int lane;
+  MPM_DEV bool first() const { return lane == 0; }
+  MPM_DEV bool share(bool v) const {
+    v = __shfl_sync(0xffffffffu, v, 0);
+    __syncwarp();                               // a shuffle alone orders no memory
+    return v;
+  }
+};
+struct EpilogueTeam {
+  int et;
+  MPM_DEV bool first() const { return et == 0; }
+  MPM_DEV bool share(bool v) const {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"((uint32_t)v) : "memory");
+    return r != 0;
+  }
+};
 // Weights are read once: they leave L2 first, and what the next call finds there
 // (its code among it) stays.
 MPM_DEV uint64_t once_policy() {
@@ -664,10 +685,8 @@ __global__ void __launch_bounds__(NT, 1) moe_few_kernel(const __grid_constant__ 
     const uint32_t tq = (uint32_t)((warp & 3) * 32) << 16;
     while (ok && walk.next(p)) {
       for (int kb = p.k0; kb < p.k1; ++kb) {
-        if (!mbar_wait(bar_w + 8 * ring.s, ring.ph, a.status) || !mbar_wait(bar_x + 8 * ring.s, ring.ph, a.status)) {
-          ok = false;
-          break;
-        }
+        ok = warp_agrees(mbar_wait(bar_w + 8 * ring.s, ring.ph, a.status) && mbar_wait(bar_x + 8 * ring.s, ring.ph, a.status));
+        if (!ok) break;
         tc_fence_after();
         const uint8_t* st = gbase + ring.s * STB;
         const uint32_t col = sf_base + tq + ring.s * sf_cols;
@@ -833,15 +852,17 @@ __global__ void __launch_bounds__(NT, 1) moe_few_kernel(const __grid_constant__ 
         // every block has one at most, else by a warp each
         const int rows = g.n ? g.start[g.n - 1] + g.rows[g.n - 1] : 0;
         const int team = rows <= (int)gridDim.x ? 128 : 32, B = (int)gridDim.x;
-        for (int r = blockIdx.x + et / team * B; r < rows; r += B * (128 / team)) {
-          const int grp = g.group[r], slot = g.slot[r];
-          if (!wait_count(grp_done + grp, a.I / 128, a.status)) { ok = false; break; }
+        auto there = [&](int r) { return wait_count(grp_done + g.group[r], a.I / 128, a.status); };
+        auto quantise = [&](int r) {
+          const int slot = g.slot[r];
           quantise_d_row(a, slot, g.row[slot], et & (team - 1), team);
           fence_proxy_global();
           if (team == 128) named_sync(1, 128);
           else __syncwarp();
-          if ((et & (team - 1)) == 0) add_release(grp_ready + grp, 1);
-        }
+          if ((et & (team - 1)) == 0) add_release(grp_ready + g.group[r], 1);
+        };
+        ok = team == 128 ? rows_as_one(EpilogueTeam{et}, (int)blockIdx.x, B, rows, there, quantise)
+                         : rows_as_one(WarpTeam{lane}, (int)blockIdx.x + et / 32 * B, B * 4, rows, there, quantise);
         if (!ok) s_fail = 1;
         named_sync(1, 128);
         ok = !s_fail;
@@ -855,9 +876,7 @@ __global__ void __launch_bounds__(NT, 1) moe_few_kernel(const __grid_constant__ 
   const int tiles = a.H / 256;
   for (int i = blockIdx.x + gridDim.x * warp; i < a.T * tiles && !s_fail; i += gridDim.x * (NT / 32)) {
     const int t = i / tiles, tile = i - t * tiles;
-    int there = 1;
-    if (lane == 0) there = wait_count(tile_done + tile, g.n, a.status);
-    if (!__shfl_sync(0xffffffffu, there, 0)) break;
+    if (!wait_as_one(WarpTeam{lane}, [&]() { return wait_count(tile_done + tile, g.n, a.status); })) break;
     float o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const float* y = a.y + (size_t)t * a.k * a.H + tile * 256 + lane * 8;
     for (int s0 = 0; s0 < a.k; s0 += 8) {
