@@ -25,6 +25,7 @@
 //                  stores
 // Every mbarrier wait is bounded; a timeout sets the device status word and
 // the CTA skips the rest of its work.
+#include <atomic>
 #include "gemm.cuh"
 
 namespace mpm {
@@ -401,7 +402,7 @@ template <int KIND, int EPI>
 static cudaError_t launch_one(const CUtensorMap& ta, const CUtensorMap& tb, const GemmArgs& a,
                               dim3 grid, cudaStream_t s) {
   constexpr int smem = smem_bytes<KIND>();
-  static bool attr_set[64] = {false};
+  static std::atomic<bool> attr_set[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && !attr_set[dev]) {

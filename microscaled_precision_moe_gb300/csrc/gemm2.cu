@@ -29,6 +29,7 @@
 // Sources: "miniTE technical report", sections 5.2 and 5.4 (grouped GEMM over
 // a contiguous buffer with device offsets; FC1 epilogue); "Towards
 // Blackwell-native 8-bit and 4-bit RL", section "Recipe 1 / Training".
+#include <atomic>
 #include "gemm.cuh"
 
 namespace mpm {
@@ -930,7 +931,7 @@ static cudaError_t launch_pair_one(const pairk::PairMaps& maps, const GemmArgs& 
   constexpr int smem = pairk::smem_bytes<KIND, EPI>();
   static_assert(smem <= 227 * 1024, "dynamic shared memory above the per-CTA limit");
   auto kern = pairk::grouped_gemm_pair_kernel<KIND, EPI, MAJ>;
-  static int max_clusters[64] = {0};
+  static std::atomic<int> max_clusters[64];
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
@@ -956,7 +957,7 @@ static cudaError_t launch_pair_one(const pairk::PairMaps& maps, const GemmArgs& 
     if (err != cudaSuccess || ncl < 1) ncl = sms / 2;
     max_clusters[dev] = ncl;
   }
-  long long ncl = dev < 64 ? max_clusters[dev] : 1;
+  long long ncl = dev < 64 ? max_clusters[dev].load() : 1;
   if (ncl > n_tasks) ncl = n_tasks;
   if (ncl < 1) ncl = 1;
   cfg.gridDim = dim3((unsigned)(2 * ncl), 1, 1);

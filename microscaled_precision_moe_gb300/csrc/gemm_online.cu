@@ -23,6 +23,7 @@
 // staging box with TMA stores.  TMEM: three accumulators (384 columns) and
 // four stages' scale tiles (32 columns each).  Expert segments are multiples of
 // 256 rows (mpm_moe_build_segments with pad = 256), as for the CTA-pair GEMM.
+#include <atomic>
 #include "gemm.cuh"
 
 namespace mpm {
@@ -373,7 +374,7 @@ cudaError_t launch_fc2_online(const CUtensorMap& ta, const CUtensorMap& tb, cons
   constexpr int smem = onlinek::smem_bytes();
   static_assert(smem <= 227 * 1024, "dynamic shared memory above the per-CTA limit");
   auto kern = onlinek::fc2_online_kernel;
-  static int max_clusters[64] = {0};
+  static std::atomic<int> max_clusters[64];
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
@@ -405,7 +406,7 @@ cudaError_t launch_fc2_online(const CUtensorMap& ta, const CUtensorMap& tb, cons
     if (err != cudaSuccess || ncl < 1) ncl = sms / 2;
     max_clusters[dev] = ncl;
   }
-  long long ncl = dev < 64 ? max_clusters[dev] : 1;
+  long long ncl = dev < 64 ? max_clusters[dev].load() : 1;
   if (ncl > n_tasks) ncl = n_tasks;
   if (ncl < 1) ncl = 1;
   cfg.gridDim = dim3((unsigned)(2 * ncl), 1, 1);

@@ -23,6 +23,7 @@
 // activation scaling" (NVFP4 rollout of the MoE experts) and the small-M
 // rollout path it names; "miniTE technical report", sections 5.2 and 5.4
 // (grouped GEMM over a contiguous buffer with device offsets; FC1 epilogue).
+#include <atomic>
 #include "gemm.cuh"
 
 namespace mpm {
@@ -647,7 +648,7 @@ static cudaError_t launch_small_one(const smallk::SmallMaps& maps, const GemmArg
   static_assert(smem <= 227 * 1024, "dynamic shared memory above the per-CTA limit");
   static_assert(smem > 114 * 1024, "one CTA per SM (each allocates all TMEM columns)");
   auto kern = smallk::grouped_gemm_small_kernel<KIND, EPI>;
-  static int sms[64] = {0};
+  static std::atomic<int> sms[64];
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
@@ -658,7 +659,7 @@ static cudaError_t launch_small_one(const smallk::SmallMaps& maps, const GemmArg
     cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
     sms[dev] = n > 0 ? n : 1;
   }
-  long long grid = dev < 64 ? sms[dev] : 1;
+  long long grid = dev < 64 ? sms[dev].load() : 1;
   if (grid > n_tasks) grid = n_tasks;
   if (grid < 1) grid = 1;
   kern<<<(unsigned)grid, smallk::NTHREADS_G, smem, s>>>(maps, a, n_wt, n_tasks);
@@ -672,7 +673,7 @@ static cudaError_t launch_splitk_one(const smallk::SmallMaps& maps, const GemmAr
   static_assert(smem <= 227 * 1024, "dynamic shared memory above the per-CTA limit");
   static_assert(smem > 114 * 1024, "one CTA per SM (TMEM allocation never waits)");
   auto kern = splitk::gemm_splitk_kernel<KIND, EPI>;
-  static bool attr_set[64] = {false};
+  static std::atomic<bool> attr_set[64];
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;

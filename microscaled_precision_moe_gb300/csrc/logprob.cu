@@ -25,6 +25,7 @@
 // 20: instructions and the waits of the first batch, with 16 reading warps an SM).
 //
 // Gradient: one read and one write (8192 x 32768 bf16 166 us, 0.97 of a plain copy's rate).
+#include <atomic>
 #include "logprob.cuh"
 #include "packed.cuh"
 
@@ -1213,7 +1214,7 @@ __global__ void __launch_bounds__(NT, PARTS ? 3 : 4) token_logprob_backward_kern
 }
 
 int sm_count() {
-  static int sms[64] = {0};
+  static std::atomic<int> sms[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
   if (!sms[dev]) {
@@ -1256,11 +1257,11 @@ cudaError_t launch_token_logprob(const LogprobFwd& p, cudaStream_t st) {
   auto kern = p.f32 ? (p.top ? token_logprob_kernel<true, true> : token_logprob_kernel<true, false>)
                     : (p.top ? token_logprob_kernel<false, true> : token_logprob_kernel<false, false>);
   const int smem = p.top ? STAGES * BATCH * 16 + 2 * CAP * (int)sizeof(uint64_t) : STAGES * BATCH * 16;
-  static bool ready[64][4] = {};                // by device and kernel
+  static std::atomic<bool> ready[64][4];        // by device and kernel
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
-  bool* done = dev >= 0 && dev < 64 ? &ready[dev][(p.f32 ? 2 : 0) + (p.top ? 1 : 0)] : nullptr;
+  std::atomic<bool>* done = dev >= 0 && dev < 64 ? &ready[dev][(p.f32 ? 2 : 0) + (p.top ? 1 : 0)] : nullptr;
   if (!done || !*done) {
     err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;

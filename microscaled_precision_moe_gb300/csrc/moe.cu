@@ -10,6 +10,7 @@
 // The counting sort is stable: rows of one expert appear in ascending flat
 // index t*k + j.  Every step is integer work, so results are bit-identical
 // run to run.
+#include <atomic>
 #include "moe.cuh"
 #include "launch.cuh"
 
@@ -584,7 +585,7 @@ size_t segments_ws_bytes(long long T, int k, long long E) {
 
 // the cooperative form; cudaErrorNotSupported when the device cannot run it
 static cudaError_t launch_segments_fused(const SegFused& a, cudaStream_t s) {
-  static int ctas[64] = {0};
+  static std::atomic<int> ctas[64];
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
@@ -605,7 +606,7 @@ static cudaError_t launch_segments_fused(const SegFused& a, cudaStream_t s) {
   // enough CTAs for the widest phase, no more than can be resident
   long long want = a.nchunks > a.E ? a.nchunks : a.E;
   if (want < 1) want = 1;
-  const unsigned grid = (unsigned)(want < ctas[dev] ? want : ctas[dev]);
+  const unsigned grid = (unsigned)(want < ctas[dev] ? want : ctas[dev].load());
   SegFused arg = a;
   void* args[] = {&arg};
   return cudaLaunchCooperativeKernel((const void*)seg_fused_kernel, dim3(grid), dim3(256), args,

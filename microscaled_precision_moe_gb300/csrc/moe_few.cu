@@ -32,6 +32,7 @@
 // tokens 187 (1.0), 64 tokens and about 125 experts 500 (0.93); 30B-shaped MXFP8, 1 token 19.5 us (0.29), 33 tokens 77 (0.92).
 // With one token the chain counts: the launch and the meeting of the blocks 4.7 us, the first rows 3, D between the products
 // 5 to 8 (partials, D and its quantised rows each pass from block to block through L2), FC2's last steps 3.
+#include <atomic>
 #include <cooperative_groups.h>
 #include <utility>
 
@@ -949,7 +950,7 @@ Layout layout(int kind, long long T, int k, long long E, long long H, long long 
 template <int KIND>
 static cudaError_t launch_few(const FewMaps& maps, FewArgs a, cudaStream_t st) {
   auto kern = few::moe_few_kernel<KIND>;
-  static int sms[64] = {0}, fixed[64] = {0};             // by device: SMs, static shared memory
+  static std::atomic<int> sms[64], fixed[64];            // by device: SMs, set last; static shared memory
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;

@@ -12,6 +12,7 @@
 // "Format background / MXFP8" and "Recipe 1 / Training").  A CTA reads a
 // 128 x 64 bf16 tile once, writes the row-wise 1x32 copy from registers and the
 // column-wise 32x1 copy, transposed, from a shared-memory copy of the tile.
+#include <atomic>
 #include <cstring>
 #include "quant.cuh"
 #include "nvfp4.cuh"
@@ -993,7 +994,7 @@ static cudaError_t launch_mxfp8_impl(const CUtensorMap& tx, const CUtensorMap& t
   const long long n_tiles = (p.M + MQ_TM - 1) / MQ_TM * n_kt;
   if (n_tiles > (1ll << 30)) return cudaErrorInvalidValue;   // tile cursors are 32-bit
   constexpr int smem = 1024 + MQ_STAGES * MQ_TILE_BYTES + 2 * MQ_OUT_BYTES + 64;
-  static int ctas[64] = {0};
+  static std::atomic<int> ctas[64];
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
@@ -1006,7 +1007,7 @@ static cudaError_t launch_mxfp8_impl(const CUtensorMap& tx, const CUtensorMap& t
     cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, mxfp8_quant_tma_kernel<GATHER>, 256, smem);
     ctas[dev] = (sms > 0 ? sms : 1) * (per > 0 ? per : 1);
   }
-  long long grid = dev < 64 ? ctas[dev] : 1;
+  long long grid = dev < 64 ? ctas[dev].load() : 1;
   if (grid > n_tiles) grid = n_tiles;
   if (grid < 1) grid = 1;
   cudaLaunchConfig_t cfg = {};
