@@ -32,26 +32,27 @@ def forward(x, ids, prob, w1, w2, kind):
     times g's error; where such an error takes an element of D across a rounding
     border, its code moves with it: D is rounded and quantised at both ends of its
     interval, and the differences go through |W2|."""
-    T, k = ids.shape
     E, H, I = w2.shape
     step = 64 if kind == "nvfp4" else 32
     xq = quantise(np.asarray(x, np.float64), kind)
-    out, tol = np.zeros((T, H)), np.zeros((T, H))
-    for t in range(T):
-        for j in range(k):
-            e, p = int(ids[t, j]), float(prob[t, j])
-            if p == 0 or not 0 <= e < E:
-                continue
-            c = w1[e] @ xq[t]
-            err = (H / step + 2) * 2 * UNIT * (np.abs(w1[e]) @ np.abs(xq[t])) + 2 * UNIT * np.abs(c)
-            g, u, dg, du = c[:I], c[I:], err[:I], err[I:]
-            with np.errstate(over="ignore"):
-                sig = 1.0 / (1.0 + np.exp(-g))
-            d = g * sig * u * p
-            dd = abs(p) * (np.abs(u) * sig * (1 + np.abs(g) * (1 - sig)) * dg + np.abs(g * sig) * du) \
-                + np.abs(d) * UNIT * (16 + 4 * np.abs(g))
-            mid, lo, hi = (quantise(F.bf16_round(v)[None], kind)[0] for v in (d, d - dd, d + dd))
-            moved = np.abs(lo - mid) + np.abs(hi - mid)
-            out[t] += w2[e] @ mid
-            tol[t] += np.abs(w2[e]) @ moved + ((I / step + 2 + k) * 2 * UNIT) * (np.abs(w2[e]) @ np.abs(mid))
+    ids, prob = np.asarray(ids), np.asarray(prob, np.float64)
+    k = ids.shape[1]
+    out, tol = np.zeros((len(ids), H)), np.zeros((len(ids), H))
+    live = (prob != 0) & (ids >= 0) & (ids < E)
+    for e in np.unique(ids[live]):
+        t, j = np.nonzero(live & (ids == e))
+        p = prob[t, j][:, None]
+        c = xq[t] @ w1[e].T
+        err = (H / step + 2) * 2 * UNIT * (np.abs(xq[t]) @ np.abs(w1[e]).T) + 2 * UNIT * np.abs(c)
+        g, u, dg, du = c[:, :I], c[:, I:], err[:, :I], err[:, I:]
+        with np.errstate(over="ignore"):
+            sig = 1.0 / (1.0 + np.exp(-g))
+        d = g * sig * u * p
+        dd = np.abs(p) * (np.abs(u) * sig * (1 + np.abs(g) * (1 - sig)) * dg + np.abs(g * sig) * du) \
+            + np.abs(d) * UNIT * (16 + 4 * np.abs(g))
+        mid, lo, hi = (quantise(F.bf16_round(v), kind) for v in (d, d - dd, d + dd))
+        moved = np.abs(lo - mid) + np.abs(hi - mid)
+        w = np.abs(w2[e])
+        np.add.at(out, t, mid @ w2[e].T)
+        np.add.at(tol, t, moved @ w.T + ((I / step + 2 + k) * 2 * UNIT) * (np.abs(mid) @ w.T))
     return out, tol
