@@ -7,8 +7,9 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import quant as Q
 from tests.gpu_util import need_gpu
-from tests.test_gpu_few import _compare, _kind, _rows, _weights
+from tests.test_gpu_few import _compare, _kind, _rows, _route, _weights
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +81,27 @@ def test_a_cut_task_in_front_of_whole_ones(kind, T, k, E, H, I, wanted):
     _compare(out, x, ids, prob, exact, kind)
     for _ in range(3):
         assert torch.equal(ops.moe_few_tokens(_kind(kind), x, ids, prob, w1, w2, E, I), out)
+
+
+def _coded_nvfp4(E, R, K, seed):
+    """NVFP4 weights written down as codes (rows longer than the library's own quantiser takes): for the call and decoded."""
+    rng = np.random.default_rng(seed)
+    q = rng.integers(0, 256, (E * R, K // 2), dtype=np.uint8)
+    s = rng.integers(0x28, 0x50, (E * R, K // 16), dtype=np.uint8)       # E4M3: 0.25 to 7.5
+    ts = (rng.uniform(0.5, 2.0, E) / K ** 0.5 / 8).astype(np.float32)
+    d = Q.nvfp4_dequantize(q, s, np.repeat(ts.astype(np.float64), R)).reshape(E, R, K)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    return (dev(q), dev(Q.swizzle_scales(s)), dev(ts)), d
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 16384, 256), (3, 8448, 512), (17, 256, 16384), (2, 1024, 12032), (64, 16384, 256)])
+def test_nvfp4_weights_wider_than_the_quantiser_takes(T, H, I):
+    """Up to the 16384 that the call accepts, on weights that another program has quantised."""
+    from microscaled_precision_moe_gb300 import ops
+    E, k = 3, 2
+    (w1, e1), (w2, e2) = _coded_nvfp4(E, 2 * I, H, H + I), _coded_nvfp4(E, H, I, H + I + 1)
+    x = _rows(T, H, seed=T)
+    ids, prob = _route(T, E, k, T)
+    out = ops.moe_few_tokens(_kind("nvfp4"), x, ids, prob, w1, w2, E, I)
+    _compare(out, x, ids, prob, (e1, e2), "nvfp4")
+    assert torch.equal(ops.moe_few_tokens(_kind("nvfp4"), x, ids, prob, w1, w2, E, I), out)
