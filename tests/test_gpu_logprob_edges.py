@@ -312,3 +312,17 @@ def test_gradient_with_logp_is_the_same_elsewhere(bf16):
         ops.token_logprob_backward(l, t, o["lse"], dlogp=dl, logp=o["logp"].double())
     with pytest.raises(ValueError):
         ops.token_logprob_backward(l, None, o["lse"], entropy=o["entropy"], dentropy=dh, logp=o["logp"])
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T,V", [(9, 50001), (9, 900), (400, 4000), (400, 7000), (400, 15000), (3, 131072)])
+@pytest.mark.parametrize("temperature", [1.0, 0.7, 3.0])
+def test_entropy_within_its_own_rounding(bf16, T, V, temperature):
+    """Near certainty, near uniformity and between: no more than what the terms' roundings give."""
+    rng = np.random.default_rng(V)
+    r = rng.normal(size=(9, V)) * np.array([0.01, 0.3, 1, 2, 4, 8, 1, 2, 0])[:, None]
+    r[6:9, V // 3] += [30, 12, 25]
+    l = torch.from_numpy(r.astype(np.float32)).to(torch.bfloat16 if bf16 else torch.float32)
+    t = l.float().argmax(1)
+    n = (T + 8) // 9
+    _forward(l.repeat(n, 1)[:T].contiguous().cuda(), t.repeat(n)[:T].cuda(), temperature, 0, min(T, 9))
