@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(NT + 64, 2) token_logprob_kernel(const Logprob
   long long row, t;
   // the next row of the queue; false at its end
   auto next_row = [&]() {
-    ok = ok && mbar_wait(smem_u32(&sh.queue[qs].full), qph, p.status);
+    ok = warp_agrees(ok && mbar_wait(smem_u32(&sh.queue[qs].full), qph, p.status));
     row = sh.queue[qs].row;
     t = sh.queue[qs].t;
     __syncwarp();
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(NT + 64, 2) token_logprob_kernel(const Logprob
       const Row<F32> r(p.logits, row, p.ld, p.V);
       const int q0 = (int)((long long)r.nv * rank >> lcs), q1 = (int)((long long)r.nv * (rank + 1) >> lcs);
       const float zt = p.targets ? logit<F32>(p.logits, row * p.ld + t) : 0.0f;
-      ok = ok && mbar_wait(smem_u32(&h.full), (use >> 1) & 1u, p.status);
+      ok = warp_agrees(ok && mbar_wait(smem_u32(&h.full), (use >> 1) & 1u, p.status));
       Stats st = block_stats<F32>(h, r, q0, q1, c, lane);
       uint64_t key = 0;
       if (TOP) {

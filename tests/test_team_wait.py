@@ -96,3 +96,13 @@ def test_the_kernel_waits_for_other_blocks_as_teams_only():
     teams = [l for l in lines if "auto there = " in l or "wait_as_one(" in l]
     lane = [l for l in lines if l not in teams]
     assert len(teams) == 2 and len(lane) == 2, lines       # the two of the rows' producer, which is one lane
+
+
+def test_the_scoring_warps_give_up_as_a_whole():
+    """A row's work has operations of a whole warp: whether it is begun, and whether its list may be worked on, is agreed."""
+    with open(os.path.join(CSRC, "logprob.cu")) as f:
+        source = f.read()
+    next_row = source.split("auto next_row = [&]() {", 1)[1].split("};", 1)[0]
+    assert "ok = warp_agrees(ok && mbar_wait(" in next_row and "return ok && row >= 0;" in next_row
+    closing = source.split("// ---------------------------------------------------------------- closing", 1)[1]
+    assert closing.index("ok = warp_agrees(ok && mbar_wait(smem_u32(&h.full)") < closing.index("if (listed > CAP && ok)")
