@@ -14,17 +14,17 @@
 // stand at the lowest value, and their quotient by a temperature may overflow): above 2^100 the next logit is more than
 // 2^76 away, only tokens equal to L weigh anything and w is 0.
 //
-// Forward: one pass over the logits, bound by reading them (8192 x 32768 bf16 81 us, 0.99 of a plain copy's rate; 64 x
-// 131072 with 8 alternatives 9.6 us and 1 x 131072 with 20 7.6, latency).  Batches of 32 KB come by bulk copies through a
+// Forward: one pass over the logits, bound by reading them (8192 x 32768 bf16 82.6 us, 0.97 of a plain copy's rate; 64 x
+// 131072 with 8 alternatives 9.7 us and 1 x 131072 with 20 7.8, latency).  Batches of 32 KB come by bulk copies through a
 // ring of three in shared memory, which runs on from row to row; a warp keeps one running maximum, raised once a batch,
 // so an element costs one difference, one product, one exponential and two accumulations.  A row goes to a block, or,
 // when there are few rows, to a cluster of up to 8 blocks that join through distributed shared memory; a short row to the
 // registers of one to four warps.  The alternatives are found in the same pass: after a row's first batch the k-th largest of 32 or 64 group maxima is
 // a bound that at least k elements reach, and only what reaches it is put on a list, which the warp that closes the row
-// ranks while the next one is read (2047 x 50001 fp32: 45.6 us without alternatives, 49.5 with one, 52 with 4, 62 with
-// 20: instructions and the waits of the first batch, with 16 reading warps an SM).
+// ranks while the next one is read (2047 x 50001 fp32, all rows: 60.6 us without alternatives, 64.5 with one, 68.8 with 4, 81
+// with 20; 8192 x 32768 bf16: 82.6, 109, 122, 145: instructions and the waits of the first batch, with 16 reading warps an SM).
 //
-// Gradient: one read and one write (8192 x 32768 bf16 166 us, 0.97 of a plain copy's rate).
+// Gradient: one read and one write (8192 x 32768 bf16 165 us, 0.98 of a plain copy's rate).
 #include <atomic>
 #include "logprob.cuh"
 #include "packed.cuh"
@@ -1086,7 +1086,8 @@ MPM_DEV uint4 at_lse(const uint4& v, float inv_t, float lse) {
 template <bool F32>
 __device__ __noinline__ uint4 at_lse_called(const uint4 v, float inv_t, float lse) { return at_lse<F32>(v, inv_t, lse); }
 
-template <bool F32, bool OUT32, bool PARTS>
+// (Whether log p is given is known as such too: tested at the target it cost the teams' registers 21 % at 8192 x 2000 fp32.)
+template <bool F32, bool OUT32, bool PARTS, bool LOGP>
 __global__ void __launch_bounds__(NT, PARTS ? 3 : 4) token_logprob_backward_kernel(const LogprobBwd p, const int chunks, const int lt) {
   constexpr int VE = Row<F32>::VE, OS = OUT32 ? 4 : 2;
   // What an item needs besides its logits
@@ -1172,7 +1173,7 @@ __global__ void __launch_bounds__(NT, PARTS ? 3 : 4) token_logprob_backward_kern
 #pragma unroll
           for (int j = 0; j < VE; ++j)
             if (x.t == e + j) {
-              const float z = element<F32>(v[u], j), own = p.logp ? p.logp[x.row] : __fsub_rn(__fmul_rn(z, p.inv_t), x.lse);
+              const float z = element<F32>(v[u], j), own = LOGP ? p.logp[x.row] : __fsub_rn(__fmul_rn(z, p.inv_t), x.lse);
               const float lp = max_nan(own, FAR);
               d[j] = z <= LOW && x.lse == x.lse ? 0.0f : -fmaf(G, expm1f(lp), expf(lp) * fmaf(-A, lp, K));
             }
@@ -1310,8 +1311,9 @@ static cudaError_t launch_backward(const LogprobBwd& p, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, lt < 8 ? token_logprob_backward_kernel<F32, OUT32, true> : token_logprob_backward_kernel<F32, OUT32, false>,
-                            p, chunks, lt);
+  auto kern = lt < 8 ? (p.logp ? token_logprob_backward_kernel<F32, OUT32, true, true> : token_logprob_backward_kernel<F32, OUT32, true, false>)
+                     : (p.logp ? token_logprob_backward_kernel<F32, OUT32, false, true> : token_logprob_backward_kernel<F32, OUT32, false, false>);
+  return cudaLaunchKernelEx(&cfg, kern, p, chunks, lt);
 }
 
 cudaError_t launch_token_logprob_backward(const LogprobBwd& p, cudaStream_t st) {
