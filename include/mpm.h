@@ -589,9 +589,10 @@ mpm_status mpm_moe_few_tokens(const mpm_moe_few_tokens_desc* desc, cudaStream_t 
  * Logits at or below bf16's lowest finite value (-inf, the types' lowest values) are out of reach:
  * probability 0, never an alternative, logp -inf as a target.  A row with
  * nothing in reach gives lse and logp -inf and entropy 0; alternatives that do
- * not exist are (-1, -inf).  A NaN, +inf or a largest quotient by the temperature
- * above 2^128 (1 - 2^-9) in magnitude makes lse, logp, entropy and all of top_logp of its row NaN; beside a NaN, top_ids are some tokens of
- * the row, or -1, not necessarily the largest.
+ * not exist are (-1, -inf).  A NaN or +inf makes lse, logp, entropy and all of
+ * top_logp of its row NaN; beside a NaN, top_ids are some tokens of the row, or -1,
+ * not necessarily the largest.  An lse above 2^128 (1 - 2^-9) in magnitude (a
+ * quotient by the temperature that fp32 does not hold) is NaN by itself.
  * Sums and statistics are fp32; the sum is kept without its largest term, so
  * that logp and the entropy of nearly certain tokens keep their relative
  * precision.

@@ -46,7 +46,7 @@ constexpr int MAX_CLUSTER = 8;
 constexpr int QUEUE = 4;              // rows handed on ahead
 constexpr float LOW = -0x1.FEp127f;  // bf16's lowest finite value: logits at or below it are out of reach
 constexpr float FAR = -0x1p100f;     // no probability is left there, unless all logits are as low (lse is -2^90 or less then)
-constexpr float MOST = 0x1.FFp127f;  // a row whose largest logit's quotient by the temperature is larger is NaN
+constexpr float MOST = 0x1.FFp127f;  // an lse past it is NaN
 constexpr float kLog2e = 1.4426950408889634f;
 
 MPM_DEV float ex2(float t) {
@@ -430,12 +430,13 @@ __device__ __noinline__ void select_by_rounds(uint64_t* best_of, const uint64_t*
 // A row's results, by one warp; key: lane i's the i-th alternative
 MPM_DEV void write_row(const LogprobFwd& p, long long row, const Stats& st, float zt, uint64_t key, int lane) {
   const bool some = st.m > LOW || st.rest != st.rest;
-  // NaN, +inf and quotients past MOST make every result of the row NaN
-  const float lr = !some || fabsf(st.m * p.inv_t) <= MOST ? log1pf(st.rest) : NAN;
+  // NaN and +inf make every result of the row NaN
+  const float lr = st.m < INFINITY ? log1pf(st.rest) : NAN;
   // (of halves: the difference of two logits may overflow where its quotient by the temperature does not)
   auto logp = [&](float z) { return fmaf(0.5f * z - 0.5f * st.m, 2.0f * p.inv_t, -lr); };
   if (lane == 0) {
-    p.lse[row] = some ? fmaf(st.m, p.inv_t, lr) : -INFINITY;
+    const float lse = fmaf(st.m, p.inv_t, lr);
+    p.lse[row] = some ? (fabsf(lse) <= MOST ? lse : NAN) : -INFINITY;       // (tested in lr instead: 1 to 2 % in short rows)
     if (p.logp) p.logp[row] = some ? (zt <= LOW ? (lr == lr ? -INFINITY : lr) : logp(zt)) : -INFINITY;
     if (p.entropy) {
       const float h = lr - (st.m > -FAR ? 0.0f : st.w * p.inv_t / (1.0f + st.rest));

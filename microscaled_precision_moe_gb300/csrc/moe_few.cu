@@ -28,8 +28,9 @@
 // that are resident (the launch is cooperative) and never wait for later work;
 // they are bounded like every wait here.
 //
-// Measured (weights alone over the time, of the 6.67 TB/s of a plain copy): 671B-shaped NVFP4, 1 token 43 us (0.69), 7
-// tokens 187 (1.0), 64 tokens and about 125 experts 500 (0.93); 30B-shaped MXFP8, 1 token 19.5 us (0.29), 33 tokens 77 (0.92).
+// Measured (weights alone over the time, of the 6.67 TB/s of a plain copy): 671B-shaped NVFP4, 1 token 43.7 us (0.68), 7
+// tokens 188 to 196 (0.96 to 1.0), 64 tokens and 124 to 152 experts 503 to 522 (1.0); 30B-shaped MXFP8, 1 token 20 us (0.29),
+// 33 tokens 77 to 80 (0.89 to 0.92).
 // With one token the chain counts: the launch and the meeting of the blocks 4.7 us, the first rows 3, D between the products
 // 5 to 8 (partials, D and its quantised rows each pass from block to block through L2), FC2's last steps 3.
 #include <atomic>
