@@ -1083,7 +1083,7 @@ MPM_DEV uint4 at_lse(const uint4& v, float inv_t, float lse) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The same as a call: where registers are short (teams; 8192 x 1000 bf16 13.5 us, 14.0 in line, whose code spills)
+// The same as a call: where registers are short (teams; in line its code spills: 14.0 us at 8192 x 1000 bf16)
 template <bool F32>
 __device__ __noinline__ uint4 at_lse_called(const uint4 v, float inv_t, float lse) { return at_lse<F32>(v, inv_t, lse); }
 
@@ -1296,8 +1296,8 @@ static cudaError_t launch_backward(const LogprobBwd& p, cudaStream_t st) {
   const long long nv = (p.V * es + (p.ld * es % 16 == 0 || p.T == 1 ? off : 16 - es) + 15) / 16;
   const long long slots = (long long)sm_count() * 4;
   // Rows of up to 2048 elements leave most of a block idle; where there are more of them than blocks at once, the smallest
-  // team that holds a row takes it (8192 x 100 bf16: 8.6 us against 28.8 by blocks, x 1000 12.7 / 26.0, x 2000 24.0 / 29.8;
-  // fp32 x 2000 26.3 / 31.8; bf16 x 4000 43.5 / 36.1; few rows, 96 x 1000: 3.1 / 2.5).
+  // team that holds a row takes it (8192 x 100 bf16: 8.8 us against 28.8 by blocks, x 1000 13.1 / 26.0, x 2000 25.0 / 29.8;
+  // fp32 x 2000 26.0 / 31.8; bf16 x 4000 43.5 / 36.1; few rows, 96 x 1000: 3.1 / 2.5).
   int lt = 8;
   if (nv * 16 <= 2048 * es)
     while (lt > 5 && nv <= (long long)U << (lt - 1) && p.T << lt > slots * NT) --lt;
