@@ -1175,8 +1175,8 @@ __global__ void __launch_bounds__(NT, PARTS ? 3 : 4) token_logprob_backward_kern
           for (int j = 0; j < VE; ++j)
             if (x.t == e + j) {
               const float z = element<F32>(v[u], j), own = LOGP ? p.logp[x.row] : __fsub_rn(__fmul_rn(z, p.inv_t), x.lse);
-              const float lp = max_nan(own, FAR);
-              d[j] = z <= LOW && x.lse == x.lse ? 0.0f : -fmaf(G, expm1f(lp), expf(lp) * fmaf(-A, lp, K));
+              const float lp = max_nan(own, FAR), pt = expf(lp);         // p log p first: 0 where p is
+              d[j] = z <= LOW && x.lse == x.lse ? 0.0f : -fmaf(G, expm1f(lp), fmaf(-A, pt * lp, pt * K));
             }
         }
       }

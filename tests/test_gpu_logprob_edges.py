@@ -328,3 +328,21 @@ def test_entropy_within_its_own_rounding(bf16, T, V, temperature):
     t = l.float().argmax(1)
     n = (T + 8) // 9
     _forward(l.repeat(n, 1)[:T].contiguous().cuda(), t.repeat(n)[:T].cuda(), temperature, 0, min(T, 9))
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T,V", [(3, 300), (2000, 300), (3, 40000)])
+def test_gradient_of_a_target_without_probability(bf16, T, V):
+    """Far below the others its log p weighs nothing, however large dentropy is: its gradient is dlogp / temperature."""
+    ops = _ops()
+    l = torch.randn(T, V, device="cuda")
+    l[:, 5] = -1e9
+    l[1, 5] = -1e33
+    l = l.to(torch.bfloat16 if bf16 else torch.float32)
+    t = torch.full((T,), 5, device="cuda")
+    o = ops.token_logprob(l, t, temperature=1e-3, entropy=True)
+    dl, dh = torch.full((T,), 0.5, device="cuda"), torch.full((T,), 1e30, device="cuda")
+    out = torch.zeros(T, V, device="cuda")
+    for logp in (None, o["logp"]):
+        d = ops.token_logprob_backward(l, t, o["lse"], dlogp=dl, entropy=o["entropy"], dentropy=dh, temperature=1e-3, out=out, logp=logp)
+        assert d.isfinite().all() and ((d[:, 5] - 500).abs() <= 500 * 4 * UNIT).all()
